@@ -22,7 +22,7 @@ import torch
 own = False
 
 E4M3_MAX = 448.0
-TINY = 2.0 ** -100      # smallest magnitude a scale is taken from, so that 1 / scale is finite
+LOWEST = -120           # least exponent of a scale
 
 
 # ---------------------------------------------------------------- cases
@@ -93,7 +93,7 @@ def work(case):
     new, old = lengths(case)
     hkv, hq, d = case["hkv"], case["hq"], case["d"]
     n, kv = sum(new), sum(new) + sum(old)
-    vec = 2 * d if case["kv"] == "bf16" else d + 4              # one cached vector and its scale
+    vec = 2 * d if case["kv"] == "bf16" else d + 1              # one cached vector and its scale
     pages = sum(-(-(a + b) // case["page"]) for a, b in zip(new, old))
     if case["op"] in ("append", "read"):
         return {"bytes": 2 * n * hkv * (2 * d + vec) + 4 * n // case["page"], "flops": 4 * n * hkv * d}
@@ -107,9 +107,12 @@ def work(case):
 
 # ---------------------------------------------------------------- inputs
 def _quantise(x):
-    """[..., d] float32 -> e4m3 codes and one scale per vector (the definition append implements)."""
-    scale = x.abs().amax(-1).clamp_min(TINY) / E4M3_MAX
-    return (x * (1.0 / scale).unsqueeze(-1)).to(torch.float8_e4m3fn), scale
+    """[..., d] float32 -> e4m3 codes and one power of two per vector, the least that keeps the codes
+    within +-448, held as its exponent + 127 (the definition append implements)."""
+    amax = x.abs().amax(-1)
+    m, e = torch.frexp(amax)                                    # 448 * 2^(e - 9) = 0.875 * 2^e
+    e = torch.where(amax > 0, e - 9 + (m > 0.875), LOWEST).clamp_min(LOWEST)
+    return torch.ldexp(x, -e.unsqueeze(-1)).to(torch.float8_e4m3fn), (e + 127).to(torch.uint8)
 
 
 def _normal(g, shape, spread=None):
@@ -194,7 +197,7 @@ def _plain_append(st):
 
 
 def _values(x, scale):
-    return x.float() if scale is None else x.float() * scale.unsqueeze(-1)
+    return x.float() if scale is None else torch.ldexp(x.float(), scale.unsqueeze(-1).int() - 127)
 
 
 def _take(pool, name, page, slot):
@@ -321,13 +324,13 @@ def exact(case, seed):
         x = st["pool"][name]
         x = x.view(torch.uint8)[table[b, pos // page], :, pos % page].view(x.dtype).double() if x.element_size() == 1 else x[table[b, pos // page], :, pos % page].double()
         scale = st["pool"][name + "_scale"]
-        return x if scale is None else x * scale[table[b, pos // page], :, pos % page].double().unsqueeze(-1)
+        return x if scale is None else x * torch.exp2(scale[table[b, pos // page], :, pos % page].double() - 127).unsqueeze(-1)
 
     if op == "append":
         out = {}
         for name in ("k", "v"):
             values = st["pool"][name].double()
-            scales = None if st["pool"][name + "_scale"] is None else st["pool"][name + "_scale"].double()
+            scales = st["pool"][name + "_scale"]
             for b in range(case["seqs"]):
                 x = st[name][cu[b]:cu[b + 1]].double()
                 pos = torch.arange(kv_len[b] - x.shape[0], kv_len[b], device="cuda")
@@ -335,8 +338,9 @@ def exact(case, seed):
                 if scales is None:
                     values[at] = x
                 else:
-                    s = x.abs().amax(-1).clamp_min(TINY) / E4M3_MAX
-                    values[at], scales[at] = _round_e4m3(x / s.unsqueeze(-1)), s
+                    e = torch.ceil(torch.log2(x.abs().amax(-1) / E4M3_MAX)).clamp_min(LOWEST)
+                    values[at] = _round_e4m3(x / torch.exp2(e).unsqueeze(-1))
+                    scales[at] = (e + 127).to(torch.uint8)
             out[name], out[name + "_scale"] = values, scales
         return out
     if op == "read":
