@@ -8,6 +8,9 @@ memory and streams.
     sv = SpecVerifier(max_batch=1024, k=7, vocab=151552, dtype=torch.bfloat16)
     out = sv.verify(target, draft, tokens, temperature, uniforms, want_tv=True)
     out["tokens"], out["tau"], out["tv"]
+
+The paged key-value cache and the attention that precede it in a serving step
+are in ``attention.py`` (``SpecAttention``, ``KVPool``; ``include/spec_attn.h``).
 """
 from __future__ import annotations
 
@@ -286,5 +289,13 @@ class SpecVerifier:
         return rc, n.value
 
 
-__all__ = ["SpecVerifier", "SpecVerifyError", "build", "check_batch", "check_outputs", "output_shapes", "SV_FP32", "SV_BF16", "SV_FLAG_HOST_STAGING",
+def __getattr__(name):
+    # attention.py needs torch at import time; the verifier's names do not
+    if name in ("KVPool", "SpecAttention", "SV_E4M3"):
+        from . import attention
+        return getattr(attention, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+__all__ = ["SpecVerifier", "SpecVerifyError", "build", "check_batch", "check_outputs", "output_shapes", "KVPool", "SpecAttention", "SV_E4M3", "SV_FP32", "SV_BF16", "SV_FLAG_HOST_STAGING",
            "SV_FLAG_NO_TMA", "SV_FLAG_KERNEL_TIMING", "SV_OK", "SV_ERR_DATA", "SV_ERR_ARG", "SV_ERR_TIMEOUT"]

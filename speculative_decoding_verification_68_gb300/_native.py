@@ -1,6 +1,7 @@
 """Build and load the native library (libspec_verify.so, CUDA for sm_103a)."""
 from __future__ import annotations
 
+import concurrent.futures
 import ctypes
 import os
 import subprocess
@@ -8,11 +9,11 @@ import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "spec_verify.cu")
-HEADER = os.path.join(ROOT, "include", "spec_verify.h")
+SOURCES = [os.path.join(PKG, "csrc", name) for name in ("spec_verify.cu", "spec_attn.cu")]
+HEADERS = [os.path.join(ROOT, "include", name) for name in ("spec_verify.h", "spec_attn.h")]
 LIB = os.path.join(PKG, "libspec_verify.so")
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
-              "-Xcompiler", "-fPIC", "-shared"]
+              "-Xcompiler", "-fPIC"]
 
 _lock = threading.Lock()
 _lib = None
@@ -26,17 +27,26 @@ def nvcc() -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/spec_verify.cu into libspec_verify.so beside this file."""
+    """Compile csrc/*.cu, in parallel, into libspec_verify.so beside this file."""
     with _lock:
         stale = not os.path.exists(LIB) or any(
-            os.path.getmtime(LIB) < os.path.getmtime(p) for p in (SRC, HEADER))
+            os.path.getmtime(LIB) < os.path.getmtime(p) for p in (*SOURCES, *HEADERS))
         if force or stale:
             tmp = LIB + f".tmp{os.getpid()}"
-            cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", tmp, SRC]
+            flags = [*NVCC_FLAGS, "-I", os.path.join(ROOT, "include")]
             if verbose:
-                cmd.insert(1, "-Xptxas=-v")
-            subprocess.check_call(cmd)
-            os.replace(tmp, LIB)
+                flags.append("-Xptxas=-v")
+            objects = [f"{tmp}.{os.path.basename(src)}.o" for src in SOURCES]
+            try:
+                with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as ex:
+                    list(ex.map(lambda so: subprocess.check_call([nvcc(), *flags, "-c", "-o", so[1], so[0]]),
+                                zip(SOURCES, objects)))
+                subprocess.check_call([nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objects])
+                os.replace(tmp, LIB)
+            finally:
+                for path in (tmp, *objects):
+                    if os.path.exists(path):
+                        os.remove(path)
     return LIB
 
 
@@ -78,5 +88,19 @@ def load() -> ctypes.CDLL:
     lib.spec_verify_destroy.argtypes = [vp]
     lib.spec_verify_strerror.restype = ctypes.c_char_p
     lib.spec_verify_strerror.argtypes = [i]
+    lib.spec_attn_init.restype = i
+    lib.spec_attn_init.argtypes = [p(vp), i, i, i, i]
+    lib.spec_attn_append.restype = i
+    lib.spec_attn_append.argtypes = [vp, vp, vp, vp, vp, vp]
+    lib.spec_attn_read.restype = i
+    lib.spec_attn_read.argtypes = [vp, vp, vp, vp, vp, vp]
+    lib.spec_attn_chunk.restype = i
+    lib.spec_attn_chunk.argtypes = [vp, vp, vp, vp, i, ctypes.c_float, vp, vp, vp]
+    lib.spec_attn_prompt.restype = i
+    lib.spec_attn_prompt.argtypes = [vp, i, i, vp, vp, vp, vp, ctypes.c_float, vp, vp, vp]
+    lib.spec_attn_get_error.restype = i
+    lib.spec_attn_get_error.argtypes = [vp]
+    lib.spec_attn_destroy.restype = None
+    lib.spec_attn_destroy.argtypes = [vp]
     _lib = lib
     return lib
