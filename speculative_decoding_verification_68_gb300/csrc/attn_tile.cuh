@@ -1,0 +1,876 @@
+// The attention kernel: softmax(scale * q k^T) v on the tensor cores, over the
+// paged cache (bf16 or e4m3) or packed prompts.
+//
+// For a row i of scores s_ij = scale * log2(e) * q_i.k_j one pass over the keys
+// keeps a reference M_i (the running maximum), l_i = sum_j 2^(s_ij - M_i) and
+// O_i = sum_j 2^(s_ij - M_i) v_j; the output is O_i / l_i and the log of the
+// sum ln 2 * (M_i + log2 l_i).  M_i only has to be near the maximum: it is
+// raised, and O_i and l_i rescaled, when a score passes it by 2^8, so most
+// blocks leave O_i, which lives in tensor memory, alone.
+//
+// Rows.  The q_heads / kv_heads query heads of a group share their keys, so a
+// tile of 128 rows holds floor(128 / group) tokens times the group and every
+// key block is read once for all of them.
+//
+// Work.  An item is (sequence, key-value head, row tile); its units are the
+// 128-key blocks that any of its rows sees.  The units of all items in order
+// are cut into equal runs, one per CTA (one CTA per SM), so few long
+// sequences fill the GPU as well as many short ones.  An item that lies in
+// several runs leaves partial (M, l, O) in the workspace and the last CTA to
+// finish merges them, in order: nothing waits, and results do not depend on
+// the order of arrival.
+//
+// Roles of a CTA's warps: one copies key and value blocks into shared memory
+// (TMA), one issues the matrix products, groups of four do the softmax, one
+// thread per row.  For an e4m3 cache four more turn the codes into f16 (see
+// below).
+#pragma once
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "attn_common.cuh"
+
+namespace {
+
+enum { KIND_BF16 = 0, KIND_E4M3 = 1, KIND_PACKED = 2 };
+
+constexpr int BN = 128;             // keys per block
+constexpr int BM = 128;             // rows per tile (tensor-memory lanes)
+constexpr int HALF_BYTES = BN * 128;  // 64 of the D columns of a block: 128 rows of one swizzled 128-byte line
+constexpr float LAZY = 8.0f;        // log2 of how far scores may pass the reference
+constexpr int POLLS = 1 << 18;      // of a bounded wait (about 1 s)
+constexpr int SMEM_LIMIT = 232448;
+constexpr int EV_MIN = -100;        // least exponent of a value block's reference (see convert)
+
+struct AttnParams {
+  Batch B;
+  Rows Q;
+  const uint8_t *ks, *vs;           // scale bytes (e4m3)
+  int q_heads, kv_heads, group;
+  int tile_tokens;                  // floor(128 / group)
+  int causal;
+  float c;                          // scale * log2(e)
+  __nv_bfloat16* out;
+  float* lse;
+  float* ws;                        // partials: [cta][2][MT] of PART floats
+  int* counters;                    // [cta][MT], zero between calls
+};
+
+// Floats of one partial: M and l per row, then O as [D / 4][128] float4
+template <int D> __host__ __device__ constexpr int part_floats() { return 2 * BM + BM * D; }
+
+// ------------------------------------------------------------------- PTX
+__device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint32_t a, unsigned n) { asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(a), "r"(n) : "memory"); }
+__device__ __forceinline__ void bar_expect(uint32_t a, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(a), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t a) { asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(a) : "memory"); }
+__device__ __forceinline__ bool bar_try(uint32_t a, unsigned parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok) : "r"(a), "r"(parity) : "memory");
+  return ok != 0;
+}
+// Bounded wait of a whole warp: false (and the handle flagged) instead of a
+// hang, in all lanes or in none.  Once one wait has given up the others see
+// the flag and give up within 256 polls.
+__device__ __noinline__ bool bar_wait_slow(uint32_t a, unsigned parity, int* flags) {
+  for (int it = 0; it < POLLS; ++it) {
+    if (__all_sync(FULL, bar_try(a, parity))) return true;
+    if ((it & 255) == 255 && __any_sync(FULL, *(volatile int*)&flags[1])) return false;
+  }
+  atomicExch(&flags[1], 1);
+  return false;
+}
+__device__ __forceinline__ bool bar_wait(uint32_t a, unsigned parity, int* flags) {
+  return __all_sync(FULL, bar_try(a, parity)) || bar_wait_slow(a, parity, flags);
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+               ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x, int y, int z, uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+               ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D[tmem] (+)= A[smem] B[smem], and with A in tensor memory
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+               ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+#define R8(r, o) "=r"((r)[o]), "=r"((r)[o + 1]), "=r"((r)[o + 2]), "=r"((r)[o + 3]), "=r"((r)[o + 4]), "=r"((r)[o + 5]), "=r"((r)[o + 6]), "=r"((r)[o + 7])
+#define I8(r, o) "r"((r)[o]), "r"((r)[o + 1]), "r"((r)[o + 2]), "r"((r)[o + 3]), "r"((r)[o + 4]), "r"((r)[o + 5]), "r"((r)[o + 6]), "r"((r)[o + 7])
+// 32 columns of this warp's 32 lanes; the loads complete at tc_wait_ld
+__device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+               "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+               : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24) : "r"(a));
+}
+__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+               "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
+               ::I8(r, 0), I8(r, 8), I8(r, 16), I8(r, 24), "r"(a) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
+typedef unsigned long long u64;
+__device__ __forceinline__ u64 pk(float lo, float hi) { u64 r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi)); return r; }
+__device__ __forceinline__ void upk(u64 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) { u64 d; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c)); return d; }
+__device__ __forceinline__ u64 add2(u64 a, u64 b) { u64 d; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b)); return d; }
+__device__ __forceinline__ void group_sync(int id, int n) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ bool group_or(int id, int n, bool v) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r) : "r"(id), "r"(n), "r"((uint32_t)v) : "memory");
+  return r != 0;
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle.  Rows of 128 bytes, 8 of
+// them (1024 bytes) a swizzle atom.  Query and key blocks are K-major (a row
+// per query or key, 64 of D in its line); value blocks are MN-major (a row per
+// key, 64 of D in its line), where the leading offset leads to the next 64 of D.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t leading_bytes) {
+  return (uint64_t)((addr & 0x3ffff) >> 4) | ((uint64_t)(leading_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor of kind::f16, M = 128, fp32 accumulators; A and B are both f16 or both bf16
+__host__ __device__ constexpr uint32_t instr_desc(bool bf16, int n, bool b_mn_major) {
+  return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(BM >> 4) << 24);
+}
+
+// ------------------------------------------------------------------ planning
+// sum over i = 0 .. n-1 of floor((a i + b) / m), by the Euclidean reduction of lattice points
+__device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+  unsigned long long s = 0;
+  while (n > 0) {
+    s += (unsigned long long)(n - 1) * n / 2 * (a / m);
+    a %= m;
+    s += (unsigned long long)n * (b / m);
+    b %= m;
+    const unsigned long long y = (unsigned long long)a * n + b;
+    if (y < m) break;
+    n = (unsigned)(y / m);
+    b = (unsigned)(y % m);
+    const unsigned t = m;
+    m = a;
+    a = t;
+  }
+  return (long long)s;
+}
+
+struct Seq {          // one sequence as the kernel sees it
+  int row0, n;        // packed rows
+  int kv;             // cached tokens (0 where the length is invalid)
+  int tiles;
+  bool bad;
+};
+__device__ __forceinline__ Seq load_seq(const Batch& B, int b, int tile_rows) {
+  Seq s;
+  const int a = __ldg(B.cu + b), e = __ldg(B.cu + b + 1);
+  const bool range = a >= 0 && e >= a && e <= B.n_tokens;
+  s.row0 = range ? a : 0;
+  s.n = range ? e - a : 0;
+  s.kv = B.kv_len ? __ldg(B.kv_len + b) : s.n;
+  s.bad = B.kv_len && !len_valid(B, s.kv);
+  if (s.bad) s.kv = 0;
+  s.tiles = (s.n + tile_rows - 1) / tile_rows;
+  s.bad |= !range;
+  return s;
+}
+// key blocks of tile t (at least one, so that its rows are written)
+__device__ __forceinline__ int tile_blocks(const Seq& s, int t, int tile_rows, int causal) {
+  const int len = causal ? s.kv - s.n + min(s.n, (t + 1) * tile_rows) : s.kv;
+  return max(1, (len + BN - 1) / BN);
+}
+// key blocks of tiles 0 .. t-1
+__device__ inline long long tiles_before(const Seq& s, int t, int tile_rows, int causal) {
+  if (t == 0) return 0;
+  if (!causal) return (long long)t * tile_blocks(s, 0, tile_rows, causal);
+  long long last = 0;
+  if (t == s.tiles) {                   // the last tile may be short
+    last = tile_blocks(s, t - 1, tile_rows, causal);
+    if (--t == 0) return last;
+  }
+  const int base = s.kv - s.n;          // tile i (from 1) ends at key base + i * tile_rows
+  const int ones = base >= BN ? 0 : min(t, (BN - base) / tile_rows);
+  if (ones == t) return last + t;
+  return last + ones + floor_sum((unsigned)(t - ones), BN, (unsigned)tile_rows, (unsigned)(base + (ones + 1) * tile_rows + BN - 1));
+}
+
+struct Segment {      // a run of blocks of one item
+  int b, head;
+  int row0, ntok;     // packed rows of the tile's tokens
+  int kv;             // cached tokens
+  int lim0;           // keys the tile's first token sees (causal) or kv
+  int j0, j1, nblk;   // blocks of this run, of the item
+  long long start;    // unit index of the item's first block
+  bool bad;
+};
+
+// Rounding the weights to bf16 costs little where many keys share the error.
+// An item whose rows see one block of keys at most has its weights in two bf16
+// parts and takes the product with the values twice.
+template <int KIND> __device__ __forceinline__ bool two_parts(const Segment& g) { return KIND != KIND_E4M3 && g.nblk == 1; }
+
+// Walks one CTA's units.  Every role walks on its own.
+struct Walker {
+  long long u, u1;
+  int b, head, t, j;
+  Seq s;
+  __device__ void begin(const AttnParams& A, int tile_rows) { s = load_seq(A.B, b, tile_rows); }
+  __device__ bool next(const AttnParams& A, int tile_rows, Segment& g) {
+    if (u >= u1) return false;
+    g.b = b; g.head = head;
+    g.row0 = s.row0 + t * tile_rows;
+    g.ntok = min(tile_rows, s.n - t * tile_rows);
+    g.kv = s.kv;
+    g.lim0 = A.causal ? s.kv - s.n + t * tile_rows + 1 : s.kv;
+    g.nblk = tile_blocks(s, t, tile_rows, A.causal);
+    g.j0 = j;
+    g.j1 = (int)min((long long)g.nblk, j + (u1 - u));
+    g.start = u - j;
+    g.bad = s.bad;
+    u += g.j1 - g.j0;
+    j = 0;
+    if (u < u1 && ++t == s.tiles) {
+      t = 0;
+      if (++head == A.kv_heads) {
+        head = 0;
+        do { s = load_seq(A.B, ++b, tile_rows); } while (s.tiles == 0 && b + 1 < A.B.n_seqs);
+      }
+    }
+    return true;
+  }
+};
+
+// -------------------------------------------------------------------- kernel
+template <int D, int KIND, int MT>
+struct Cfg {
+  static constexpr bool FP8 = KIND == KIND_E4M3;
+  static constexpr int HALVES = D / 64;
+  static constexpr int BUF = HALVES * HALF_BYTES;             // a block of keys or values in 16 bits
+  static constexpr int QBYTES = MT * BUF;
+  static constexpr int RAW = BN * D;                          // a block of codes
+  static constexpr int NRAW = FP8 ? (D == 128 ? 4 : 8) : 0;
+  static constexpr int SMALL = 1024;                          // barriers and bookkeeping, behind the buffers
+  static constexpr int NBUF = FP8 ? (D == 128 ? 4 : 6) : (SMEM_LIMIT - 1024 - SMALL - QBYTES) / BUF;
+  static constexpr int NK = (NBUF + 1) / 2, NV = NBUF / 2;
+  static constexpr int SMEM = 1024 + QBYTES + NBUF * BUF + NRAW * RAW + SMALL;   // 1024: alignment of the base
+  static constexpr int SOFT_WARP0 = 4;
+  static constexpr int CONV_WARP0 = SOFT_WARP0 + 4 * MT;
+  static constexpr int CONV_WARPS = FP8 ? 4 : 0;
+  static constexpr int WARPS = CONV_WARP0 + CONV_WARPS;
+  static constexpr int THREADS = WARPS * 32;
+  static constexpr int INFO = 8;                              // ring of block references (more than NK + 1)
+};
+
+template <int D, int KIND, int MT>
+__global__ void __launch_bounds__(Cfg<D, KIND, MT>::THREADS, 1)
+sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  using C = Cfg<D, KIND, MT>;
+  constexpr int NK = C::NK, NV = C::NV, NT = C::THREADS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (saddr(smem_raw) + 1023) & ~1023u;
+  uint8_t* const gbase = smem_raw + (base - saddr(smem_raw));
+  const uint32_t q_at = base, k_at = q_at + C::QBYTES, v_at = k_at + NK * C::BUF, raw_at = v_at + NV * C::BUF;
+  uint8_t* const small = gbase + (raw_at - base) + C::NRAW * C::RAW;
+  const uint32_t bars = saddr(small);
+  // barriers, 8 bytes each
+  const uint32_t k_full = bars, k_empty = k_full + 8 * NK, v_full = k_empty + 8 * NK, v_empty = v_full + 8 * NV,
+                 raw_full = v_empty + 8 * NV, raw_empty = raw_full + 8 * C::NRAW, s_full = raw_empty + 8 * C::NRAW,
+                 p_full = s_full + 16, o_done = p_full + 16, q_full = o_done + 16, drain = q_full + 8;
+  static_assert(8 * (2 * NK + 2 * NV + 2 * C::NRAW + 8) <= 320, "barrier area");
+  int* const work = (int*)(small + 320);                  // tensor-memory base, plan, merge flags
+  float2* const info = (float2*)(small + 448);            // block references of an e4m3 cache [INFO]
+  int* const red = (int*)(small + 512);                   // planning and reductions
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tile_rows = MT * A.tile_tokens;
+  int* const flags = A.B.flags;
+
+  // ---- set-up: barriers, tensor memory, and this CTA's run of units
+  if (tid == 0) {
+    for (int i = 0; i < NK; ++i) { bar_init(k_full + 8 * i, C::FP8 ? C::CONV_WARPS : 1); bar_init(k_empty + 8 * i, 1); }
+    for (int i = 0; i < NV; ++i) { bar_init(v_full + 8 * i, C::FP8 ? C::CONV_WARPS : 1); bar_init(v_empty + 8 * i, 1); }
+    for (int i = 0; i < C::NRAW; ++i) { bar_init(raw_full + 8 * i, 1); bar_init(raw_empty + 8 * i, C::CONV_WARPS); }
+    for (int i = 0; i < 2; ++i) { bar_init(s_full + 8 * i, 1); bar_init(p_full + 8 * i, 4); bar_init(o_done + 8 * i, 1); }
+    bar_init(q_full, 4 * MT);
+    bar_init(drain, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(work)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  long long* const red64 = (long long*)red;               // [0..15] warp sums, [16] running base
+  long long mine = 0;
+  for (int b = tid; b < A.B.n_seqs; b += NT) {
+    const Seq s = load_seq(A.B, b, tile_rows);
+    if (s.bad && blockIdx.x == 0) flags[0] = 1;
+    mine += tiles_before(s, s.tiles, tile_rows, A.causal) * A.kv_heads;
+  }
+  long long sum = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+  if (lane == 0) red64[warp] = sum;
+  __syncthreads();
+  long long units = 0;
+  for (int w = 0; w < C::WARPS; ++w) units += red64[w];
+  Walker W;
+  const long long ctas = min((long long)gridDim.x, units);   // every one of them has a unit
+  W.u = blockIdx.x < ctas ? units * blockIdx.x / ctas : 0;
+  W.u1 = blockIdx.x < ctas ? units * (blockIdx.x + 1) / ctas : 0;
+  W.b = W.head = W.t = W.j = 0;
+  if (W.u < W.u1) {
+    long long before = 0;
+    for (int b0 = 0; b0 < A.B.n_seqs; b0 += NT) {         // the sequence that holds unit u
+      const int b = b0 + tid;
+      if (A.B.n_seqs > NT) {
+        mine = 0;
+        if (b < A.B.n_seqs) {
+          const Seq s = load_seq(A.B, b, tile_rows);
+          mine = tiles_before(s, s.tiles, tile_rows, A.causal) * A.kv_heads;
+        }
+      }
+      long long scan = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(FULL, scan, o);
+        if (lane >= o) scan += x;
+      }
+      __syncthreads();
+      if (lane == 31) red64[warp] = scan;
+      __syncthreads();
+      long long chunk = 0, below = before;
+      for (int w = 0; w < C::WARPS; ++w) {
+        const long long x = red64[w];
+        if (w < warp) below += x;
+        chunk += x;
+      }
+      const long long end = below + scan, begin = end - mine;
+      if (begin <= W.u && W.u < end) {
+        const Seq s = load_seq(A.B, b, tile_rows);
+        const long long per = mine / A.kv_heads, at = W.u - begin, r = at % per;
+        int lo = 0, hi = s.tiles;                         // tile: largest t with tiles_before(t) <= r
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (tiles_before(s, mid, tile_rows, A.causal) <= r) lo = mid; else hi = mid;
+        }
+        work[1] = b;
+        work[2] = (int)(at / per);
+        work[3] = lo;
+        work[4] = (int)(r - tiles_before(s, lo, tile_rows, A.causal));
+      }
+      before += chunk;
+      if (before > W.u) break;                            // uniform
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = (uint32_t)work[0];
+  const bool busy = W.u < W.u1;
+  if (busy) {
+    W.b = work[1]; W.head = work[2]; W.t = work[3]; W.j = work[4];
+    W.begin(A, tile_rows);
+  }
+  // tensor memory: scores (and weights over them) at 0 and 128, outputs at 256 and 384
+  const uint32_t S_COL = tmem, O_COL = tmem + 256;
+  constexpr bool BF = !C::FP8;
+  constexpr uint32_t ID_QK = instr_desc(BF, BN, false), ID_PV = instr_desc(BF, D, true);
+  Segment g;
+
+  if (busy && warp == 0) {
+    // ---------------------------------------------------------------- copies
+    const int ps = 1 << A.B.page_shift, ppb = BN >> A.B.page_shift;
+    const int nowhere = A.B.num_pages * A.kv_heads * ps;   // a row past the pool: the copy fills zeros
+    unsigned nk = 0, nv = 0;                               // blocks issued
+    bool ok = true;
+    while (ok && W.next(A, tile_rows, g)) {
+      const int32_t* const tab = KIND == KIND_PACKED ? nullptr : A.B.table + (size_t)g.b * A.B.max_pages;
+      const int used = KIND == KIND_PACKED ? 0 : (g.kv + ps - 1) >> A.B.page_shift;
+      auto row_of = [&](int j) {                           // this lane's page of block j
+        const int p = j * ppb + lane;
+        if (lane >= ppb || p >= used) return nowhere;
+        const int page = __ldg(tab + p);
+        return (unsigned)page < (unsigned)A.B.num_pages ? (page * A.kv_heads + g.head) * ps : nowhere;
+      };
+      int row = KIND == KIND_PACKED ? 0 : row_of(g.j0);
+      for (int j = g.j0; j < g.j1; ++j) {
+        const int cur = row;
+        if (KIND != KIND_PACKED && j + 1 < g.j1) row = row_of(j + 1);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          const CUtensorMap* const map = kv ? &map_v : &map_k;
+          if constexpr (C::FP8) {
+            const unsigned n = nk++, s = n % C::NRAW;
+            if (!(ok = bar_wait(raw_empty + 8 * s, ((n / C::NRAW) & 1) ^ 1, flags))) break;
+            if (lane == 0) bar_expect(raw_full + 8 * s, C::RAW);
+            __syncwarp();
+            if (lane < ppb) tma_2d(raw_at + s * C::RAW + lane * ps * D, map, 0, cur, raw_full + 8 * s);
+          } else {
+            const unsigned n = kv ? nv++ : nk++, ring = kv ? NV : NK, s = n % ring;
+            const uint32_t full = (kv ? v_full : k_full) + 8 * s, empty = (kv ? v_empty : k_empty) + 8 * s;
+            const uint32_t dst = (kv ? v_at : k_at) + s * C::BUF;
+            if (!(ok = bar_wait(empty, ((n / ring) & 1) ^ 1, flags))) break;
+            if (lane == 0) bar_expect(full, C::BUF);
+            __syncwarp();
+            if (KIND == KIND_PACKED) {
+              if (lane < C::HALVES) tma_3d(dst + lane * HALF_BYTES, map, lane * 64, g.head, g.row0 - (g.lim0 - 1) + j * BN, full);
+            } else if (lane < ppb) {
+#pragma unroll
+              for (int x = 0; x < C::HALVES; ++x) tma_2d(dst + x * HALF_BYTES + lane * ps * 128, map, x * 64, cur, full);
+            }
+          }
+        }
+        if (!ok) break;
+      }
+    }
+    if (!ok) {                                             // let the copies in flight land
+      const int rings = C::FP8 ? 1 : 2;
+      for (int kv = 0; kv < rings; ++kv) {
+        const unsigned n = kv ? nv : nk, ring = C::FP8 ? C::NRAW : kv ? NV : NK;
+        for (unsigned i = n > ring ? n - ring : 0; i + 1 < n; ++i) {
+          const uint32_t full = (C::FP8 ? raw_full : kv ? v_full : k_full) + 8 * (i % ring);
+          for (int it = 0; it < 4096 && !bar_try(full, (i / ring) & 1); ++it) {}
+        }
+      }
+    }
+  } else if (busy && warp == 1) {
+    // -------------------------------------------------------------- products
+    unsigned n = 0;                                        // blocks whose scores have been issued
+    unsigned m = 0;                                        // blocks whose products with the values have been issued
+    unsigned segs = 0;
+    bool ok = true;
+    const bool one = lane == 0;
+    auto scores = [&](int tile, uint32_t s_at, unsigned i) {   // S = Q K^T of block i
+      if (one) {
+        const uint32_t kb = k_at + (i % NK) * C::BUF, qb = q_at + tile * C::BUF;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t off = (x / 4) * HALF_BYTES + (x % 4) * 32;
+          mma_ss(s_at, smem_desc(qb + off, 16), smem_desc(kb + off, 16), ID_QK, x > 0);
+        }
+      }
+    };
+    auto values = [&](int tile, uint32_t p_at, unsigned i, bool acc) {   // O (+)= P V of block i
+      if (one) {
+        const uint32_t vb = v_at + (i % NV) * C::BUF;
+#pragma unroll
+        for (int x = 0; x < BN / 16; ++x)
+          mma_ts(O_COL + tile * 128, p_at + x * 8, smem_desc(vb + x * 16 * 128, HALF_BYTES), ID_PV, acc || x > 0);
+      }
+    };
+    auto wait_k = [&](unsigned i) { return bar_wait(k_full + 8 * (i % NK), (i / NK) & 1, flags); };
+    auto wait_v = [&](unsigned i, int valid) {
+      if (!bar_wait(v_full + 8 * (i % NV), (i / NV) & 1, flags)) return false;
+      if (!C::FP8 && valid < BN) {
+        // slots past the sequence's end may hold anything; a weight of 0 does not clear NaN
+        uint8_t* const vb = gbase + (v_at - base) + (i % NV) * C::BUF;
+        for (int x = 0; x < C::HALVES; ++x)
+          for (int o = max(valid, 0) * 128 + lane * 16; o < HALF_BYTES; o += 512) *(uint4*)(vb + x * HALF_BYTES + o) = make_uint4(0, 0, 0, 0);
+        fence_async();
+        __syncwarp();
+      }
+      return true;
+    };
+    while (ok && W.next(A, tile_rows, g)) {
+      const int nb = g.j1 - g.j0;
+      if (!(ok = bar_wait(q_full, segs++ & 1, flags))) break;
+      tc_after();
+      if constexpr (MT == 2) {
+        if (!(ok = wait_k(n))) break;
+        for (int tile = 0; tile < 2; ++tile) {
+          scores(tile, S_COL + tile * 128, n);
+          if (one) tc_commit(s_full + 8 * tile);
+        }
+        if (one) tc_commit(k_empty + 8 * (n % NK));
+        ++n;
+        for (int j = 0; j < nb && ok; ++j, ++m) {
+          if (!(ok = wait_v(m, g.kv - (g.j0 + j) * BN))) break;
+          const bool more = j + 1 < nb;
+          for (int tile = 0; tile < 2 && ok; ++tile) {
+            if (!(ok = bar_wait(p_full + 8 * tile, m & 1, flags))) break;
+            tc_after();
+            values(tile, S_COL + tile * 128, m, j > 0);
+            if (two_parts<KIND>(g)) values(tile, S_COL + tile * 128 + 64, m, true);
+            if (one) tc_commit(o_done + 8 * tile);
+            if (more) {
+              if (tile == 0 && !(ok = wait_k(n))) break;
+              tc_after();
+              scores(tile, S_COL + tile * 128, n);         // in order behind the product that reads its weights
+              if (one) tc_commit(s_full + 8 * tile);
+            }
+          }
+          if (!ok) break;
+          if (one) tc_commit(v_empty + 8 * (m % NV));
+          if (more) {
+            if (one) tc_commit(k_empty + 8 * (n % NK));
+            ++n;
+          }
+        }
+      } else {
+        auto issue = [&]() {
+          if (!wait_k(n)) return false;
+          tc_after();
+          scores(0, S_COL + (n & 1) * 128, n);
+          if (one) {
+            tc_commit(s_full + 8 * (n & 1));
+            tc_commit(k_empty + 8 * (n % NK));
+          }
+          ++n;
+          return true;
+        };
+        ok = issue() && (nb < 2 || issue());
+        for (int j = 0; j < nb && ok; ++j, ++m) {
+          if (!(ok = bar_wait(p_full + 8 * (m & 1), (m >> 1) & 1, flags)) || !(ok = wait_v(m, g.kv - (g.j0 + j) * BN))) break;
+          tc_after();
+          values(0, S_COL + (m & 1) * 128, m, j > 0);
+          if (two_parts<KIND>(g)) values(0, S_COL + (m & 1) * 128 + 64, m, true);
+          if (one) {
+            tc_commit(o_done);
+            tc_commit(v_empty + 8 * (m % NV));
+          }
+          if (j + 2 < nb) ok = issue();
+        }
+      }
+    }
+    if (one) tc_commit(drain);                             // products and arrivals in flight end before the CTA does
+    __syncwarp();
+    for (int it = 0; it < POLLS && !bar_try(drain, 0); ++it) {}
+  } else if (busy && warp >= C::SOFT_WARP0 && warp < C::CONV_WARP0) {
+    // --------------------------------------------------------------- softmax
+    const int tile = MT == 2 ? (warp - C::SOFT_WARP0) >> 2 : 0;
+    const int r = tid & 127;                               // row of the tile, lane of tensor memory
+    const uint32_t lane_at = (uint32_t)(warp & 3) << 21;   // 32 lanes a warp, lane number in bits 16..31
+    const int bar_id = 1 + tile;
+    const int tok = r / A.group, head_in = r - tok * A.group;
+    unsigned n = 0;                                        // blocks done
+    bool ok = true;
+    while (W.next(A, tile_rows, g)) {
+      const int tk = tile * A.tile_tokens + tok;           // token of the item
+      const bool have = tok < A.tile_tokens && tk < g.ntok;
+      const int row = g.row0 + tk, hq = g.head * A.group + head_in;
+      const int lim = A.causal ? g.lim0 + tk : g.kv;
+      // -- query rows to shared memory, in f16 normalised by a power of two for an e4m3 cache
+      float c = A.c;
+      {
+        uint4 x[D / 8];
+        const uint4* const src = (const uint4*)(A.Q.ptr + row * A.Q.st + hq * A.Q.sh);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) x[i] = have ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+        if constexpr (C::FP8) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+          }
+          // largest magnitude in [1, 2): f16 holds it exactly, and what is 2^-14 of it or more
+          const int e = top >= 0x7f80u ? 0 : min(max((int)(top >> 7), 7), 247) - EXP_BIAS;
+          const float f = __int_as_float((EXP_BIAS - e) << 23);
+          c *= __int_as_float((EXP_BIAS + e) << 23);
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int e2 = 0; e2 < 4; ++e2) w[e2] = pack_f16(bf_lo(w[e2]) * f, bf_hi(w[e2]) * f);
+            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        uint8_t* const q = gbase + (q_at - base) + tile * C::BUF + r * 128;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) *(uint4*)(q + (i / 8) * HALF_BYTES + (((i % 8) ^ (r & 7)) << 4)) = x[i];
+      }
+      fence_async();
+      tc_before();
+      __syncwarp();
+      if (lane == 0) bar_arrive(q_full);
+      // -- pages of this run that do not exist
+      bool bad = g.bad;
+      if (KIND != KIND_PACKED) {
+        const int used = (g.kv + (1 << A.B.page_shift) - 1) >> A.B.page_shift, ppb = BN >> A.B.page_shift;
+        for (int p = g.j0 * ppb + r; p < min(g.j1 * ppb, used); p += BM)
+          bad |= (unsigned)__ldg(A.B.table + (size_t)g.b * A.B.max_pages + p) >= (unsigned)A.B.num_pages;
+      }
+      // -- blocks
+      float M = -INFINITY, l = 0.0f;
+      for (int j = g.j0; j < g.j1; ++j, ++n) {
+        const unsigned buf = MT == 2 ? tile : n & 1, ph = MT == 2 ? n & 1 : (n >> 1) & 1;
+        const uint32_t s_at = S_COL + buf * 128 + lane_at;
+        if (!(ok = bar_wait(s_full + 8 * buf, ph, flags))) break;
+        tc_after();
+        uint32_t x[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tm_ld32(s_at + 32 * i, x + 32 * i);
+        float cb = c, ev = 0.0f;
+        if constexpr (C::FP8) {
+          const float2 t = info[n % C::INFO];
+          cb = fmaxf(c * t.x, 1.17549435e-38f);              // a masked score's -inf times 0 would be NaN
+          ev = t.y;
+        }
+        tc_wait_ld();
+        const int rel = lim - j * BN;                      // keys of the block this row sees
+        if (rel < BN) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) x[i] = i < rel ? x[i] : 0xff800000u;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int i = 0; i < 128; i += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + e]), __uint_as_float(x[i + 4 + e])));
+        const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), cb, ev);
+        if (j == g.j0) {
+          M = top;
+        } else if (__any_sync(FULL, top > M + LAZY)) {
+          // raise the reference; the block before must have been added to O
+          if (!(ok = bar_wait(o_done + 8 * tile, (n - 1) & 1, flags))) break;
+          tc_after();
+          const float up = fmaxf(M, top), f = up == -INFINITY ? 1.0f : ex2(M - up);
+          M = up;
+          l *= f;
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            uint32_t o[32];
+            tm_ld32(O_COL + tile * 128 + lane_at + 32 * i, o);
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tm_st32(O_COL + tile * 128 + lane_at + 32 * i, o);
+          }
+        }
+        const float neg = ev - (M == -INFINITY ? 0.0f : M);
+        const u64 c2 = pk(cb, cb), n2 = pk(neg, neg);
+        u64 acc[2] = {0, 0};
+        auto weights = [&](auto split) {                   // exponentials, their sum, and the weights over the scores
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[32], low[decltype(split)::value ? 32 : 1];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float a, b;
+              upk(fma2(pk(__uint_as_float(x[64 * h + 2 * i]), __uint_as_float(x[64 * h + 2 * i + 1])), c2, n2), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              acc[i & 1] = add2(acc[i & 1], pk(a, b));
+              w[i] = C::FP8 ? pack_f16(a, b) : pack_bf16(a, b);
+              if constexpr (decltype(split)::value) low[i] = pack_bf16(a - bf_lo(w[i]), b - bf_hi(w[i]));
+            }
+            tm_st32(s_at + 32 * h, w);
+            if constexpr (decltype(split)::value) tm_st32(s_at + 64 + 32 * h, low);
+          }
+        };
+        if (two_parts<KIND>(g)) weights(std::true_type{}); else weights(std::false_type{});
+        float s0, s1, s2, s3;
+        upk(acc[0], s0, s1);
+        upk(acc[1], s2, s3);
+        const float add = (s0 + s1) + (s2 + s3);
+        l += C::FP8 ? add * __int_as_float((EXP_BIAS - (int)ev) << 23) : add;
+        tc_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(p_full + 8 * buf);
+      }
+      // -- the run's result
+      if (ok) ok = bar_wait(o_done + 8 * tile, (n - 1) & 1, flags);
+      if (group_or(bar_id, BM, !ok)) break;                // all four warps leave, or none
+      tc_after();
+      bad = group_or(bar_id, BM, bad);
+      if (bad) {
+        l = quiet_nan();
+        if (r == 0) flags[0] = 1;
+      }
+      const bool whole = g.j0 == 0 && g.j1 == g.nblk;
+      if (whole) {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          tm_ld32(O_COL + tile * 128 + lane_at + 32 * i, o);
+          tc_wait_ld();
+          if (have) {
+            uint4* const dst = (uint4*)(A.out + ((size_t)row * A.q_heads + hq) * D + 32 * i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[y] = pack_bf16(__uint_as_float(o[8 * e + 2 * y]) * inv, __uint_as_float(o[8 * e + 2 * y + 1]) * inv);
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        }
+        if (A.lse && have) A.lse[(size_t)row * A.q_heads + hq] = (M + log2f(l)) * LN2_F;
+      } else {
+        // partial: slot 1 of this CTA holds an item's beginning, slot 0 a later part
+        constexpr int PART = part_floats<D>();
+        auto part = [&](int cta, int slot) { return A.ws + ((size_t)(cta * 2 + slot) * MT + tile) * PART; };
+        float* const dst = part(blockIdx.x, g.j0 == 0 ? 1 : 0);
+        if (have) {
+          __stcg(dst + r, M);
+          __stcg(dst + BM + r, l);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t o[32];
+          tm_ld32(O_COL + tile * 128 + lane_at + 32 * i, o);
+          tc_wait_ld();
+          if (have) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              __stcg((float4*)(dst + 2 * BM) + (8 * i + e) * BM + r,
+                     make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
+          }
+        }
+        // runs that hold the item: CTA x has units [units x / ctas, units (x + 1) / ctas)
+        const int c0 = (int)(((g.start + 1) * ctas - 1) / units), c1 = (int)(((g.start + g.nblk) * ctas - 1) / units);
+        __threadfence();
+        group_sync(bar_id, BM);
+        if (r == 0) work[8 + tile] = atomicAdd(A.counters + c0 * MT + tile, 1) == c1 - c0;
+        group_sync(bar_id, BM);
+        if (work[8 + tile]) {                              // the last to finish
+          __threadfence();
+          if (r == 0) A.counters[c0 * MT + tile] = 0;
+          const int rows = min(A.tile_tokens, max(0, g.ntok - tile * A.tile_tokens)) * A.group;
+          for (int i = r; i < rows * (D / 4); i += BM) {
+            const int d4 = i / rows, rr = i - d4 * rows;
+            float top = -INFINITY;
+            bool nan = false;
+            for (int x = c0; x <= c1; ++x) {
+              const float m = __ldcg(part(x, x == c0) + rr);
+              nan |= isnan(m);
+              top = fmaxf(top, m);
+            }
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float sum = nan ? quiet_nan() : 0.0f;
+            float4 o = make_float4(0, 0, 0, 0);
+            for (int x = c0; x <= c1; ++x) {
+              const float* const p = part(x, x == c0);
+              const float f = ex2(__ldcg(p + rr) - ref);
+              const float4 y = __ldcg((const float4*)(p + 2 * BM) + d4 * BM + rr);
+              sum += f * __ldcg(p + BM + rr);
+              o.x += f * y.x; o.y += f * y.y; o.z += f * y.z; o.w += f * y.w;
+            }
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const int rt = rr / A.group, rh = rr - rt * A.group;
+            const size_t at = (size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + rh;
+            *(uint2*)(A.out + at * D + 4 * d4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+            if (A.lse && d4 == 0) A.lse[at] = (top + log2f(sum)) * LN2_F;
+          }
+        }
+      }
+      tc_before();
+    }
+  } else if constexpr (C::FP8) if (busy && warp >= C::CONV_WARP0) {
+    // ---------------------------------------------- e4m3 codes to f16 blocks
+    // A code is exact in f16, and so is its product with 2^(e_j - e), e the
+    // largest exponent among the block's vectors, unless the vector is 2^15
+    // times smaller than that one (then what is lost is 2^-25 of the largest).
+    // The softmax applies e once per block: key scores times 2^e, and for the
+    // values the reference M covers s_ij + e, so a weight times a block value
+    // stays within range whatever the vectors' sizes.  e of the values is kept
+    // within 2^64 of the run's largest so that the weights do not vanish.
+    const int t = tid - C::CONV_WARP0 * 32, cw = warp - C::CONV_WARP0;
+    constexpr int NTC = C::CONV_WARPS * 32;
+    static_assert(NTC == BN, "one converting thread per key");
+    uint8_t* const bytes = small + 704;                    // scale bytes of the block: keys, then values
+    int* const wmax = red + 4;                             // maxima per warp
+    unsigned n = 0, raw = 0;
+    bool ok = true, stop = false;
+    while (!stop && W.next(A, tile_rows, g)) {
+      const int32_t* const tab = A.B.table + (size_t)g.b * A.B.max_pages;
+      int run = EV_MIN;
+      auto load_bytes = [&](int j) {                       // this thread's key: bytes of key and value (0: none)
+        const int p = j * BN + t;
+        if (p >= g.kv) return make_int2(0, 0);
+        const int page = __ldg(tab + (p >> A.B.page_shift));
+        if ((unsigned)page >= (unsigned)A.B.num_pages) return make_int2(0, 0);
+        const size_t at = ((size_t)(page * A.kv_heads + g.head) << A.B.page_shift) + (p & ((1 << A.B.page_shift) - 1));
+        return make_int2(__ldg(A.ks + at), __ldg(A.vs + at));
+      };
+      int2 nxt = load_bytes(g.j0);
+      for (int j = g.j0; j < g.j1; ++j, ++n) {
+        const int2 cur = nxt;
+        if (j + 1 < g.j1) nxt = load_bytes(j + 1);
+        const int ka = __reduce_max_sync(FULL, cur.x == BYTE_NAN ? 0 : cur.x), va = __reduce_max_sync(FULL, cur.y == BYTE_NAN ? 0 : cur.y);
+        // the block before has read its bytes; all four warps leave, or none
+        if ((stop = group_or(3, NTC, !ok))) break;
+        bytes[t] = (uint8_t)cur.x;
+        bytes[BN + t] = (uint8_t)cur.y;
+        if (lane == 0) { wmax[cw] = ka; wmax[4 + cw] = va; }
+        group_sync(3, NTC);
+        int eb[2];
+        eb[0] = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])) - EXP_BIAS;
+        eb[1] = max(max(max(wmax[4], wmax[5]), max(wmax[6], wmax[7])) - EXP_BIAS, run - 64);
+        eb[0] = max(eb[0], EXP_MIN);
+        run = max(run, eb[1]);
+        eb[1] = max(eb[1], run - 64);
+        if (t == 0) info[n % C::INFO] = make_float2(__int_as_float((eb[0] + EXP_BIAS) << 23), (float)eb[1]);
+        const int valid = g.kv - j * BN;
+#pragma unroll
+        for (int kv = 0; kv < 2 && ok; ++kv, ++raw) {
+          const unsigned rs = raw % C::NRAW, ring = kv ? NV : NK, bs = n % ring;
+          const uint32_t full = (kv ? v_full : k_full) + 8 * bs, empty = (kv ? v_empty : k_empty) + 8 * bs;
+          if (!(ok = bar_wait(raw_full + 8 * rs, (raw / C::NRAW) & 1, flags)) || !(ok = bar_wait(empty, ((n / ring) & 1) ^ 1, flags))) break;
+          const uint8_t* const src = gbase + (raw_at - base) + rs * C::RAW;
+          uint8_t* const dst = gbase + ((kv ? v_at : k_at) - base) + bs * C::BUF;
+          constexpr int CH = BN * D / 16;                  // 16-code chunks of the block
+#pragma unroll 4
+          for (int i = t; i < CH; i += NTC) {
+            const int key = i / (D / 16), ch = i % (D / 16);
+            const uint4 x = *(const uint4*)(src + i * 16);
+            const int by = bytes[kv * BN + key];
+            const int d = by == BYTE_NAN ? 0 : by - EXP_BIAS - eb[kv];        // <= 0
+            const uint32_t f1 = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
+            const uint32_t f = f1 | (f1 << 16);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t hcode = e4m3_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+              asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(hcode), "r"(f));
+              if (key >= valid) y[e] = 0;
+            }
+            uint8_t* const line = dst + (ch / 4) * HALF_BYTES + key * 128;
+            const int c0 = (ch % 4) * 2;
+            *(uint4*)(line + ((c0 ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+            *(uint4*)(line + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(raw_empty + 8 * rs);
+            bar_arrive(full);
+          }
+        }
+      }
+    }
+  }
+  tc_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+}  // namespace

@@ -8,122 +8,11 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include "attn_common.cuh"
+#include "attn_tile.cuh"
 #include "spec_attn.h"
 
 namespace {
-
-constexpr unsigned FULL = 0xffffffffu;
-constexpr float LOG2E_F = 1.44269504088896341f;
-constexpr float LN2_F = 0.69314718055994531f;
-constexpr int EXP_MIN = -120;      // least exponent of a cached vector's scale
-constexpr int EXP_BIAS = 127;
-constexpr int BYTE_NAN = 255;      // scale byte of a vector that holds an infinity or NaN
-
-// ---------------------------------------------------------------- parameters
-struct Batch {                     // spec_attn_batch, plus what follows from the handle
-  const int32_t* cu;
-  const int32_t* kv_len;           // null: packed prompts (a sequence holds its new tokens only)
-  const int32_t* table;
-  int n_seqs, n_tokens, max_pages;
-  int page_shift;
-  int num_pages;
-  int* flags;                      // [0] invalid metadata, [1] wait timeout
-};
-struct Pool {
-  void* k;
-  void* v;
-  uint8_t* ks;
-  uint8_t* vs;
-};
-struct Rows {
-  const __nv_bfloat16* ptr;
-  long long st, sh;                // token and head strides, elements
-};
-
-// ------------------------------------------------------------------- helpers
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-// four floats to four e4m3 codes (nearest even, saturating; NaN stays NaN)
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-  uint16_t lo, hi;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-  return (uint32_t)lo | ((uint32_t)hi << 16);
-}
-// two e4m3 codes to two f16 values (exact)
-__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint16_t c) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
-  return r;
-}
-__device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
-  float2 r;
-  asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(h));
-  return r;
-}
-// 2^e for the exponents a scale byte can hold; NaN for BYTE_NAN
-__device__ __forceinline__ float scale_of(int byte) {
-  return byte == BYTE_NAN ? __int_as_float(0x7fc00000) : __int_as_float(byte << 23);
-}
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
-  return v;
-}
-
-// The sequence that holds packed token t, or -1.  cu need not be trusted: the
-// search stays in range whatever it holds, and the result is checked.
-__device__ __forceinline__ int find_seq(const Batch& B, int t) {
-  int lo = 0, hi = B.n_seqs;                      // largest b with cu[b] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(B.cu + mid) <= t) lo = mid; else hi = mid;
-  }
-  const int a = __ldg(B.cu + lo), e = __ldg(B.cu + lo + 1);
-  return (a >= 0 && a <= t && t < e && e <= B.n_tokens) ? lo : -1;
-}
-// Slot index (page * page_size + slot, the head still to be added) of position
-// pos; -1 where it has none, -2 where the metadata is invalid (flagged).
-__device__ __forceinline__ long long find_slot(const Batch& B, int b, int pos) {
-  if (pos < 0) return -1;
-  const int page = __ldg(B.table + (size_t)b * B.max_pages + (pos >> B.page_shift));
-  if ((unsigned)page >= (unsigned)B.num_pages) return -2;
-  return ((long long)page << B.page_shift) | (pos & ((1 << B.page_shift) - 1));
-}
-// Position of packed token t; false where the sequence is invalid.
-__device__ __forceinline__ bool token_place(const Batch& B, int t, int& b, int& pos) {
-  b = find_seq(B, t);
-  if (b < 0) return false;
-  const int len = __ldg(B.kv_len + b);
-  if (len < 0 || (long long)len > ((long long)B.max_pages << B.page_shift)) return false;
-  pos = len - __ldg(B.cu + b + 1) + t;
-  return true;
-}
-// element offset of the vector of (slot, head) in a pool [page, head, slot, D]
-__device__ __forceinline__ long long vec_index(long long slot, int head, int heads, int page_shift) {
-  const long long page = slot >> page_shift;
-  return ((page * heads + head) << page_shift) + (slot & ((1 << page_shift) - 1));
-}
-
-// Whether sequence b's row range and length are within the call's limits.
-__device__ __forceinline__ bool seq_valid(const Batch& B, int b) {
-  const int a = __ldg(B.cu + b), e = __ldg(B.cu + b + 1);
-  if (a < 0 || e < a || e > B.n_tokens) return false;
-  if (!B.kv_len) return true;
-  const int len = __ldg(B.kv_len + b);
-  return len >= 0 && (long long)len <= ((long long)B.max_pages << B.page_shift);
-}
-// The first block reports sequences that no token leads to (a decreasing cu).
-__device__ __forceinline__ void flag_invalid_seqs(const Batch& B) {
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < B.n_seqs; b += blockDim.x)
-      if (!seq_valid(B, b)) B.flags[0] = 1;
-}
 
 // -------------------------------------------------------------------- append
 // One 16-byte lane-load per 8 elements: D / 8 lanes hold one vector, so its
@@ -233,102 +122,6 @@ __global__ void __launch_bounds__(256) sa_read_kernel(Batch B, Pool P, uint4* ko
   }
 }
 
-// ----------------------------------------------------------------- attention
-// One warp per row (token, query head).  32 keys at a time: each lane scores
-// one key, the running maximum and sum are merged, then each lane adds the 32
-// values of its D / 32 dimensions.  Everything in 32 bits.
-template <int D, bool FP8, bool PACKED>
-__global__ void __launch_bounds__(128) sa_attention_simple(Batch B, Pool P, Rows Q, Rows K, Rows V, int q_heads, int kv_heads,
-                                                           int causal, float scale, __nv_bfloat16* out, float* lse) {
-  constexpr int DL = D / 32;
-  flag_invalid_seqs(B);
-  __shared__ float qs[4][D];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * 4 + w;
-  if (row >= (long long)B.n_tokens * q_heads) return;
-  const int t = (int)(row / q_heads), hq = (int)(row % q_heads), head = hq / (q_heads / kv_heads);
-  const int b = find_seq(B, t);
-  if (b < 0) {
-    if (lane == 0) B.flags[0] = 1;
-    return;
-  }
-  const int first = __ldg(B.cu + b), n = __ldg(B.cu + b + 1) - first;
-  int len = PACKED ? n : __ldg(B.kv_len + b);
-  bool bad = !PACKED && (len < 0 || (long long)len > ((long long)B.max_pages << B.page_shift));
-  const int seen = bad ? 0 : causal ? max(0, len - n + (t - first) + 1) : len;
-  for (int d = lane; d < D; d += 32) qs[w][d] = __bfloat162float(Q.ptr[t * Q.st + hq * Q.sh + d]) * (scale * LOG2E_F);
-  __syncwarp();
-  float m = -INFINITY, l = 0.0f, o[DL];
-#pragma unroll
-  for (int i = 0; i < DL; ++i) o[i] = 0.0f;
-  for (int j0 = 0; j0 < seen; j0 += 32) {
-    const int j = j0 + lane;
-    float s = -INFINITY;
-    long long vec = -1;
-    if (j < seen) {
-      if (PACKED) {
-        vec = first + j;
-      } else {
-        const long long slot = find_slot(B, b, j);
-        if (slot < 0) bad = true; else vec = vec_index(slot, head, kv_heads, B.page_shift);
-      }
-      if (vec >= 0) {
-        s = 0.0f;
-        if constexpr (FP8) {
-          const uint2* p = (const uint2*)((const char*)P.k + vec * D);
-          for (int c = 0; c < D / 8; ++c) {
-            const uint2 x = __ldg(p + c);
-            const uint32_t ww[2] = {x.x, x.y};
-            for (int e = 0; e < 4; ++e) {
-              const float2 z = f16x2_to_f32(e4m3_to_f16x2((uint16_t)(ww[e >> 1] >> (16 * (e & 1)))));
-              s += z.x * qs[w][c * 8 + 2 * e];
-              s += z.y * qs[w][c * 8 + 2 * e + 1];
-            }
-          }
-          s *= scale_of(__ldg(P.ks + vec));
-        } else {
-          const uint4* p = (const uint4*)(PACKED ? K.ptr + vec * K.st + head * K.sh : (const __nv_bfloat16*)P.k + vec * D);
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = __ldg(p + c);
-            const uint32_t ww[4] = {x.x, x.y, x.z, x.w};
-            for (int e = 0; e < 4; ++e) {
-              s += bf_lo(ww[e]) * qs[w][c * 8 + 2 * e];
-              s += bf_hi(ww[e]) * qs[w][c * 8 + 2 * e + 1];
-            }
-          }
-        }
-      }
-    }
-    float mx = s;
-    for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, x));
-    const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.0f : mn;
-    const float p = exp2f(s - ref), f = exp2f(m - ref);
-    float sum = p;
-    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(FULL, sum, x);
-    l = l * f + sum;
-    m = mn;
-    for (int i = 0; i < DL; ++i) o[i] *= f;
-    for (int k = 0; k < 32 && j0 + k < seen; ++k) {
-      const float pk = __shfl_sync(FULL, p, k);
-      const long long vk = __shfl_sync(FULL, vec, k);
-      if (vk < 0) continue;
-      if constexpr (FP8) {
-        const float f2 = scale_of(__ldg(P.vs + vk)) * pk;
-        const uint8_t* p8 = (const uint8_t*)P.v + vk * D + lane * DL;
-        for (int i = 0; i < DL; ++i) o[i] += f2 * f16x2_to_f32(e4m3_to_f16x2(p8[i])).x;
-      } else {
-        const __nv_bfloat16* pv = (PACKED ? V.ptr + vk * V.st + head * V.sh : (const __nv_bfloat16*)P.v + vk * D) + lane * DL;
-        for (int i = 0; i < DL; ++i) o[i] += pk * __bfloat162float(pv[i]);
-      }
-    }
-  }
-  bad = __any_sync(FULL, bad);
-  if (bad && lane == 0) B.flags[0] = 1;
-  const float inv = bad ? __int_as_float(0x7fc00000) : l == 0.0f ? 0.0f : 1.0f / l;
-  for (int i = 0; i < DL; ++i) out[row * D + lane * DL + i] = __float2bfloat16(o[i] * inv);
-  if (lse && lane == 0) lse[row] = bad ? inv : (m + log2f(l)) * LN2_F;
-}
-
 }  // namespace
 
 // ---------------------------------------------------------------------- host
@@ -336,35 +129,16 @@ struct spec_attn_ctx {
   int device, q_heads, kv_heads, D, max_seqs;
   int n_sm;
   int* d_flags;
+  float* ws;                         // partial results of the split attention
+  int* counters;
 };
 
 static void free_ctx(spec_attn_ctx* h) {
   if (!h) return;
-  if (h->d_flags) cudaFree(h->d_flags);
+  void* ptrs[] = {h->d_flags, h->ws, h->counters};
+  for (void* p : ptrs)
+    if (p) cudaFree(p);
   free(h);
-}
-
-extern "C" int spec_attn_init(spec_attn_t* out, int q_heads, int kv_heads, int head_dim, int max_seqs) {
-  if (!out) return SV_ERR_ARG;
-  *out = nullptr;
-  if (q_heads < 1 || kv_heads < 1 || max_seqs < 1) return SV_ERR_ARG;
-  if (q_heads % kv_heads || q_heads / kv_heads > 64 || q_heads > 1024 || max_seqs > 65536 || (head_dim != 64 && head_dim != 128))
-    return SV_ERR_SIZE;
-  spec_attn_ctx* h = (spec_attn_ctx*)calloc(1, sizeof(spec_attn_ctx));
-  if (!h) return SV_ERR_ALLOC;
-  h->q_heads = q_heads; h->kv_heads = kv_heads; h->D = head_dim; h->max_seqs = max_seqs;
-  if (cudaGetDevice(&h->device) != cudaSuccess || cudaDeviceGetAttribute(&h->n_sm, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
-    cudaGetLastError();
-    free_ctx(h);
-    return SV_ERR_CUDA;
-  }
-  if (cudaMalloc(&h->d_flags, 4 * sizeof(int)) != cudaSuccess || cudaMemset(h->d_flags, 0, 4 * sizeof(int)) != cudaSuccess) {
-    cudaGetLastError();
-    free_ctx(h);
-    return SV_ERR_ALLOC;
-  }
-  *out = h;
-  return SV_OK;
 }
 
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
@@ -452,12 +226,98 @@ extern "C" int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const s
   return launched();
 }
 
-template <int D, bool FP8, bool PACKED>
-static void launch_attention(spec_attn_ctx* h, const Batch& B, const Pool& P, const Rows& Q, const Rows& K, const Rows& V, int causal,
-                             float scale, void* out, float* lse, cudaStream_t s) {
-  const long long rows = (long long)B.n_tokens * h->q_heads;
-  sa_attention_simple<D, FP8, PACKED><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(B, P, Q, K, V, h->q_heads, h->kv_heads, causal, scale,
-                                                                              (__nv_bfloat16*)out, lse);
+// ---- attention launches
+constexpr int MT_MAX = 2;
+static size_t ws_bytes(int n_sm, int D) { return (size_t)n_sm * 2 * MT_MAX * (D == 128 ? part_floats<128>() : part_floats<64>()) * sizeof(float); }
+
+typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeTiled encode_tiled() {
+  static const EncodeTiled f = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return (EncodeTiled)p;
+  }();
+  return f;
+}
+// Pool pages as rows of D elements, one page and head a box (64 columns of it for 16-bit elements, which swizzled lines hold)
+static bool map_pool(CUtensorMap* m, const spec_attn_ctx* h, const spec_attn_pool* p, void* base) {
+  const bool e4m3 = p->dtype == SV_E4M3;
+  const cuuint64_t dims[2] = {(cuuint64_t)h->D, (cuuint64_t)p->num_pages * h->kv_heads * p->page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)h->D * (e4m3 ? 1 : 2)};
+  const cuuint32_t box[2] = {(cuuint32_t)(e4m3 ? h->D : 64), (cuuint32_t)p->page_size}, step[2] = {1, 1};
+  return encode_tiled()(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// Packed rows [token, head, D], 128 tokens of one head and 64 columns a box
+static bool map_rows(CUtensorMap* m, const spec_attn_ctx* h, const Rows& r, int n_tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)h->D, (cuuint64_t)h->kv_heads, (cuuint64_t)n_tokens};
+  // a dimension of one element has no stride worth the name
+  const cuuint64_t strides[2] = {(cuuint64_t)(h->kv_heads > 1 ? r.sh : h->D) * 2, (cuuint64_t)(n_tokens > 1 ? r.st : (long long)h->D * h->kv_heads) * 2};
+  const cuuint32_t box[3] = {64, 1, BN}, step[3] = {1, 1, 1};
+  return encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void*)r.ptr, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+template <int D, int KIND, int MT>
+static bool allow_smem() {
+  return cudaFuncSetAttribute(sa_attention_kernel<D, KIND, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D, KIND, MT>::SMEM) == cudaSuccess;
+}
+template <int D>
+static bool allow_smem_all() {
+  return allow_smem<D, KIND_BF16, 1>() && allow_smem<D, KIND_BF16, 2>() && allow_smem<D, KIND_E4M3, 1>() && allow_smem<D, KIND_PACKED, 2>();
+}
+template <int D, int KIND, int MT>
+static int launch_attention(const spec_attn_ctx* h, const AttnParams& A, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  sa_attention_kernel<D, KIND, MT><<<h->n_sm, Cfg<D, KIND, MT>::THREADS, Cfg<D, KIND, MT>::SMEM, s>>>(A, mk, mv);
+  return launched();
+}
+static AttnParams attn_params(const spec_attn_ctx* h, const Batch& B, const Rows& Q, int causal, float scale, void* out, float* lse) {
+  AttnParams A;
+  A.B = B; A.Q = Q;
+  A.ks = A.vs = nullptr;
+  A.q_heads = h->q_heads; A.kv_heads = h->kv_heads; A.group = h->q_heads / h->kv_heads;
+  A.tile_tokens = BM / A.group;
+  A.causal = causal != 0;
+  A.c = fmaxf(scale * LOG2E_F, 1.17549435e-38f);
+  A.out = (__nv_bfloat16*)out; A.lse = lse;
+  A.ws = h->ws; A.counters = h->counters;
+  return A;
+}
+
+extern "C" int spec_attn_init(spec_attn_t* out, int q_heads, int kv_heads, int head_dim, int max_seqs) {
+  if (!out) return SV_ERR_ARG;
+  *out = nullptr;
+  if (q_heads < 1 || kv_heads < 1 || max_seqs < 1) return SV_ERR_ARG;
+  if (q_heads % kv_heads || q_heads / kv_heads > 64 || q_heads > 1024 || max_seqs > 65536 || (head_dim != 64 && head_dim != 128))
+    return SV_ERR_SIZE;
+  spec_attn_ctx* h = (spec_attn_ctx*)calloc(1, sizeof(spec_attn_ctx));
+  if (!h) return SV_ERR_ALLOC;
+  h->q_heads = q_heads; h->kv_heads = kv_heads; h->D = head_dim; h->max_seqs = max_seqs;
+  if (cudaGetDevice(&h->device) != cudaSuccess || cudaDeviceGetAttribute(&h->n_sm, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess) {
+    cudaGetLastError();
+    free_ctx(h);
+    return SV_ERR_CUDA;
+  }
+  if (!encode_tiled() || !(head_dim == 128 ? allow_smem_all<128>() : allow_smem_all<64>())) {
+    cudaGetLastError();
+    free_ctx(h);
+    return SV_ERR_CUDA;
+  }
+  const size_t counters = (size_t)h->n_sm * MT_MAX * sizeof(int);
+  if (cudaMalloc(&h->d_flags, 4 * sizeof(int)) != cudaSuccess || cudaMemset(h->d_flags, 0, 4 * sizeof(int)) != cudaSuccess ||
+      cudaMalloc(&h->counters, counters) != cudaSuccess || cudaMemset(h->counters, 0, counters) != cudaSuccess ||
+      cudaMalloc(&h->ws, ws_bytes(h->n_sm, head_dim)) != cudaSuccess) {
+    cudaGetLastError();
+    free_ctx(h);
+    return SV_ERR_ALLOC;
+  }
+  *out = h;
+  return SV_OK;
 }
 
 extern "C" int spec_attn_chunk(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch,
@@ -470,16 +330,16 @@ extern "C" int spec_attn_chunk(spec_attn_t h, const spec_attn_pool* pool, const 
   if (!out || !aligned16(out)) return SV_ERR_ARG;
   const cudaStream_t s = (cudaStream_t)cuda_stream;
   const Batch B = batch_of(h, batch, pool);
-  const Pool P = pool_of(pool);
-  const Rows Q = rows_of(q), none{};
-  if (h->D == 128) {
-    if (pool->dtype == SV_E4M3) launch_attention<128, true, false>(h, B, P, Q, none, none, causal, scale, out, lse, s);
-    else launch_attention<128, false, false>(h, B, P, Q, none, none, causal, scale, out, lse, s);
-  } else {
-    if (pool->dtype == SV_E4M3) launch_attention<64, true, false>(h, B, P, Q, none, none, causal, scale, out, lse, s);
-    else launch_attention<64, false, false>(h, B, P, Q, none, none, causal, scale, out, lse, s);
+  AttnParams A = attn_params(h, B, rows_of(q), causal, scale, out, lse);
+  CUtensorMap mk, mv;
+  if (!map_pool(&mk, h, pool, pool->k) || !map_pool(&mv, h, pool, pool->v)) return SV_ERR_CUDA;
+  if (pool->dtype == SV_E4M3) {
+    A.ks = pool->k_scale; A.vs = pool->v_scale;
+    return h->D == 128 ? launch_attention<128, KIND_E4M3, 1>(h, A, mk, mv, s) : launch_attention<64, KIND_E4M3, 1>(h, A, mk, mv, s);
   }
-  return launched();
+  const bool two = (long long)B.n_tokens * A.group > (long long)B.n_seqs * BM;   // more rows per sequence and head than one tile holds
+  if (h->D == 128) return two ? launch_attention<128, KIND_BF16, 2>(h, A, mk, mv, s) : launch_attention<128, KIND_BF16, 1>(h, A, mk, mv, s);
+  return two ? launch_attention<64, KIND_BF16, 2>(h, A, mk, mv, s) : launch_attention<64, KIND_BF16, 1>(h, A, mk, mv, s);
 }
 
 extern "C" int spec_attn_prompt(spec_attn_t h, int n_seqs, int n_tokens, const int32_t* cu,
@@ -495,16 +355,19 @@ extern "C" int spec_attn_prompt(spec_attn_t h, int n_seqs, int n_tokens, const i
   const cudaStream_t s = (cudaStream_t)cuda_stream;
   const spec_attn_batch batch = {cu, nullptr, nullptr, n_seqs, n_tokens, 0};
   const Batch B = batch_of(h, &batch, nullptr);
-  if (h->D == 128) launch_attention<128, false, true>(h, B, Pool{}, rows_of(q), rows_of(k), rows_of(v), 1, scale, out, lse, s);
-  else launch_attention<64, false, true>(h, B, Pool{}, rows_of(q), rows_of(k), rows_of(v), 1, scale, out, lse, s);
-  return launched();
+  const AttnParams A = attn_params(h, B, rows_of(q), 1, scale, out, lse);
+  CUtensorMap mk, mv;
+  if (!map_rows(&mk, h, rows_of(k), n_tokens) || !map_rows(&mv, h, rows_of(v), n_tokens)) return SV_ERR_ARG;
+  return h->D == 128 ? launch_attention<128, KIND_PACKED, 2>(h, A, mk, mv, s) : launch_attention<64, KIND_PACKED, 2>(h, A, mk, mv, s);
 }
 
 extern "C" int spec_attn_get_error(spec_attn_t h) {
   if (!h) return SV_ERR_ARG;
   int f[2] = {0, 0};
   if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(f, h->d_flags, sizeof f, cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(h->d_flags, 0, sizeof f) != cudaSuccess) {
+      cudaMemset(h->d_flags, 0, sizeof f) != cudaSuccess ||
+      // a call whose wait expired may have left its merge counters behind
+      (f[1] && cudaMemset(h->counters, 0, (size_t)h->n_sm * MT_MAX * sizeof(int)) != cudaSuccess)) {
     cudaGetLastError();
     return SV_ERR_CUDA;
   }
