@@ -45,6 +45,7 @@ constexpr int HALF_BYTES = BN * 128;  // 64 of the D columns of a block: 128 row
 constexpr float LAZY = 8.0f;        // log2 of how far scores may pass the reference
 constexpr int POLLS = 1 << 18;      // of a bounded wait (about 1 s)
 constexpr int SMEM_LIMIT = 232448;
+constexpr int MIN_RUN = 2;          // units of a CTA at least
 constexpr int EV_MIN = -100;        // least exponent of a value block's reference (see convert)
 
 struct AttnParams {
@@ -61,8 +62,8 @@ struct AttnParams {
   int* counters;                    // [cta][MT], zero between calls
 };
 
-// Floats of one partial: M and l per row, then O as [D / 4][128] float4
-template <int D> __host__ __device__ constexpr int part_floats() { return 2 * BM + BM * D; }
+// Floats of one partial: M, l and its correction per row, then O as [D / 4][128] float4
+template <int D> __host__ __device__ constexpr int part_floats() { return 3 * BM + BM * D; }
 
 // ------------------------------------------------------------------- PTX
 __device__ __forceinline__ uint32_t saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -105,7 +106,6 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // D[tmem] (+)= A[smem] B[smem], and with A in tensor memory
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
@@ -118,6 +118,11 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 #define R8(r, o) "=r"((r)[o]), "=r"((r)[o + 1]), "=r"((r)[o + 2]), "=r"((r)[o + 3]), "=r"((r)[o + 4]), "=r"((r)[o + 5]), "=r"((r)[o + 6]), "=r"((r)[o + 7])
 #define I8(r, o) "r"((r)[o]), "r"((r)[o + 1]), "r"((r)[o + 2]), "r"((r)[o + 3]), "r"((r)[o + 4]), "r"((r)[o + 5]), "r"((r)[o + 6]), "r"((r)[o + 7])
+#define P8(r, o) "+r"((r)[o]), "+r"((r)[o + 1]), "+r"((r)[o + 2]), "+r"((r)[o + 3]), "+r"((r)[o + 4]), "+r"((r)[o + 5]), "+r"((r)[o + 6]), "+r"((r)[o + 7])
+// Waits for this thread's loads; the registers pass through, so that no use of them moves before it
+__device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : P8(r, 0), P8(r, 8), P8(r, 16), P8(r, 24)::"memory");
+}
 // 32 columns of this warp's 32 lanes; the loads complete at tc_wait_ld
 __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -128,6 +133,10 @@ __device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
                "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
                ::I8(r, 0), I8(r, 8), I8(r, 16), I8(r, 24), "r"(a) : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
+               ::I8(r, 0), I8(r, 8), "r"(a) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
 typedef unsigned long long u64;
@@ -334,8 +343,8 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   long long units = 0;
   for (int w = 0; w < C::WARPS; ++w) units += red64[w];
   Walker W;
-  const long long ctas = min((long long)gridDim.x, units);   // every one of them has a unit
-  W.u = blockIdx.x < ctas ? units * blockIdx.x / ctas : 0;
+  const long long ctas = min((long long)gridDim.x, max(1ll, units / MIN_RUN));
+  W.u = blockIdx.x < ctas ? units * blockIdx.x / ctas : 0;   // none without units
   W.u1 = blockIdx.x < ctas ? units * (blockIdx.x + 1) / ctas : 0;
   W.b = W.head = W.t = W.j = 0;
   if (W.u < W.u1) {
@@ -397,7 +406,8 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   constexpr uint32_t ID_QK = instr_desc(BF, BN, false), ID_PV = instr_desc(BF, D, true);
   Segment g;
 
-  if (busy && warp == 0) {
+  if (warp < C::SOFT_WARP0) {
+    if (busy && warp == 0) {
     // ---------------------------------------------------------------- copies
     const int ps = 1 << A.B.page_shift, ppb = BN >> A.B.page_shift;
     const int nowhere = A.B.num_pages * A.kv_heads * ps;   // a row past the pool: the copy fills zeros
@@ -453,7 +463,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         }
       }
     }
-  } else if (busy && warp == 1) {
+    } else if (busy && warp == 1) {
     // -------------------------------------------------------------- products
     unsigned n = 0;                                        // blocks whose scores have been issued
     unsigned m = 0;                                        // blocks whose products with the values have been issued
@@ -475,7 +485,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const uint32_t vb = v_at + (i % NV) * C::BUF;
 #pragma unroll
         for (int x = 0; x < BN / 16; ++x)
-          mma_ts(O_COL + tile * 128, p_at + x * 8, smem_desc(vb + x * 16 * 128, HALF_BYTES), ID_PV, acc || x > 0);
+          mma_ts(O_COL + tile * 128, p_at + (x / 2) * 32 + (x % 2) * 8, smem_desc(vb + x * 16 * 128, HALF_BYTES), ID_PV, acc || x > 0);
       }
     };
     auto wait_k = [&](unsigned i) { return bar_wait(k_full + 8 * (i % NK), (i / NK) & 1, flags); };
@@ -510,7 +520,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             if (!(ok = bar_wait(p_full + 8 * tile, m & 1, flags))) break;
             tc_after();
             values(tile, S_COL + tile * 128, m, j > 0);
-            if (two_parts<KIND>(g)) values(tile, S_COL + tile * 128 + 64, m, true);
+            if (two_parts<KIND>(g)) values(tile, S_COL + tile * 128 + 16, m, true);
             if (one) tc_commit(o_done + 8 * tile);
             if (more) {
               if (tile == 0 && !(ok = wait_k(n))) break;
@@ -543,7 +553,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           if (!(ok = bar_wait(p_full + 8 * (m & 1), (m >> 1) & 1, flags)) || !(ok = wait_v(m, g.kv - (g.j0 + j) * BN))) break;
           tc_after();
           values(0, S_COL + (m & 1) * 128, m, j > 0);
-          if (two_parts<KIND>(g)) values(0, S_COL + (m & 1) * 128 + 64, m, true);
+          if (two_parts<KIND>(g)) values(0, S_COL + (m & 1) * 128 + 16, m, true);
           if (one) {
             tc_commit(o_done);
             tc_commit(v_empty + 8 * (m % NV));
@@ -555,7 +565,9 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     if (one) tc_commit(drain);                             // products and arrivals in flight end before the CTA does
     __syncwarp();
     for (int it = 0; it < POLLS && !bar_try(drain, 0); ++it) {}
-  } else if (busy && warp >= C::SOFT_WARP0 && warp < C::CONV_WARP0) {
+    }
+  } else if (warp < C::CONV_WARP0) {
+    if (busy) {
     // --------------------------------------------------------------- softmax
     const int tile = MT == 2 ? (warp - C::SOFT_WARP0) >> 2 : 0;
     const int r = tid & 127;                               // row of the tile, lane of tensor memory
@@ -612,33 +624,50 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           bad |= (unsigned)__ldg(A.B.table + (size_t)g.b * A.B.max_pages + p) >= (unsigned)A.B.num_pages;
       }
       // -- blocks
-      float M = -INFINITY, l = 0.0f;
+      float M = -INFINITY, l = 0.0f, off = 0.0f;
       for (int j = g.j0; j < g.j1; ++j, ++n) {
         const unsigned buf = MT == 2 ? tile : n & 1, ph = MT == 2 ? n & 1 : (n >> 1) & 1;
         const uint32_t s_at = S_COL + buf * 128 + lane_at;
         if (!(ok = bar_wait(s_full + 8 * buf, ph, flags))) break;
         tc_after();
-        uint32_t x[128];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) tm_ld32(s_at + 32 * i, x + 32 * i);
+        const int rel = lim - j * BN;                      // keys of the block this row sees
         float cb = c, ev = 0.0f;
         if constexpr (C::FP8) {
           const float2 t = info[n % C::INFO];
           cb = fmaxf(c * t.x, 1.17549435e-38f);              // a masked score's -inf times 0 would be NaN
           ev = t.y;
         }
-        tc_wait_ld();
-        const int rel = lim - j * BN;                      // keys of the block this row sees
-        if (rel < BN) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) x[i] = i < rel ? x[i] : 0xff800000u;
-        }
+        // The row is read twice, 32 scores at a time (once for the maximum, once for the weights), so
+        // that it needs no 128 registers; the next 32 are on their way while these are worked on.
+        uint32_t xa[32], xb[32];
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto mask = [&](uint32_t* x, int h) {
+          if (rel < BN) {
 #pragma unroll
-        for (int i = 0; i < 128; i += 8)
+            for (int i = 0; i < 32; ++i) x[i] = 32 * h + i < rel ? x[i] : 0xff800000u;
+          }
+        };
+        auto maximum = [&](uint32_t* x, int h) {
+          mask(x, h);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + e]), __uint_as_float(x[i + 4 + e])));
-        const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), cb, ev);
+          for (int i = 0; i < 32; i += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + e]), __uint_as_float(x[i + 4 + e])));
+        };
+        tm_ld32(s_at, xa);
+        tc_wait_ld(xa);
+        tm_ld32(s_at + 32, xb);
+        maximum(xa, 0);
+        tc_wait_ld(xb);
+        tm_ld32(s_at + 64, xa);
+        maximum(xb, 1);
+        tc_wait_ld(xa);
+        tm_ld32(s_at + 96, xb);
+        maximum(xa, 2);
+        tc_wait_ld(xb);
+        tm_ld32(s_at, xa);
+        maximum(xb, 3);
+        const float best = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), top = fmaf(best, cb, ev);
         if (j == g.j0) {
           M = top;
         } else if (__any_sync(FULL, top > M + LAZY)) {
@@ -648,11 +677,12 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           const float up = fmaxf(M, top), f = up == -INFINITY ? 1.0f : ex2(M - up);
           M = up;
           l *= f;
+          off *= f;
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             uint32_t o[32];
             tm_ld32(O_COL + tile * 128 + lane_at + 32 * i, o);
-            tc_wait_ld();
+            tc_wait_ld(o);
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
             tm_st32(O_COL + tile * 128 + lane_at + 32 * i, o);
@@ -661,52 +691,80 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const float neg = ev - (M == -INFINITY ? 0.0f : M);
         const u64 c2 = pk(cb, cb), n2 = pk(neg, neg);
         u64 acc[2] = {0, 0};
-        auto weights = [&](auto split) {                   // exponentials, their sum, and the weights over the scores
+        const bool split = two_parts<KIND>(g);
+        // exponentials, their sum, and the weights in 16 bits in place of their scores: 32 scores become 16
+        // columns of weights and 16 of what rounding left of them
+        auto weights = [&](uint32_t* x, int h) {
+          mask(x, h);
+          uint32_t w[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w[32], low[decltype(split)::value ? 32 : 1];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              float a, b;
-              upk(fma2(pk(__uint_as_float(x[64 * h + 2 * i]), __uint_as_float(x[64 * h + 2 * i + 1])), c2, n2), a, b);
-              a = ex2(a);
-              b = ex2(b);
-              acc[i & 1] = add2(acc[i & 1], pk(a, b));
-              w[i] = C::FP8 ? pack_f16(a, b) : pack_bf16(a, b);
-              if constexpr (decltype(split)::value) low[i] = pack_bf16(a - bf_lo(w[i]), b - bf_hi(w[i]));
+          for (int i = 0; i < 16; ++i) {
+            float a, b;
+            upk(fma2(pk(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, n2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            acc[i & 1] = add2(acc[i & 1], pk(a, b));
+            w[i] = C::FP8 ? pack_f16(a, b) : pack_bf16(a, b);
+            if (!C::FP8) {
+              x[2 * i] = __float_as_uint(a);
+              x[2 * i + 1] = __float_as_uint(b);
             }
-            tm_st32(s_at + 32 * h, w);
-            if constexpr (decltype(split)::value) tm_st32(s_at + 64 + 32 * h, low);
+          }
+          tm_st16(s_at + 32 * h, w);
+          if (!C::FP8 && split) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(__uint_as_float(x[2 * i]) - bf_lo(w[i]), __uint_as_float(x[2 * i + 1]) - bf_hi(w[i]));
+            tm_st16(s_at + 32 * h + 16, w);
           }
         };
-        if (two_parts<KIND>(g)) weights(std::true_type{}); else weights(std::false_type{});
+        tc_wait_ld(xa);
+        tm_ld32(s_at + 32, xb);
+        weights(xa, 0);
+        tc_wait_ld(xb);
+        tm_ld32(s_at + 64, xa);
+        weights(xb, 1);
+        tc_wait_ld(xa);
+        tm_ld32(s_at + 96, xb);
+        weights(xa, 2);
+        tc_wait_ld(xb);
+        weights(xb, 3);
         float s0, s1, s2, s3;
         upk(acc[0], s0, s1);
         upk(acc[1], s2, s3);
         const float add = (s0 + s1) + (s2 + s3);
         l += C::FP8 ? add * __int_as_float((EXP_BIAS - (int)ev) << 23) : add;
+        if (!C::FP8 && !split) {
+          // what rounding to bf16 did to the block's largest weight (see the run's result)
+          const float p = ex2(fmaf(best, cb, neg));
+          off += __bfloat162float(__float2bfloat16(p)) - p;
+        }
         tc_wait_st();
         tc_before();
         __syncwarp();
         if (lane == 0) bar_arrive(p_full + 8 * buf);
       }
-      // -- the run's result
+      // -- the run's result.  Dividing by the sum of the rounded weights would cancel the rounding of a
+      // key that dominates its row, where it does not average out; off corrects the sum for the largest
+      // weight of each block, which is the one that can.
+      // With two score buffers of one tile, the last two products may both be on their way, and a wait
+      // for a phase must not start two phases ahead of the barrier.
+      if (MT == 1 && ok && n >= 2) ok = bar_wait(o_done + 8 * tile, (n - 2) & 1, flags);
       if (ok) ok = bar_wait(o_done + 8 * tile, (n - 1) & 1, flags);
       if (group_or(bar_id, BM, !ok)) break;                // all four warps leave, or none
       tc_after();
       bad = group_or(bar_id, BM, bad);
       if (bad) {
-        l = quiet_nan();
+        l = off = quiet_nan();
         if (r == 0) flags[0] = 1;
       }
       const bool whole = g.j0 == 0 && g.j1 == g.nblk;
       if (whole) {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float inv = l == 0.0f ? 0.0f : 1.0f / (l + off);
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           uint32_t o[32];
           tm_ld32(O_COL + tile * 128 + lane_at + 32 * i, o);
-          tc_wait_ld();
+          tc_wait_ld(o);
           if (have) {
             uint4* const dst = (uint4*)(A.out + ((size_t)row * A.q_heads + hq) * D + 32 * i);
 #pragma unroll
@@ -728,16 +786,17 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         if (have) {
           __stcg(dst + r, M);
           __stcg(dst + BM + r, l);
+          __stcg(dst + 2 * BM + r, off);
         }
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
           uint32_t o[32];
           tm_ld32(O_COL + tile * 128 + lane_at + 32 * i, o);
-          tc_wait_ld();
+          tc_wait_ld(o);
           if (have) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              __stcg((float4*)(dst + 2 * BM) + (8 * i + e) * BM + r,
+              __stcg((float4*)(dst + 3 * BM) + (8 * i + e) * BM + r,
                      make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
           }
         }
@@ -751,36 +810,76 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           __threadfence();
           if (r == 0) A.counters[c0 * MT + tile] = 0;
           const int rows = min(A.tile_tokens, max(0, g.ntok - tile * A.tile_tokens)) * A.group;
-          for (int i = r; i < rows * (D / 4); i += BM) {
-            const int d4 = i / rows, rr = i - d4 * rows;
-            float top = -INFINITY;
+          // weight of every partial, left where its reference was
+          float top = -INFINITY, sum = 0.0f, fix = 0.0f;
+          if (r < rows) {
             bool nan = false;
+#pragma unroll 4
             for (int x = c0; x <= c1; ++x) {
-              const float m = __ldcg(part(x, x == c0) + rr);
+              const float m = __ldcg(part(x, x == c0) + r);
               nan |= isnan(m);
               top = fmaxf(top, m);
             }
             const float ref = top == -INFINITY ? 0.0f : top;
-            float sum = nan ? quiet_nan() : 0.0f;
-            float4 o = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int x = c0; x <= c1; ++x) {
+              float* const p = part(x, x == c0);
+              const float f = ex2(__ldcg(p + r) - ref);
+              sum += f * __ldcg(p + BM + r);
+              fix += f * __ldcg(p + 2 * BM + r);
+            }
+            const float inv = nan ? quiet_nan() : sum == 0.0f ? 0.0f : 1.0f / (sum + fix);
+#pragma unroll 4
+            for (int x = c0; x <= c1; ++x) {
+              float* const p = part(x, x == c0);
+              __stcg(p + r, ex2(__ldcg(p + r) - ref) * inv);
+            }
+            const int rt = r / A.group;
+            if (A.lse)
+              A.lse[(size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + r - rt * A.group] =
+                  nan ? quiet_nan() : (top + log2f(sum)) * LN2_F;
+          }
+          group_sync(bar_id, BM);
+          constexpr int U = 8;                             // quadruples of a thread in flight
+          const int all = rows * (D / 4);
+          for (int i0 = r; i0 < all; i0 += BM * U) {
+            float4 o[U];
+            int at[U], rr[U];
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+              const int i = min(i0 + q * BM, all - 1), d4 = i / rows;
+              rr[q] = i - d4 * rows;
+              at[q] = d4;
+              o[q] = make_float4(0, 0, 0, 0);
+            }
             for (int x = c0; x <= c1; ++x) {
               const float* const p = part(x, x == c0);
-              const float f = ex2(__ldcg(p + rr) - ref);
-              const float4 y = __ldcg((const float4*)(p + 2 * BM) + d4 * BM + rr);
-              sum += f * __ldcg(p + BM + rr);
-              o.x += f * y.x; o.y += f * y.y; o.z += f * y.z; o.w += f * y.w;
+              float f[U];
+              float4 y[U];
+#pragma unroll
+              for (int q = 0; q < U; ++q) {
+                f[q] = __ldcg(p + rr[q]);
+                y[q] = __ldcg((const float4*)(p + 3 * BM) + at[q] * BM + rr[q]);
+              }
+#pragma unroll
+              for (int q = 0; q < U; ++q) {
+                o[q].x += f[q] * y[q].x; o[q].y += f[q] * y[q].y; o[q].z += f[q] * y[q].z; o[q].w += f[q] * y[q].w;
+              }
             }
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-            const int rt = rr / A.group, rh = rr - rt * A.group;
-            const size_t at = (size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + rh;
-            *(uint2*)(A.out + at * D + 4 * d4) = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-            if (A.lse && d4 == 0) A.lse[at] = (top + log2f(sum)) * LN2_F;
+#pragma unroll
+            for (int q = 0; q < U; ++q) {
+              if (i0 + q * BM >= all) break;
+              const int rt = rr[q] / A.group;
+              const size_t to = (size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + rr[q] - rt * A.group;
+              *(uint2*)(A.out + to * D + 4 * at[q]) = make_uint2(pack_bf16(o[q].x, o[q].y), pack_bf16(o[q].z, o[q].w));
+            }
           }
         }
       }
       tc_before();
     }
-  } else if constexpr (C::FP8) if (busy && warp >= C::CONV_WARP0) {
+    }
+  } else if constexpr (C::FP8) if (busy) {
     // ---------------------------------------------- e4m3 codes to f16 blocks
     // A code is exact in f16, and so is its product with 2^(e_j - e), e the
     // largest exponent among the block's vectors, unless the vector is 2^15
