@@ -92,6 +92,24 @@ __device__ __noinline__ bool bar_wait_slow(uint32_t a, unsigned parity, int* fla
 __device__ __forceinline__ bool bar_wait(uint32_t a, unsigned parity, int* flags) {
   return __all_sync(FULL, bar_try(a, parity)) || bar_wait_slow(a, parity, flags);
 }
+// The same for a thread on its own
+__device__ __noinline__ bool bar_wait_slow1(uint32_t a, unsigned parity, int* flags) {
+  for (int it = 0; it < POLLS; ++it) {
+    if (bar_try(a, parity)) return true;
+    if ((it & 255) == 255 && *(volatile int*)&flags[1]) return false;
+  }
+  atomicExch(&flags[1], 1);
+  return false;
+}
+__device__ __forceinline__ bool bar_wait1(uint32_t a, unsigned parity, int* flags) {
+  return bar_try(a, parity) || bar_wait_slow1(a, parity, flags);
+}
+// One lane of a converged warp, the same one every time; the compiler knows that only one is active
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* m, int x, int y, uint32_t bar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
                ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(bar) : "memory");
@@ -139,6 +157,7 @@ __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t* r) {
                ::I8(r, 0), I8(r, 8), "r"(a) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
+__device__ __forceinline__ float max3(float a, float b, float c) { float y; asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c)); return y; }
 typedef unsigned long long u64;
 __device__ __forceinline__ u64 pk(float lo, float hi) { u64 r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi)); return r; }
 __device__ __forceinline__ void upk(u64 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
@@ -465,106 +484,89 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     }
     } else if (busy && warp == 1) {
     // -------------------------------------------------------------- products
-    unsigned n = 0;                                        // blocks whose scores have been issued
-    unsigned m = 0;                                        // blocks whose products with the values have been issued
-    unsigned segs = 0;
-    bool ok = true;
-    const bool one = lane == 0;
-    auto scores = [&](int tile, uint32_t s_at, unsigned i) {   // S = Q K^T of block i
-      if (one) {
-        const uint32_t kb = k_at + (i % NK) * C::BUF, qb = q_at + tile * C::BUF;
+      if (elect_one()) {
+        unsigned n = 0;                                    // blocks whose scores have been issued
+        unsigned m = 0;                                    // blocks whose products with the values have been issued
+        unsigned segs = 0;
+        bool ok = true;
+        auto scores = [&](int tile, uint32_t s_at, unsigned i) {   // S = Q K^T of block i
+          const uint64_t kd = smem_desc(k_at + (i % NK) * C::BUF, 16), qd = smem_desc(q_at + tile * C::BUF, 16);
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const uint32_t off = (x / 4) * HALF_BYTES + (x % 4) * 32;
-          mma_ss(s_at, smem_desc(qb + off, 16), smem_desc(kb + off, 16), ID_QK, x > 0);
-        }
-      }
-    };
-    auto values = [&](int tile, uint32_t p_at, unsigned i, bool acc) {   // O (+)= P V of block i
-      if (one) {
-        const uint32_t vb = v_at + (i % NV) * C::BUF;
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t off = ((x / 4) * HALF_BYTES + (x % 4) * 32) >> 4;
+            mma_ss(s_at, qd + off, kd + off, ID_QK, x > 0);
+          }
+        };
+        auto values = [&](int tile, uint32_t p_at, unsigned i, bool acc) {   // O (+)= P V of block i
+          const uint64_t vd = smem_desc(v_at + (i % NV) * C::BUF, HALF_BYTES);
 #pragma unroll
-        for (int x = 0; x < BN / 16; ++x)
-          mma_ts(O_COL + tile * 128, p_at + (x / 2) * 32 + (x % 2) * 8, smem_desc(vb + x * 16 * 128, HALF_BYTES), ID_PV, acc || x > 0);
-      }
-    };
-    auto wait_k = [&](unsigned i) { return bar_wait(k_full + 8 * (i % NK), (i / NK) & 1, flags); };
-    auto wait_v = [&](unsigned i, int valid) {
-      if (!bar_wait(v_full + 8 * (i % NV), (i / NV) & 1, flags)) return false;
-      if (!C::FP8 && valid < BN) {
-        // slots past the sequence's end may hold anything; a weight of 0 does not clear NaN
-        uint8_t* const vb = gbase + (v_at - base) + (i % NV) * C::BUF;
-        for (int x = 0; x < C::HALVES; ++x)
-          for (int o = max(valid, 0) * 128 + lane * 16; o < HALF_BYTES; o += 512) *(uint4*)(vb + x * HALF_BYTES + o) = make_uint4(0, 0, 0, 0);
-        fence_async();
-        __syncwarp();
-      }
-      return true;
-    };
-    while (ok && W.next(A, tile_rows, g)) {
-      const int nb = g.j1 - g.j0;
-      if (!(ok = bar_wait(q_full, segs++ & 1, flags))) break;
-      tc_after();
-      if constexpr (MT == 2) {
-        if (!(ok = wait_k(n))) break;
-        for (int tile = 0; tile < 2; ++tile) {
-          scores(tile, S_COL + tile * 128, n);
-          if (one) tc_commit(s_full + 8 * tile);
-        }
-        if (one) tc_commit(k_empty + 8 * (n % NK));
-        ++n;
-        for (int j = 0; j < nb && ok; ++j, ++m) {
-          if (!(ok = wait_v(m, g.kv - (g.j0 + j) * BN))) break;
-          const bool more = j + 1 < nb;
-          for (int tile = 0; tile < 2 && ok; ++tile) {
-            if (!(ok = bar_wait(p_full + 8 * tile, m & 1, flags))) break;
+          for (int x = 0; x < BN / 16; ++x)
+            mma_ts(O_COL + tile * 128, p_at + (x / 2) * 32 + (x % 2) * 8, vd + ((x * 16 * 128) >> 4), ID_PV, acc || x > 0);
+        };
+        auto wait_k = [&](unsigned i) { return bar_wait1(k_full + 8 * (i % NK), (i / NK) & 1, flags); };
+        auto wait_v = [&](unsigned i) { return bar_wait1(v_full + 8 * (i % NV), (i / NV) & 1, flags); };
+        while (ok && W.next(A, tile_rows, g)) {
+          const int nb = g.j1 - g.j0;
+          const bool split = two_parts<KIND>(g);
+          if (!(ok = bar_wait1(q_full, segs++ & 1, flags))) break;
+          if constexpr (MT == 2) {
+            if (!(ok = wait_k(n))) break;
             tc_after();
-            values(tile, S_COL + tile * 128, m, j > 0);
-            if (two_parts<KIND>(g)) values(tile, S_COL + tile * 128 + 16, m, true);
-            if (one) tc_commit(o_done + 8 * tile);
-            if (more) {
-              if (tile == 0 && !(ok = wait_k(n))) break;
+            for (int tile = 0; tile < 2; ++tile) {
+              scores(tile, S_COL + tile * 128, n);
+              tc_commit(s_full + 8 * tile);
+            }
+            tc_commit(k_empty + 8 * (n % NK));
+            ++n;
+            for (int j = 0; j < nb && ok; ++j, ++m) {
+              const bool more = j + 1 < nb;
+              if (!(ok = wait_v(m) && (!more || wait_k(n)))) break;
+#pragma unroll
+              for (int tile = 0; tile < 2; ++tile) {
+                if (!(ok = bar_wait1(p_full + 8 * tile, m & 1, flags))) break;
+                tc_after();
+                values(tile, S_COL + tile * 128, m, j > 0);
+                if (split) values(tile, S_COL + tile * 128 + 16, m, true);
+                if (more) {
+                  scores(tile, S_COL + tile * 128, n);     // in order behind the product that reads its weights
+                  tc_commit(s_full + 8 * tile);            // and so a sign that this product is done
+                } else {
+                  tc_commit(o_done + 8 * tile);
+                }
+              }
+              if (!ok) break;
+              tc_commit(v_empty + 8 * (m % NV));
+              if (more) {
+                tc_commit(k_empty + 8 * (n % NK));
+                ++n;
+              }
+            }
+          } else {
+            auto issue = [&]() {
+              if (!wait_k(n)) return false;
               tc_after();
-              scores(tile, S_COL + tile * 128, n);         // in order behind the product that reads its weights
-              if (one) tc_commit(s_full + 8 * tile);
+              scores(0, S_COL + (n & 1) * 128, n);
+              tc_commit(s_full + 8 * (n & 1));
+              tc_commit(k_empty + 8 * (n % NK));
+              ++n;
+              return true;
+            };
+            ok = issue() && (nb < 2 || issue());
+            for (int j = 0; j < nb && ok; ++j, ++m) {
+              if (!(ok = wait_v(m) && bar_wait1(p_full + 8 * (m & 1), (m >> 1) & 1, flags))) break;
+              tc_after();
+              values(0, S_COL + (m & 1) * 128, m, j > 0);
+              if (split) values(0, S_COL + (m & 1) * 128 + 16, m, true);
+              tc_commit(o_done);
+              tc_commit(v_empty + 8 * (m % NV));
+              if (j + 2 < nb) ok = issue();
             }
           }
-          if (!ok) break;
-          if (one) tc_commit(v_empty + 8 * (m % NV));
-          if (more) {
-            if (one) tc_commit(k_empty + 8 * (n % NK));
-            ++n;
-          }
         }
-      } else {
-        auto issue = [&]() {
-          if (!wait_k(n)) return false;
-          tc_after();
-          scores(0, S_COL + (n & 1) * 128, n);
-          if (one) {
-            tc_commit(s_full + 8 * (n & 1));
-            tc_commit(k_empty + 8 * (n % NK));
-          }
-          ++n;
-          return true;
-        };
-        ok = issue() && (nb < 2 || issue());
-        for (int j = 0; j < nb && ok; ++j, ++m) {
-          if (!(ok = bar_wait(p_full + 8 * (m & 1), (m >> 1) & 1, flags)) || !(ok = wait_v(m, g.kv - (g.j0 + j) * BN))) break;
-          tc_after();
-          values(0, S_COL + (m & 1) * 128, m, j > 0);
-          if (two_parts<KIND>(g)) values(0, S_COL + (m & 1) * 128 + 16, m, true);
-          if (one) {
-            tc_commit(o_done);
-            tc_commit(v_empty + 8 * (m % NV));
-          }
-          if (j + 2 < nb) ok = issue();
-        }
+        tc_commit(drain);                                  // products and arrivals in flight end before the CTA does
+        for (int it = 0; it < POLLS && !bar_try(drain, 0); ++it) {}
       }
-    }
-    if (one) tc_commit(drain);                             // products and arrivals in flight end before the CTA does
-    __syncwarp();
-    for (int it = 0; it < POLLS && !bar_try(drain, 0); ++it) {}
+      __syncwarp();
     }
   } else if (warp < C::CONV_WARP0) {
     if (busy) {
@@ -574,7 +576,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     const uint32_t lane_at = (uint32_t)(warp & 3) << 21;   // 32 lanes a warp, lane number in bits 16..31
     const int bar_id = 1 + tile;
     const int tok = r / A.group, head_in = r - tok * A.group;
-    unsigned n = 0;                                        // blocks done
+    unsigned n = 0, segs = 0;                              // blocks and runs done
     bool ok = true;
     while (W.next(A, tile_rows, g)) {
       const int tk = tile * A.tile_tokens + tok;           // token of the item
@@ -652,7 +654,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 #pragma unroll
           for (int i = 0; i < 32; i += 8)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], fmaxf(__uint_as_float(x[i + e]), __uint_as_float(x[i + 4 + e])));
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + 4 + e]));
         };
         tm_ld32(s_at, xa);
         tc_wait_ld(xa);
@@ -671,9 +673,12 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         if (j == g.j0) {
           M = top;
         } else if (__any_sync(FULL, top > M + LAZY)) {
-          // raise the reference; the block before must have been added to O
-          if (!(ok = bar_wait(o_done + 8 * tile, (n - 1) & 1, flags))) break;
-          tc_after();
+          // Raise the reference.  The block before must have been added to O; with two tiles its product
+          // was issued ahead of these scores.
+          if (MT == 1) {
+            if (!(ok = bar_wait(o_done, (n - 1) & 1, flags))) break;
+            tc_after();
+          }
           const float up = fmaxf(M, top), f = up == -INFINITY ? 1.0f : ex2(M - up);
           M = up;
           l *= f;
@@ -687,6 +692,17 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
             tm_st32(O_COL + tile * 128 + lane_at + 32 * i, o);
           }
+        }
+        if (!C::FP8 && tile == 0 && (j + 1) * BN > g.kv) {
+          // slots past the sequence's end may hold anything, and a weight of 0 does not clear NaN:
+          // thread r clears value row r
+          if (!(ok = bar_wait(v_full + 8 * (n % NV), (n / NV) & 1, flags))) break;
+          if (j * BN + r >= g.kv) {
+            uint8_t* const line = gbase + (v_at - base) + (n % NV) * C::BUF + r * 128;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) *(uint4*)(line + (i / 8) * HALF_BYTES + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async();
         }
         const float neg = ev - (M == -INFINITY ? 0.0f : M);
         const u64 c2 = pk(cb, cb), n2 = pk(neg, neg);
@@ -748,8 +764,9 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       // weight of each block, which is the one that can.
       // With two score buffers of one tile, the last two products may both be on their way, and a wait
       // for a phase must not start two phases ahead of the barrier.
-      if (MT == 1 && ok && n >= 2) ok = bar_wait(o_done + 8 * tile, (n - 2) & 1, flags);
-      if (ok) ok = bar_wait(o_done + 8 * tile, (n - 1) & 1, flags);
+      if (MT == 1 && ok && n >= 2) ok = bar_wait(o_done, (n - 2) & 1, flags);
+      if (ok) ok = bar_wait(o_done + 8 * tile, (MT == 2 ? segs : n - 1) & 1, flags);
+      ++segs;
       if (group_or(bar_id, BM, !ok)) break;                // all four warps leave, or none
       tc_after();
       bad = group_or(bar_id, BM, bad);
