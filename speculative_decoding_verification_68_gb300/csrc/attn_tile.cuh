@@ -21,9 +21,10 @@
 // the order of arrival.
 //
 // Roles of a CTA's warps: one copies key and value blocks into shared memory
-// (TMA), one issues the matrix products, groups of four do the softmax, one
-// thread per row.  For an e4m3 cache four more turn the codes into f16 (see
-// below).
+// (TMA), one issues the matrix products, two load the query rows of the next
+// run, and eight per tile do the softmax, two threads a row (a warp reaches
+// only the 32 tensor-memory lanes of its place in its warpgroup).  For an e4m3
+// cache eight more turn the codes into f16 (see below).
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -81,7 +82,7 @@ __device__ __forceinline__ bool bar_try(uint32_t a, unsigned parity) {
 // Bounded wait of a whole warp: false (and the handle flagged) instead of a
 // hang, in all lanes or in none.  Once one wait has given up the others see
 // the flag and give up within 256 polls.
-__device__ __noinline__ bool bar_wait_slow(uint32_t a, unsigned parity, int* flags) {
+__device__ __forceinline__ bool bar_wait_slow(uint32_t a, unsigned parity, int* flags) {
   for (int it = 0; it < POLLS; ++it) {
     if (__all_sync(FULL, bar_try(a, parity))) return true;
     if ((it & 255) == 255 && __any_sync(FULL, *(volatile int*)&flags[1])) return false;
@@ -93,7 +94,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t a, unsigned parity, int* flags
   return __all_sync(FULL, bar_try(a, parity)) || bar_wait_slow(a, parity, flags);
 }
 // The same for a thread on its own
-__device__ __noinline__ bool bar_wait_slow1(uint32_t a, unsigned parity, int* flags) {
+__device__ __forceinline__ bool bar_wait_slow1(uint32_t a, unsigned parity, int* flags) {
   for (int it = 0; it < POLLS; ++it) {
     if (bar_try(a, parity)) return true;
     if ((it & 255) == 255 && *(volatile int*)&flags[1]) return false;
@@ -147,10 +148,10 @@ __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t* r) {
                "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
                : R8(r, 0), R8(r, 8), R8(r, 16), R8(r, 24) : "r"(a));
 }
-__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-               "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};"
-               ::I8(r, 0), I8(r, 8), I8(r, 16), I8(r, 24), "r"(a) : "memory");
+__device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : R8(r, 0), R8(r, 8) : "r"(a));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : P8(r, 0), P8(r, 8)::"memory");
 }
 __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};"
@@ -248,8 +249,8 @@ struct Segment {      // a run of blocks of one item
   int kv;             // cached tokens
   int lim0;           // keys the tile's first token sees (causal) or kv
   int j0, j1, nblk;   // blocks of this run, of the item
+  int bad, more;      // invalid sequence; another run of this CTA follows
   long long start;    // unit index of the item's first block
-  bool bad;
 };
 
 // Rounding the weights to bf16 costs little where many keys share the error.
@@ -276,6 +277,7 @@ struct Walker {
     g.start = u - j;
     g.bad = s.bad;
     u += g.j1 - g.j0;
+    g.more = u < u1;
     j = 0;
     if (u < u1 && ++t == s.tiles) {
       t = 0;
@@ -297,37 +299,51 @@ struct Cfg {
   static constexpr int QBYTES = MT * BUF;
   static constexpr int RAW = BN * D;                          // a block of codes
   static constexpr int NRAW = FP8 ? (D == 128 ? 4 : 8) : 0;
-  static constexpr int SMALL = 1024;                          // barriers and bookkeeping, behind the buffers
-  static constexpr int NBUF = FP8 ? (D == 128 ? 4 : 6) : (SMEM_LIMIT - 1024 - SMALL - QBYTES) / BUF;
+  static constexpr int SMALL = 3072;                          // barriers and bookkeeping, behind the buffers
+  static constexpr int NBUF = FP8 ? (D == 128 ? 4 : 6) : (SMEM_LIMIT - SMALL - QBYTES) / BUF;
   static constexpr int NK = (NBUF + 1) / 2, NV = NBUF / 2;
-  static constexpr int SMEM = 1024 + QBYTES + NBUF * BUF + NRAW * RAW + SMALL;   // 1024: alignment of the base
-  static constexpr int SOFT_WARP0 = 4;
-  static constexpr int CONV_WARP0 = SOFT_WARP0 + 4 * MT;
-  static constexpr int CONV_WARPS = FP8 ? 4 : 0;
+  static constexpr int SMEM = QBYTES + NBUF * BUF + NRAW * RAW + SMALL;
+  static constexpr int Q_WARP0 = 2, Q_WARPS = 2;
+  static constexpr int SOFT_WARP0 = 4, SOFT_WARPS = 8;        // per tile
+  static constexpr int CONV_WARP0 = SOFT_WARP0 + SOFT_WARPS * MT;
+  static constexpr int CONV_WARPS = FP8 ? 8 : 0;
   static constexpr int WARPS = CONV_WARP0 + CONV_WARPS;
   static constexpr int THREADS = WARPS * 32;
+  // Registers: five warpgroups start with 96 each; the first one, which copies and issues, gives up
+  // what the softmax needs to hold half a row of scores.
+  static constexpr int REGS_SOFT = MT == 2 ? 104 : 0, REGS_WORK = 64;
+  static_assert(REGS_SOFT == 0 || 128 * REGS_WORK + SOFT_WARPS * MT * 32 * REGS_SOFT <= THREADS * 96, "register split");
   static constexpr int INFO = 8;                              // ring of block references (more than NK + 1)
 };
+// named barriers: pairs of softmax warps of a quarter of a tile's rows, tiles, converting warps
+enum { BAR_PAIR = 1, BAR_TILE = 9, BAR_CONV = 11 };
 
 template <int D, int KIND, int MT>
 __global__ void __launch_bounds__(Cfg<D, KIND, MT>::THREADS, 1)
-sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant__ CUtensorMap map_q,
+                    const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   using C = Cfg<D, KIND, MT>;
   constexpr int NK = C::NK, NV = C::NV, NT = C::THREADS;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t base = (saddr(smem_raw) + 1023) & ~1023u;
-  uint8_t* const gbase = smem_raw + (base - saddr(smem_raw));
+  extern __shared__ __align__(1024) uint8_t gbase[];
+  const uint32_t base = saddr(gbase);
   const uint32_t q_at = base, k_at = q_at + C::QBYTES, v_at = k_at + NK * C::BUF, raw_at = v_at + NV * C::BUF;
   uint8_t* const small = gbase + (raw_at - base) + C::NRAW * C::RAW;
   const uint32_t bars = saddr(small);
   // barriers, 8 bytes each
   const uint32_t k_full = bars, k_empty = k_full + 8 * NK, v_full = k_empty + 8 * NK, v_empty = v_full + 8 * NV,
                  raw_full = v_empty + 8 * NV, raw_empty = raw_full + 8 * C::NRAW, s_full = raw_empty + 8 * C::NRAW,
-                 p_full = s_full + 16, o_done = p_full + 16, q_full = o_done + 16, drain = q_full + 8;
-  static_assert(8 * (2 * NK + 2 * NV + 2 * C::NRAW + 8) <= 320, "barrier area");
-  int* const work = (int*)(small + 320);                  // tensor-memory base, plan, merge flags
-  float2* const info = (float2*)(small + 448);            // block references of an e4m3 cache [INFO]
-  int* const red = (int*)(small + 512);                   // planning and reductions
+                 p_full = s_full + 16,
+                 o_done = p_full + 16,   // a run's last product, per tile; with one tile, also every product (second barrier)
+                 q_full = o_done + 16, q_empty = q_full + 8, drain = q_empty + 8;
+  static_assert(8 * (2 * NK + 2 * NV + 2 * C::NRAW + 9) <= 320, "barrier area");
+  int* const work = (int*)(small + 320);                  // tensor-memory base, plan, merge flags [16]
+  float2* const info = (float2*)(small + 384);            // block references of an e4m3 cache [INFO]
+  int* const red = (int*)(small + 448);                   // planning (20 sums of 8 bytes), then the converters' maxima
+  Segment* const runs = (Segment*)(small + 768);          // runs as the query warps announce them [4]
+  static_assert(sizeof(Segment) <= 64, "ring of runs");
+  float* const swap = (float*)(small + 1024);             // [tile][half][row]: between the two threads of a row
+  float* const q_scale = (float*)(small + 2048);          // [2][row]: powers of two taken out of query rows (e4m3)
+  static_assert(!C::FP8 || MT == 1, "the second tile's part of swap lies over q_scale");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile_rows = MT * A.tile_tokens;
@@ -338,8 +354,9 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     for (int i = 0; i < NK; ++i) { bar_init(k_full + 8 * i, C::FP8 ? C::CONV_WARPS : 1); bar_init(k_empty + 8 * i, 1); }
     for (int i = 0; i < NV; ++i) { bar_init(v_full + 8 * i, C::FP8 ? C::CONV_WARPS : 1); bar_init(v_empty + 8 * i, 1); }
     for (int i = 0; i < C::NRAW; ++i) { bar_init(raw_full + 8 * i, 1); bar_init(raw_empty + 8 * i, C::CONV_WARPS); }
-    for (int i = 0; i < 2; ++i) { bar_init(s_full + 8 * i, 1); bar_init(p_full + 8 * i, 4); bar_init(o_done + 8 * i, 1); }
-    bar_init(q_full, 4 * MT);
+    for (int i = 0; i < 2; ++i) { bar_init(s_full + 8 * i, 1); bar_init(p_full + 8 * i, C::SOFT_WARPS); bar_init(o_done + 8 * i, 1); }
+    bar_init(q_full, C::FP8 ? C::Q_WARPS : 1);
+    bar_init(q_empty, 1);
     bar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -347,7 +364,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(work)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  long long* const red64 = (long long*)red;               // [0..15] warp sums, [16] running base
+  long long* const red64 = (long long*)red;
   long long mine = 0;
   for (int b = tid; b < A.B.n_seqs; b += NT) {
     const Seq s = load_seq(A.B, b, tile_rows);
@@ -394,17 +411,10 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       }
       const long long end = below + scan, begin = end - mine;
       if (begin <= W.u && W.u < end) {
-        const Seq s = load_seq(A.B, b, tile_rows);
-        const long long per = mine / A.kv_heads, at = W.u - begin, r = at % per;
-        int lo = 0, hi = s.tiles;                         // tile: largest t with tiles_before(t) <= r
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (tiles_before(s, mid, tile_rows, A.causal) <= r) lo = mid; else hi = mid;
-        }
+        const unsigned per = (unsigned)(mine / A.kv_heads), at = (unsigned)(W.u - begin);
         work[1] = b;
         work[2] = (int)(at / per);
-        work[3] = lo;
-        work[4] = (int)(r - tiles_before(s, lo, tile_rows, A.causal));
+        work[3] = (int)(at % per);
       }
       before += chunk;
       if (before > W.u) break;                            // uniform
@@ -416,8 +426,18 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   const uint32_t tmem = (uint32_t)work[0];
   const bool busy = W.u < W.u1;
   if (busy) {
-    W.b = work[1]; W.head = work[2]; W.t = work[3]; W.j = work[4];
+    W.b = work[1]; W.head = work[2];
     W.begin(A, tile_rows);
+    const int r = work[3];                                // unit within the head: its tile and block
+    for (int t = tid; t < W.s.tiles; t += NT) {
+      const long long lo = tiles_before(W.s, t, tile_rows, A.causal);
+      if (lo <= r && r < lo + tile_blocks(W.s, t, tile_rows, A.causal)) {
+        work[4] = t;
+        work[5] = (int)(r - lo);
+      }
+    }
+    __syncthreads();
+    W.t = work[4]; W.j = work[5];
   }
   // tensor memory: scores (and weights over them) at 0 and 128, outputs at 256 and 384
   const uint32_t S_COL = tmem, O_COL = tmem + 256;
@@ -426,6 +446,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   Segment g;
 
   if (warp < C::SOFT_WARP0) {
+    if constexpr (C::REGS_SOFT > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_WORK));
     if (busy && warp == 0) {
     // ---------------------------------------------------------------- copies
     const int ps = 1 << A.B.page_shift, ppb = BN >> A.B.page_shift;
@@ -517,6 +538,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               tc_commit(s_full + 8 * tile);
             }
             tc_commit(k_empty + 8 * (n % NK));
+            if (nb == 1) tc_commit(q_empty);
             ++n;
             for (int j = 0; j < nb && ok; ++j, ++m) {
               const bool more = j + 1 < nb;
@@ -538,16 +560,19 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               tc_commit(v_empty + 8 * (m % NV));
               if (more) {
                 tc_commit(k_empty + 8 * (n % NK));
+                if (j + 2 == nb) tc_commit(q_empty);
                 ++n;
               }
             }
           } else {
+            int left = nb;
             auto issue = [&]() {
               if (!wait_k(n)) return false;
               tc_after();
               scores(0, S_COL + (n & 1) * 128, n);
               tc_commit(s_full + 8 * (n & 1));
               tc_commit(k_empty + 8 * (n % NK));
+              if (--left == 0) tc_commit(q_empty);
               ++n;
               return true;
             };
@@ -557,7 +582,8 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               tc_after();
               values(0, S_COL + (m & 1) * 128, m, j > 0);
               if (split) values(0, S_COL + (m & 1) * 128 + 16, m, true);
-              tc_commit(o_done);
+              tc_commit(o_done + 8);
+              if (j + 1 == nb) tc_commit(o_done);
               tc_commit(v_empty + 8 * (m % NV));
               if (j + 2 < nb) ok = issue();
             }
@@ -567,140 +593,163 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         for (int it = 0; it < POLLS && !bar_try(drain, 0); ++it) {}
       }
       __syncwarp();
-    }
-  } else if (warp < C::CONV_WARP0) {
-    if (busy) {
-    // --------------------------------------------------------------- softmax
-    const int tile = MT == 2 ? (warp - C::SOFT_WARP0) >> 2 : 0;
-    const int r = tid & 127;                               // row of the tile, lane of tensor memory
-    const uint32_t lane_at = (uint32_t)(warp & 3) << 21;   // 32 lanes a warp, lane number in bits 16..31
-    const int bar_id = 1 + tile;
-    const int tok = r / A.group, head_in = r - tok * A.group;
-    unsigned n = 0, segs = 0;                              // blocks and runs done
-    bool ok = true;
-    while (W.next(A, tile_rows, g)) {
-      const int tk = tile * A.tile_tokens + tok;           // token of the item
-      const bool have = tok < A.tile_tokens && tk < g.ntok;
-      const int row = g.row0 + tk, hq = g.head * A.group + head_in;
-      const int lim = A.causal ? g.lim0 + tk : g.kv;
-      // -- query rows to shared memory, in f16 normalised by a power of two for an e4m3 cache
-      float c = A.c;
-      {
-        uint4 x[D / 8];
-        const uint4* const src = (const uint4*)(A.Q.ptr + row * A.Q.st + hq * A.Q.sh);
+    } else if (busy) {
+      // ------------------------------------------------------------ query rows
+      // The rows of the next run, as soon as the scores of this one are all done.
+      unsigned segs = 0;
+      bool ok = true;
+      if constexpr (!C::FP8) {
+        const int used = A.tile_tokens * A.group;          // rows of a tile: floor(128 / group) tokens, the same box every time
+        if (warp == C::Q_WARP0) {
+          for (int i = lane; i < MT * C::HALVES * (BM - used) * 8; i += 32) {   // the rest never changes
+            const int o = i % ((BM - used) * 8), x = i / ((BM - used) * 8);
+            *(uint4*)(gbase + x * HALF_BYTES + used * 128 + o * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_async();
+          __syncwarp();
+          if (elect_one()) {
+            while (W.next(A, tile_rows, g)) {
+              if (!bar_wait1(q_empty, (segs & 1) ^ 1, flags)) break;
+              runs[segs & 3] = g;                          // the softmax is at most two runs behind
+              bar_expect(q_full, MT * C::HALVES * used * 128);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = have ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-        if constexpr (C::FP8) {
-          uint32_t top = 0;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+              for (int i = 0; i < MT * C::HALVES; ++i)
+                tma_3d(q_at + i * HALF_BYTES, &map_q, (i % C::HALVES) * 64, g.head * A.group, g.row0 + (i / C::HALVES) * A.tile_tokens, q_full);
+              ++segs;
+            }
+            if (segs > 0 && *(volatile int*)&flags[1])     // given up somewhere: let the last copy land
+              for (int it = 0; it < 4096 && !bar_try(q_full, (segs - 1) & 1); ++it) {}
+          }
+          __syncwarp();
+        }
+      } else {
+        // as f16, normalised by a power of two: 16 bytes a thread, the threads of a row together
+        constexpr int LR = D / 8, RP = C::Q_WARPS * 32 / LR;   // threads of a row, rows a pass
+        const int t = tid - C::Q_WARP0 * 32, ch = t % LR;
+        while (ok && W.next(A, tile_rows, g)) {
+          if (!(ok = bar_wait(q_empty, (segs & 1) ^ 1, flags))) break;
+          uint8_t* const q = gbase + (ch / 8) * HALF_BYTES;
+          if (t == 0) runs[segs & 3] = g;                  // the softmax is at most two runs behind
+#pragma unroll 8
+          for (int r0 = 0; r0 < BM; r0 += RP) {
+            const int r = r0 + t / LR, tok = r / A.group, head_in = r - tok * A.group;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (tok < min(A.tile_tokens, g.ntok))
+              x = __ldg((const uint4*)(A.Q.ptr + (g.row0 + tok) * A.Q.st + (g.head * A.group + head_in) * A.Q.sh) + ch);
+            uint32_t w[4] = {x.x, x.y, x.z, x.w}, top = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
-          }
-          // largest magnitude in [1, 2): f16 holds it exactly, and what is 2^-14 of it or more
-          const int e = top >= 0x7f80u ? 0 : min(max((int)(top >> 7), 7), 247) - EXP_BIAS;
-          const float f = __int_as_float((EXP_BIAS - e) << 23);
-          c *= __int_as_float((EXP_BIAS + e) << 23);
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            for (int o = LR / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(FULL, top, o));
+            // largest magnitude in [1, 2): f16 holds it exactly, and what is 2^-14 of it or more
+            const int e = top >= 0x7f80u ? 0 : min(max((int)(top >> 7), 7), 247) - EXP_BIAS;
+            const float f = __int_as_float((EXP_BIAS - e) << 23);
+            if (ch == 0) q_scale[(segs & 1) * BM + r] = __int_as_float((EXP_BIAS + e) << 23);
 #pragma unroll
-            for (int e2 = 0; e2 < 4; ++e2) w[e2] = pack_f16(bf_lo(w[e2]) * f, bf_hi(w[e2]) * f);
-            x[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 4; ++i) w[i] = pack_f16(bf_lo(w[i]) * f, bf_hi(w[i]) * f);
+            *(uint4*)(q + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          fence_async();
+          __syncwarp();
+          if (lane == 0) bar_arrive(q_full);
+          ++segs;
         }
-        uint8_t* const q = gbase + (q_at - base) + tile * C::BUF + r * 128;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) *(uint4*)(q + (i / 8) * HALF_BYTES + (((i % 8) ^ (r & 7)) << 4)) = x[i];
       }
-      fence_async();
-      tc_before();
-      __syncwarp();
-      if (lane == 0) bar_arrive(q_full);
-      // -- pages of this run that do not exist
-      bool bad = g.bad;
-      if (KIND != KIND_PACKED) {
-        const int used = (g.kv + (1 << A.B.page_shift) - 1) >> A.B.page_shift, ppb = BN >> A.B.page_shift;
-        for (int p = g.j0 * ppb + r; p < min(g.j1 * ppb, used); p += BM)
-          bad |= (unsigned)__ldg(A.B.table + (size_t)g.b * A.B.max_pages + p) >= (unsigned)A.B.num_pages;
-      }
-      // -- blocks
-      float M = -INFINITY, l = 0.0f, off = 0.0f;
-      for (int j = g.j0; j < g.j1; ++j, ++n) {
-        const unsigned buf = MT == 2 ? tile : n & 1, ph = MT == 2 ? n & 1 : (n >> 1) & 1;
-        const uint32_t s_at = S_COL + buf * 128 + lane_at;
-        if (!(ok = bar_wait(s_full + 8 * buf, ph, flags))) break;
+    }
+  } else if (warp < C::CONV_WARP0) {
+    if constexpr (C::REGS_SOFT > 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SOFT));
+    if (busy) {
+    // --------------------------------------------------------------- softmax
+    const int sw = warp - C::SOFT_WARP0, tile = MT == 2 ? sw >> 3 : 0, half = (sw >> 2) & 1;
+    const int r = (warp & 3) * 32 + lane;                  // row of the tile, lane of tensor memory
+    const uint32_t lane_at = (uint32_t)(warp & 3) << 21;   // 32 lanes a warp, lane number in bits 16..31
+    const int pair = BAR_PAIR + tile * 4 + (warp & 3), group_bar = BAR_TILE + tile;
+    constexpr int NS = C::SOFT_WARPS * 32;                 // threads of a tile
+    const int ts = half * BM + r;                          // among them
+    float* const to_pair = swap + (tile * 2 + half) * BM + r;
+    const float* const from_pair = swap + (tile * 2 + (half ^ 1)) * BM + r;
+    const int tok = r / A.group, head_in = r - tok * A.group;
+    const int tk = tile * A.tile_tokens + tok;             // token of the item
+    constexpr int DH = D / 2;                              // output columns of this thread
+    const uint32_t o_at = O_COL + tile * 128 + lane_at + half * DH;
+    unsigned n = 0, segs = 0;                              // blocks and runs done
+    bool ok = true;
+    do {
+      auto wait_scores = [&]() {                           // a wait that gives up takes all to the exits below
+        if (ok) ok = MT == 2 ? bar_wait(s_full + 8 * tile, n & 1, flags) : bar_wait(s_full + 8 * (n & 1), (n >> 1) & 1, flags);
         tc_after();
-        const int rel = lim - j * BN;                      // keys of the block this row sees
+      };
+      wait_scores();
+      if (group_or(group_bar, NS, !ok)) break;             // all warps of the tile leave, or none
+      const Segment& g = runs[segs & 3];                   // announced before its first scores
+      const int j0 = g.j0, j1 = g.j1, lim = A.causal ? g.lim0 + tk : g.kv;
+      float c = A.c;
+      float M = -INFINITY, l = 0.0f, off = 0.0f;
+      for (int j = j0; j < j1; ++j, ++n) {
+        const unsigned buf = MT == 2 ? tile : n & 1;
+        const uint32_t s_at = S_COL + buf * 128 + lane_at + half * 64;
+        if (j > j0) wait_scores();
+        uint32_t x[64];
+        tm_ld32(s_at, x);
+        tm_ld32(s_at + 32, x + 32);
         float cb = c, ev = 0.0f;
         if constexpr (C::FP8) {
           const float2 t = info[n % C::INFO];
+          if (j == j0) c *= q_scale[(segs & 1) * BM + r];
           cb = fmaxf(c * t.x, 1.17549435e-38f);              // a masked score's -inf times 0 would be NaN
           ev = t.y;
         }
-        // The row is read twice, 32 scores at a time (once for the maximum, once for the weights), so
-        // that it needs no 128 registers; the next 32 are on their way while these are worked on.
-        uint32_t xa[32], xb[32];
+        tc_wait_ld(x);
+        tc_wait_ld(x + 32);
+        const int rel = lim - j * BN - half * 64;          // keys of this half that the row sees
+        if (rel < 64) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i) x[i] = i < rel ? x[i] : 0xff800000u;
+        }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        auto mask = [&](uint32_t* x, int h) {
-          if (rel < BN) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = 32 * h + i < rel ? x[i] : 0xff800000u;
-          }
-        };
-        auto maximum = [&](uint32_t* x, int h) {
-          mask(x, h);
+        for (int i = 0; i < 64; i += 8)
 #pragma unroll
-          for (int i = 0; i < 32; i += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + 4 + e]));
-        };
-        tm_ld32(s_at, xa);
-        tc_wait_ld(xa);
-        tm_ld32(s_at + 32, xb);
-        maximum(xa, 0);
-        tc_wait_ld(xb);
-        tm_ld32(s_at + 64, xa);
-        maximum(xb, 1);
-        tc_wait_ld(xa);
-        tm_ld32(s_at + 96, xb);
-        maximum(xa, 2);
-        tc_wait_ld(xb);
-        tm_ld32(s_at, xa);
-        maximum(xb, 3);
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + 4 + e]));
         const float best = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), top = fmaf(best, cb, ev);
-        if (j == g.j0) {
-          M = top;
-        } else if (__any_sync(FULL, top > M + LAZY)) {
-          // Raise the reference.  The block before must have been added to O; with two tiles its product
-          // was issued ahead of these scores.
-          if (MT == 1) {
-            if (!(ok = bar_wait(o_done, (n - 1) & 1, flags))) break;
-            tc_after();
+        if (group_or(pair, 64, j == j0 || top > M + LAZY || !ok)) {
+          // Set or raise the reference, the same for both threads of the row.
+          *to_pair = top;
+          group_sync(pair, 64);
+          const float up = fmaxf(fmaxf(M, top), *from_pair);
+          if (j > j0) {
+            // The block before must have been added to O; with two tiles its product was issued ahead of
+            // these scores.
+            if (MT == 1) {
+              if (ok) ok = bar_wait(o_done + 8, (n - 1) & 1, flags);
+              tc_after();
+            }
+            const float f = up == -INFINITY ? 1.0f : ex2(M - up);
+            l *= f;
+            off *= f;
+#pragma unroll 1
+            for (int i = 0; i < DH; i += 16) {             // few at a time: the scores hold most registers
+              uint32_t o[16];
+              tm_ld16(o_at + i, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tm_st16(o_at + i, o);
+            }
           }
-          const float up = fmaxf(M, top), f = up == -INFINITY ? 1.0f : ex2(M - up);
           M = up;
-          l *= f;
-          off *= f;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            uint32_t o[32];
-            tm_ld32(O_COL + tile * 128 + lane_at + 32 * i, o);
-            tc_wait_ld(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tm_st32(O_COL + tile * 128 + lane_at + 32 * i, o);
-          }
+          if (group_or(pair, 64, !ok)) { ok = false; break; }   // both have read; both leave, or none
         }
         if (!C::FP8 && tile == 0 && (j + 1) * BN > g.kv) {
           // slots past the sequence's end may hold anything, and a weight of 0 does not clear NaN:
-          // thread r clears value row r
-          if (!(ok = bar_wait(v_full + 8 * (n % NV), (n / NV) & 1, flags))) break;
-          if (j * BN + r >= g.kv) {
+          // the threads of row r clear value row r
+          ok = bar_wait(v_full + 8 * (n % NV), (n / NV) & 1, flags);
+          if (ok && j * BN + r >= g.kv) {
             uint8_t* const line = gbase + (v_at - base) + (n % NV) * C::BUF + r * 128;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) *(uint4*)(line + (i / 8) * HALF_BYTES + (i % 8) * 16) = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < D / 16; ++i) {
+              const int ch = half * (D / 16) + i;
+              *(uint4*)(line + (ch / 8) * HALF_BYTES + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
+            }
           }
           fence_async();
         }
@@ -710,47 +759,37 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const bool split = two_parts<KIND>(g);
         // exponentials, their sum, and the weights in 16 bits in place of their scores: 32 scores become 16
         // columns of weights and 16 of what rounding left of them
-        auto weights = [&](uint32_t* x, int h) {
-          mask(x, h);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
           uint32_t w[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float a, b;
-            upk(fma2(pk(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), c2, n2), a, b);
+            upk(fma2(pk(__uint_as_float(x[32 * h + 2 * i]), __uint_as_float(x[32 * h + 2 * i + 1])), c2, n2), a, b);
             a = ex2(a);
             b = ex2(b);
             acc[i & 1] = add2(acc[i & 1], pk(a, b));
             w[i] = C::FP8 ? pack_f16(a, b) : pack_bf16(a, b);
             if (!C::FP8) {
-              x[2 * i] = __float_as_uint(a);
-              x[2 * i + 1] = __float_as_uint(b);
+              x[32 * h + 2 * i] = __float_as_uint(a);
+              x[32 * h + 2 * i + 1] = __float_as_uint(b);
             }
           }
           tm_st16(s_at + 32 * h, w);
           if (!C::FP8 && split) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(__uint_as_float(x[2 * i]) - bf_lo(w[i]), __uint_as_float(x[2 * i + 1]) - bf_hi(w[i]));
+            for (int i = 0; i < 16; ++i)
+              w[i] = pack_bf16(__uint_as_float(x[32 * h + 2 * i]) - bf_lo(w[i]), __uint_as_float(x[32 * h + 2 * i + 1]) - bf_hi(w[i]));
             tm_st16(s_at + 32 * h + 16, w);
           }
-        };
-        tc_wait_ld(xa);
-        tm_ld32(s_at + 32, xb);
-        weights(xa, 0);
-        tc_wait_ld(xb);
-        tm_ld32(s_at + 64, xa);
-        weights(xb, 1);
-        tc_wait_ld(xa);
-        tm_ld32(s_at + 96, xb);
-        weights(xa, 2);
-        tc_wait_ld(xb);
-        weights(xb, 3);
+        }
         float s0, s1, s2, s3;
         upk(acc[0], s0, s1);
         upk(acc[1], s2, s3);
         const float add = (s0 + s1) + (s2 + s3);
         l += C::FP8 ? add * __int_as_float((EXP_BIAS - (int)ev) << 23) : add;
         if (!C::FP8 && !split) {
-          // what rounding to bf16 did to the block's largest weight (see the run's result)
+          // what rounding to bf16 did to the largest of these weights (see the run's result)
           const float p = ex2(fmaf(best, cb, neg));
           off += __bfloat162float(__float2bfloat16(p)) - p;
         }
@@ -761,29 +800,40 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       }
       // -- the run's result.  Dividing by the sum of the rounded weights would cancel the rounding of a
       // key that dominates its row, where it does not average out; off corrects the sum for the largest
-      // weight of each block, which is the one that can.
-      // With two score buffers of one tile, the last two products may both be on their way, and a wait
-      // for a phase must not start two phases ahead of the barrier.
-      if (MT == 1 && ok && n >= 2) ok = bar_wait(o_done, (n - 2) & 1, flags);
-      if (ok) ok = bar_wait(o_done + 8 * tile, (MT == 2 ? segs : n - 1) & 1, flags);
+      // weight of each half block, which are the ones that can.
+      bool bad = g.bad != 0;
+      if (KIND != KIND_PACKED) {                           // pages of this run that do not exist
+        const int used = (g.kv + (1 << A.B.page_shift) - 1) >> A.B.page_shift, ppb = BN >> A.B.page_shift;
+        for (int p = g.j0 * ppb + ts; p < min(g.j1 * ppb, used); p += NS)
+          bad |= (unsigned)__ldg(A.B.table + (size_t)g.b * A.B.max_pages + p) >= (unsigned)A.B.num_pages;
+      }
+      if (ok) ok = bar_wait(o_done + 8 * tile, segs & 1, flags);
       ++segs;
-      if (group_or(bar_id, BM, !ok)) break;                // all four warps leave, or none
+      if (group_or(group_bar, NS, !ok)) break;             // all warps of the tile leave, or none
       tc_after();
-      bad = group_or(bar_id, BM, bad);
+      *to_pair = l;
+      bad = group_or(group_bar, NS, bad);
+      l += *from_pair;
+      group_sync(pair, 64);
+      *to_pair = off;
+      group_sync(pair, 64);
+      off += *from_pair;
+      group_sync(pair, 64);
       if (bad) {
         l = off = quiet_nan();
-        if (r == 0) flags[0] = 1;
+        if (ts == 0) flags[0] = 1;
       }
-      const bool whole = g.j0 == 0 && g.j1 == g.nblk;
-      if (whole) {
+      const bool have = tok < A.tile_tokens && tk < g.ntok;
+      if (g.j0 == 0 && g.j1 == g.nblk) {
+        const size_t at = (size_t)(g.row0 + tk) * A.q_heads + g.head * A.group + head_in;
         const float inv = l == 0.0f ? 0.0f : 1.0f / (l + off);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
+        for (int i = 0; i < DH / 32; ++i) {
           uint32_t o[32];
-          tm_ld32(O_COL + tile * 128 + lane_at + 32 * i, o);
+          tm_ld32(o_at + 32 * i, o);
           tc_wait_ld(o);
           if (have) {
-            uint4* const dst = (uint4*)(A.out + ((size_t)row * A.q_heads + hq) * D + 32 * i);
+            uint4* const dst = (uint4*)(A.out + at * D + half * DH + 32 * i);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t w[4];
@@ -794,81 +844,82 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             }
           }
         }
-        if (A.lse && have) A.lse[(size_t)row * A.q_heads + hq] = (M + log2f(l)) * LN2_F;
+        if (A.lse && have && half == 0) A.lse[at] = (M + log2f(l)) * LN2_F;
       } else {
         // partial: slot 1 of this CTA holds an item's beginning, slot 0 a later part
         constexpr int PART = part_floats<D>();
         auto part = [&](int cta, int slot) { return A.ws + ((size_t)(cta * 2 + slot) * MT + tile) * PART; };
         float* const dst = part(blockIdx.x, g.j0 == 0 ? 1 : 0);
-        if (have) {
+        if (have && half == 0) {
           __stcg(dst + r, M);
           __stcg(dst + BM + r, l);
           __stcg(dst + 2 * BM + r, off);
         }
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
+        for (int i = 0; i < DH / 32; ++i) {
           uint32_t o[32];
-          tm_ld32(O_COL + tile * 128 + lane_at + 32 * i, o);
+          tm_ld32(o_at + 32 * i, o);
           tc_wait_ld(o);
           if (have) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              __stcg((float4*)(dst + 3 * BM) + (8 * i + e) * BM + r,
+              __stcg((float4*)(dst + 3 * BM) + (half * (DH / 4) + 8 * i + e) * BM + r,
                      make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
           }
         }
         // runs that hold the item: CTA x has units [units x / ctas, units (x + 1) / ctas)
         const int c0 = (int)(((g.start + 1) * ctas - 1) / units), c1 = (int)(((g.start + g.nblk) * ctas - 1) / units);
         __threadfence();
-        group_sync(bar_id, BM);
-        if (r == 0) work[8 + tile] = atomicAdd(A.counters + c0 * MT + tile, 1) == c1 - c0;
-        group_sync(bar_id, BM);
+        group_sync(group_bar, NS);
+        if (ts == 0) work[8 + tile] = atomicAdd(A.counters + c0 * MT + tile, 1) == c1 - c0;
+        group_sync(group_bar, NS);
         if (work[8 + tile]) {                              // the last to finish
           __threadfence();
-          if (r == 0) A.counters[c0 * MT + tile] = 0;
+          if (ts == 0) A.counters[c0 * MT + tile] = 0;
           const int rows = min(A.tile_tokens, max(0, g.ntok - tile * A.tile_tokens)) * A.group;
           // weight of every partial, left where its reference was
-          float top = -INFINITY, sum = 0.0f, fix = 0.0f;
-          if (r < rows) {
+          if (ts < rows) {
+            float m_top = -INFINITY, sum = 0.0f, fix = 0.0f;
             bool nan = false;
 #pragma unroll 4
             for (int x = c0; x <= c1; ++x) {
-              const float m = __ldcg(part(x, x == c0) + r);
+              const float m = __ldcg(part(x, x == c0) + ts);
               nan |= isnan(m);
-              top = fmaxf(top, m);
+              m_top = fmaxf(m_top, m);
             }
-            const float ref = top == -INFINITY ? 0.0f : top;
-#pragma unroll 4
+            const float ref = m_top == -INFINITY ? 0.0f : m_top;
+#pragma unroll 2
             for (int x = c0; x <= c1; ++x) {
               float* const p = part(x, x == c0);
-              const float f = ex2(__ldcg(p + r) - ref);
-              sum += f * __ldcg(p + BM + r);
-              fix += f * __ldcg(p + 2 * BM + r);
+              const float f = ex2(__ldcg(p + ts) - ref);
+              sum += f * __ldcg(p + BM + ts);
+              fix += f * __ldcg(p + 2 * BM + ts);
             }
             const float inv = nan ? quiet_nan() : sum == 0.0f ? 0.0f : 1.0f / (sum + fix);
 #pragma unroll 4
             for (int x = c0; x <= c1; ++x) {
               float* const p = part(x, x == c0);
-              __stcg(p + r, ex2(__ldcg(p + r) - ref) * inv);
+              __stcg(p + ts, ex2(__ldcg(p + ts) - ref) * inv);
             }
-            const int rt = r / A.group;
+            const int rt = ts / A.group;
             if (A.lse)
-              A.lse[(size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + r - rt * A.group] =
-                  nan ? quiet_nan() : (top + log2f(sum)) * LN2_F;
+              A.lse[(size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + ts - rt * A.group] =
+                  nan ? quiet_nan() : (m_top + log2f(sum)) * LN2_F;
           }
-          group_sync(bar_id, BM);
-          constexpr int U = 8;                             // quadruples of a thread in flight
+          group_sync(group_bar, NS);
+          constexpr int U = 4;                             // quadruples of a thread in flight, of two partials
           const int all = rows * (D / 4);
-          for (int i0 = r; i0 < all; i0 += BM * U) {
+          for (int i0 = ts; i0 < all; i0 += NS * U) {
             float4 o[U];
             int at[U], rr[U];
 #pragma unroll
             for (int q = 0; q < U; ++q) {
-              const int i = min(i0 + q * BM, all - 1), d4 = i / rows;
+              const int i = min(i0 + q * NS, all - 1), d4 = i / rows;
               rr[q] = i - d4 * rows;
-              at[q] = d4;
+              at[q] = d4 * BM + rr[q];
               o[q] = make_float4(0, 0, 0, 0);
             }
+#pragma unroll 2
             for (int x = c0; x <= c1; ++x) {
               const float* const p = part(x, x == c0);
               float f[U];
@@ -876,7 +927,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 #pragma unroll
               for (int q = 0; q < U; ++q) {
                 f[q] = __ldcg(p + rr[q]);
-                y[q] = __ldcg((const float4*)(p + 3 * BM) + at[q] * BM + rr[q]);
+                y[q] = __ldcg((const float4*)(p + 3 * BM) + at[q]);
               }
 #pragma unroll
               for (int q = 0; q < U; ++q) {
@@ -885,16 +936,17 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             }
 #pragma unroll
             for (int q = 0; q < U; ++q) {
-              if (i0 + q * BM >= all) break;
+              if (i0 + q * NS >= all) break;
               const int rt = rr[q] / A.group;
               const size_t to = (size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + rr[q] - rt * A.group;
-              *(uint2*)(A.out + to * D + 4 * at[q]) = make_uint2(pack_bf16(o[q].x, o[q].y), pack_bf16(o[q].z, o[q].w));
+              *(uint2*)(A.out + to * D + 4 * (at[q] / BM)) = make_uint2(pack_bf16(o[q].x, o[q].y), pack_bf16(o[q].z, o[q].w));
             }
           }
         }
       }
       tc_before();
-    }
+      if (!g.more) break;
+    } while (true);
     }
   } else if constexpr (C::FP8) if (busy) {
     // ---------------------------------------------- e4m3 codes to f16 blocks
@@ -905,18 +957,19 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     // values the reference M covers s_ij + e, so a weight times a block value
     // stays within range whatever the vectors' sizes.  e of the values is kept
     // within 2^64 of the run's largest so that the weights do not vanish.
-    const int t = tid - C::CONV_WARP0 * 32, cw = warp - C::CONV_WARP0;
+    // Two threads a key: raw lines are swizzled like the f16 ones, so that eight
+    // threads of eight keys reach eight different 16-byte columns.
+    const int t = tid - C::CONV_WARP0 * 32, key = t & 127, part = t >> 7;
     constexpr int NTC = C::CONV_WARPS * 32;
-    static_assert(NTC == BN, "one converting thread per key");
-    uint8_t* const bytes = small + 704;                    // scale bytes of the block: keys, then values
-    int* const wmax = red + 4;                             // maxima per warp
+    static_assert(NTC == 2 * BN, "two converting threads per key");
+    int2* const wmax = (int2*)red;                         // [2][4]: maxima per quarter of the keys
     unsigned n = 0, raw = 0;
     bool ok = true, stop = false;
     while (!stop && W.next(A, tile_rows, g)) {
       const int32_t* const tab = A.B.table + (size_t)g.b * A.B.max_pages;
       int run = EV_MIN;
-      auto load_bytes = [&](int j) {                       // this thread's key: bytes of key and value (0: none)
-        const int p = j * BN + t;
+      auto load_bytes = [&](int j) {                       // scale bytes of this thread's key and value (0: none)
+        const int p = j * BN + key;
         if (p >= g.kv) return make_int2(0, 0);
         const int page = __ldg(tab + (p >> A.B.page_shift));
         if ((unsigned)page >= (unsigned)A.B.num_pages) return make_int2(0, 0);
@@ -928,46 +981,44 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const int2 cur = nxt;
         if (j + 1 < g.j1) nxt = load_bytes(j + 1);
         const int ka = __reduce_max_sync(FULL, cur.x == BYTE_NAN ? 0 : cur.x), va = __reduce_max_sync(FULL, cur.y == BYTE_NAN ? 0 : cur.y);
-        // the block before has read its bytes; all four warps leave, or none
-        if ((stop = group_or(3, NTC, !ok))) break;
-        bytes[t] = (uint8_t)cur.x;
-        bytes[BN + t] = (uint8_t)cur.y;
-        if (lane == 0) { wmax[cw] = ka; wmax[4 + cw] = va; }
-        group_sync(3, NTC);
+        int2* const wm = wmax + (n & 1) * 4;
+        if (lane == 0 && part == 0) wm[warp & 3] = make_int2(ka, va);
+        if ((stop = group_or(BAR_CONV, NTC, !ok))) break;  // all warps leave, or none
         int eb[2];
-        eb[0] = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])) - EXP_BIAS;
-        eb[1] = max(max(max(wmax[4], wmax[5]), max(wmax[6], wmax[7])) - EXP_BIAS, run - 64);
-        eb[0] = max(eb[0], EXP_MIN);
+        eb[0] = max(max(max(wm[0].x, wm[1].x), max(wm[2].x, wm[3].x)) - EXP_BIAS, EXP_MIN);
+        eb[1] = max(max(max(wm[0].y, wm[1].y), max(wm[2].y, wm[3].y)) - EXP_BIAS, run - 64);
         run = max(run, eb[1]);
         eb[1] = max(eb[1], run - 64);
         if (t == 0) info[n % C::INFO] = make_float2(__int_as_float((eb[0] + EXP_BIAS) << 23), (float)eb[1]);
-        const int valid = g.kv - j * BN;
+        const bool valid = key < g.kv - j * BN;
 #pragma unroll
         for (int kv = 0; kv < 2 && ok; ++kv, ++raw) {
           const unsigned rs = raw % C::NRAW, ring = kv ? NV : NK, bs = n % ring;
           const uint32_t full = (kv ? v_full : k_full) + 8 * bs, empty = (kv ? v_empty : k_empty) + 8 * bs;
+          const int by = kv ? cur.y : cur.x, d = by == BYTE_NAN ? 0 : by - EXP_BIAS - eb[kv];   // <= 0
+          const uint32_t f1 = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u, f = f1 | (f1 << 16);
           if (!(ok = bar_wait(raw_full + 8 * rs, (raw / C::NRAW) & 1, flags)) || !(ok = bar_wait(empty, ((n / ring) & 1) ^ 1, flags))) break;
-          const uint8_t* const src = gbase + (raw_at - base) + rs * C::RAW;
-          uint8_t* const dst = gbase + ((kv ? v_at : k_at) - base) + bs * C::BUF;
-          constexpr int CH = BN * D / 16;                  // 16-code chunks of the block
-#pragma unroll 4
-          for (int i = t; i < CH; i += NTC) {
-            const int key = i / (D / 16), ch = i % (D / 16);
-            const uint4 x = *(const uint4*)(src + i * 16);
-            const int by = bytes[kv * BN + key];
-            const int d = by == BYTE_NAN ? 0 : by - EXP_BIAS - eb[kv];        // <= 0
-            const uint32_t f1 = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u;
-            const uint32_t f = f1 | (f1 << 16);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          const uint8_t* const src = gbase + (raw_at - base) + rs * C::RAW + key * D;
+          uint8_t* const dst = gbase + ((kv ? v_at : k_at) - base) + bs * C::BUF + key * 128;
+          constexpr int CH = D / 32;                       // 16-code chunks of this thread
+          uint4 xs[CH];
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int ch = part * CH + i;
+            xs[i] = *(const uint4*)(src + ((D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4));
+          }
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int ch = part * CH + i, c0 = (ch % 4) * 2;
+            const uint32_t w[4] = {xs[i].x, xs[i].y, xs[i].z, xs[i].w};
             uint32_t y[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const uint32_t hcode = e4m3_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
               asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(hcode), "r"(f));
-              if (key >= valid) y[e] = 0;
+              if (!valid) y[e] = 0;                        // slots past the end may hold anything
             }
-            uint8_t* const line = dst + (ch / 4) * HALF_BYTES + key * 128;
-            const int c0 = (ch % 4) * 2;
+            uint8_t* const line = dst + (ch / 4) * HALF_BYTES;
             *(uint4*)(line + ((c0 ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
             *(uint4*)(line + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
           }

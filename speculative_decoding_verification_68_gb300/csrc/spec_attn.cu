@@ -251,17 +251,20 @@ static bool map_pool(CUtensorMap* m, const spec_attn_ctx* h, const spec_attn_poo
   const cuuint64_t strides[1] = {(cuuint64_t)h->D * (e4m3 ? 1 : 2)};
   const cuuint32_t box[2] = {(cuuint32_t)(e4m3 ? h->D : 64), (cuuint32_t)p->page_size}, step[2] = {1, 1};
   return encode_tiled()(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, step,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 && h->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// Packed rows [token, head, D], 128 tokens of one head and 64 columns a box
-static bool map_rows(CUtensorMap* m, const spec_attn_ctx* h, const Rows& r, int n_tokens) {
-  const cuuint64_t dims[3] = {(cuuint64_t)h->D, (cuuint64_t)h->kv_heads, (cuuint64_t)n_tokens};
+// Packed rows [token, head, D]; a box of `tokens` tokens of `box_heads` heads and 64 columns
+static bool map_rows(CUtensorMap* m, int D, int heads, const Rows& r, int n_tokens, int box_heads, int tokens) {
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)n_tokens};
   // a dimension of one element has no stride worth the name
-  const cuuint64_t strides[2] = {(cuuint64_t)(h->kv_heads > 1 ? r.sh : h->D) * 2, (cuuint64_t)(n_tokens > 1 ? r.st : (long long)h->D * h->kv_heads) * 2};
-  const cuuint32_t box[3] = {64, 1, BN}, step[3] = {1, 1, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? r.sh : D) * 2, (cuuint64_t)(n_tokens > 1 ? r.st : (long long)D * heads) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)tokens}, step[3] = {1, 1, 1};
   return encode_tiled()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void*)r.ptr, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+static bool map_queries(CUtensorMap* m, const spec_attn_ctx* h, const AttnParams& A) {
+  return map_rows(m, h->D, h->q_heads, A.Q, A.B.n_tokens, A.group, A.tile_tokens);
 }
 template <int D, int KIND, int MT>
 static bool allow_smem() {
@@ -272,8 +275,8 @@ static bool allow_smem_all() {
   return allow_smem<D, KIND_BF16, 1>() && allow_smem<D, KIND_BF16, 2>() && allow_smem<D, KIND_E4M3, 1>() && allow_smem<D, KIND_PACKED, 2>();
 }
 template <int D, int KIND, int MT>
-static int launch_attention(const spec_attn_ctx* h, const AttnParams& A, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
-  sa_attention_kernel<D, KIND, MT><<<h->n_sm, Cfg<D, KIND, MT>::THREADS, Cfg<D, KIND, MT>::SMEM, s>>>(A, mk, mv);
+static int launch_attention(const spec_attn_ctx* h, const AttnParams& A, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
+  sa_attention_kernel<D, KIND, MT><<<h->n_sm, Cfg<D, KIND, MT>::THREADS, Cfg<D, KIND, MT>::SMEM, s>>>(A, mq, mk, mv);
   return launched();
 }
 static AttnParams attn_params(const spec_attn_ctx* h, const Batch& B, const Rows& Q, int causal, float scale, void* out, float* lse) {
@@ -331,15 +334,16 @@ extern "C" int spec_attn_chunk(spec_attn_t h, const spec_attn_pool* pool, const 
   const cudaStream_t s = (cudaStream_t)cuda_stream;
   const Batch B = batch_of(h, batch, pool);
   AttnParams A = attn_params(h, B, rows_of(q), causal, scale, out, lse);
-  CUtensorMap mk, mv;
+  CUtensorMap mq, mk, mv;
+  if (!map_queries(&mq, h, A)) return SV_ERR_ARG;
   if (!map_pool(&mk, h, pool, pool->k) || !map_pool(&mv, h, pool, pool->v)) return SV_ERR_CUDA;
   if (pool->dtype == SV_E4M3) {
     A.ks = pool->k_scale; A.vs = pool->v_scale;
-    return h->D == 128 ? launch_attention<128, KIND_E4M3, 1>(h, A, mk, mv, s) : launch_attention<64, KIND_E4M3, 1>(h, A, mk, mv, s);
+    return h->D == 128 ? launch_attention<128, KIND_E4M3, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E4M3, 1>(h, A, mq, mk, mv, s);
   }
   const bool two = (long long)B.n_tokens * A.group > (long long)B.n_seqs * BM;   // more rows per sequence and head than one tile holds
-  if (h->D == 128) return two ? launch_attention<128, KIND_BF16, 2>(h, A, mk, mv, s) : launch_attention<128, KIND_BF16, 1>(h, A, mk, mv, s);
-  return two ? launch_attention<64, KIND_BF16, 2>(h, A, mk, mv, s) : launch_attention<64, KIND_BF16, 1>(h, A, mk, mv, s);
+  if (h->D == 128) return two ? launch_attention<128, KIND_BF16, 2>(h, A, mq, mk, mv, s) : launch_attention<128, KIND_BF16, 1>(h, A, mq, mk, mv, s);
+  return two ? launch_attention<64, KIND_BF16, 2>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_BF16, 1>(h, A, mq, mk, mv, s);
 }
 
 extern "C" int spec_attn_prompt(spec_attn_t h, int n_seqs, int n_tokens, const int32_t* cu,
@@ -356,9 +360,11 @@ extern "C" int spec_attn_prompt(spec_attn_t h, int n_seqs, int n_tokens, const i
   const spec_attn_batch batch = {cu, nullptr, nullptr, n_seqs, n_tokens, 0};
   const Batch B = batch_of(h, &batch, nullptr);
   const AttnParams A = attn_params(h, B, rows_of(q), 1, scale, out, lse);
-  CUtensorMap mk, mv;
-  if (!map_rows(&mk, h, rows_of(k), n_tokens) || !map_rows(&mv, h, rows_of(v), n_tokens)) return SV_ERR_ARG;
-  return h->D == 128 ? launch_attention<128, KIND_PACKED, 2>(h, A, mk, mv, s) : launch_attention<64, KIND_PACKED, 2>(h, A, mk, mv, s);
+  CUtensorMap mq, mk, mv;
+  if (!map_queries(&mq, h, A) || !map_rows(&mk, h->D, h->kv_heads, rows_of(k), n_tokens, 1, BN) ||
+      !map_rows(&mv, h->D, h->kv_heads, rows_of(v), n_tokens, 1, BN))
+    return SV_ERR_ARG;
+  return h->D == 128 ? launch_attention<128, KIND_PACKED, 2>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_PACKED, 2>(h, A, mq, mk, mv, s);
 }
 
 extern "C" int spec_attn_get_error(spec_attn_t h) {
