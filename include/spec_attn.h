@@ -109,7 +109,7 @@ int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_ba
  * (causal != 0) or 0 .. kv_len[b] - 1 (causal == 0: draft steps that attend
  * only to target-written entries pass the length of those; "Optimizing
  * speculative decoding", section "IndexShare and KVShare").
- *   out [n_tokens, q_heads, head_dim] contiguous bf16: sum_j softmax(scale * q.k_j) v_j
+ *   out [n_tokens, q_heads, head_dim] contiguous bf16, 32-byte aligned: sum_j softmax(scale * q.k_j) v_j
  *   lse [n_tokens, q_heads] fp32 or NULL: ln sum_j exp(scale * q.k_j)
  * A row that sees nothing gets out = 0 and lse = -inf.  scale > 0, finite.
  * One kernel launch; single tokens and chunks of any length. */

@@ -191,8 +191,8 @@ class SpecAttention:
                 out["lse"] = torch.empty((n, self.q_heads), dtype=torch.float32, device=self.device)
             return out
         _check(out.get("out"), "output out", torch.bfloat16, (n, self.q_heads, self.head_dim), self.device)
-        if out["out"].data_ptr() % 16:
-            raise ValueError("output out must be 16-byte aligned")
+        if out["out"].data_ptr() % 32:
+            raise ValueError("output out must be 32-byte aligned")
         if out.get("lse") is not None:
             _check(out["lse"], "output lse", torch.float32, (n, self.q_heads), self.device)
         elif want_lse:

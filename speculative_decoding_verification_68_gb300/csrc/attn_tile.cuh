@@ -12,10 +12,13 @@
 // tile of 128 rows holds floor(128 / group) tokens times the group and every
 // key block is read once for all of them.
 //
-// Work.  An item is (sequence, key-value head, row tile); its units are the
-// 128-key blocks that any of its rows sees.  The units of all items in order
-// are cut into equal runs, one per CTA (one CTA per SM), so few long
-// sequences fill the GPU as well as many short ones.  An item that lies in
+// Work.  An item is (sequence, key-value head, row tile); it costs a unit for
+// each 128-key block that any of its rows sees, and SETUP units that stand for
+// what an item costs besides (its query rows, its first scores, its output).
+// The units of all items in order are cut into equal runs, one per CTA (one CTA
+// per SM), so few long sequences fill the GPU as well as many short ones.  A cut
+// within SNAP units of an item's end moves there: splitting an item has a price
+// too.  An item that lies in
 // several runs leaves partial (M, l, O) in the workspace and the last CTA to
 // finish merges them, in order: nothing waits, and results do not depend on
 // the order of arrival.
@@ -46,7 +49,9 @@ constexpr int HALF_BYTES = BN * 128;  // 64 of the D columns of a block: 128 row
 constexpr float LAZY = 8.0f;        // log2 of how far scores may pass the reference
 constexpr int POLLS = 1 << 18;      // of a bounded wait (about 1 s)
 constexpr int SMEM_LIMIT = 232448;
-constexpr int MIN_RUN = 2;          // units of a CTA at least
+constexpr int SETUP = 3;            // units of an item besides its blocks
+constexpr int SNAP = 3;             // units that a run gives up or takes on to end with an item (SETUP at least)
+constexpr int MIN_RUN = 3;          // units of a CTA at least
 constexpr int EV_MIN = -100;        // least exponent of a value block's reference (see convert)
 
 struct AttnParams {
@@ -119,6 +124,15 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x
   asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
+#define R8(r, o) "=r"((r)[o]), "=r"((r)[o + 1]), "=r"((r)[o + 2]), "=r"((r)[o + 3]), "=r"((r)[o + 4]), "=r"((r)[o + 5]), "=r"((r)[o + 6]), "=r"((r)[o + 7])
+#define I8(r, o) "r"((r)[o]), "r"((r)[o + 1]), "r"((r)[o + 2]), "r"((r)[o + 3]), "r"((r)[o + 4]), "r"((r)[o + 5]), "r"((r)[o + 6]), "r"((r)[o + 7])
+__device__ __forceinline__ void prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(m), "r"(x), "r"(y), "r"(z) : "memory");
+}
+// 32 bytes, a whole memory sector
+__device__ __forceinline__ void st_32(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), I8(w, 0) : "memory");
+}
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -135,8 +149,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
                ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
 }
-#define R8(r, o) "=r"((r)[o]), "=r"((r)[o + 1]), "=r"((r)[o + 2]), "=r"((r)[o + 3]), "=r"((r)[o + 4]), "=r"((r)[o + 5]), "=r"((r)[o + 6]), "=r"((r)[o + 7])
-#define I8(r, o) "r"((r)[o]), "r"((r)[o + 1]), "r"((r)[o + 2]), "r"((r)[o + 3]), "r"((r)[o + 4]), "r"((r)[o + 5]), "r"((r)[o + 6]), "r"((r)[o + 7])
 #define P8(r, o) "+r"((r)[o]), "+r"((r)[o + 1]), "+r"((r)[o + 2]), "+r"((r)[o + 3]), "+r"((r)[o + 4]), "+r"((r)[o + 5]), "+r"((r)[o + 6]), "+r"((r)[o + 7])
 // Waits for this thread's loads; the registers pass through, so that no use of them moves before it
 __device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
@@ -228,13 +240,13 @@ __device__ __forceinline__ int tile_blocks(const Seq& s, int t, int tile_rows, i
   const int len = causal ? s.kv - s.n + min(s.n, (t + 1) * tile_rows) : s.kv;
   return max(1, (len + BN - 1) / BN);
 }
-// key blocks of tiles 0 .. t-1
+// units of tiles 0 .. t-1
 __device__ inline long long tiles_before(const Seq& s, int t, int tile_rows, int causal) {
   if (t == 0) return 0;
-  if (!causal) return (long long)t * tile_blocks(s, 0, tile_rows, causal);
-  long long last = 0;
+  if (!causal) return (long long)t * (SETUP + tile_blocks(s, 0, tile_rows, causal));
+  long long last = (long long)t * SETUP;
   if (t == s.tiles) {                   // the last tile may be short
-    last = tile_blocks(s, t - 1, tile_rows, causal);
+    last += tile_blocks(s, t - 1, tile_rows, causal);
     if (--t == 0) return last;
   }
   const int base = s.kv - s.n;          // tile i (from 1) ends at key base + i * tile_rows
@@ -250,42 +262,44 @@ struct Segment {      // a run of blocks of one item
   int lim0;           // keys the tile's first token sees (causal) or kv
   int j0, j1, nblk;   // blocks of this run, of the item
   int bad, more;      // invalid sequence; another run of this CTA follows
-  long long start;    // unit index of the item's first block
+  long long start;    // unit of the item's first block
 };
 
 // Rounding the weights to bf16 costs little where many keys share the error.
-// An item whose rows see one block of keys at most has its weights in two bf16
-// parts and takes the product with the values twice.
-template <int KIND> __device__ __forceinline__ bool two_parts(const Segment& g) { return KIND != KIND_E4M3 && g.nblk == 1; }
+// An item of few blocks has its weights in two bf16 parts and takes the product
+// with the values twice.
+template <int KIND> __device__ __forceinline__ bool two_parts(const Segment& g) { return KIND != KIND_E4M3 && g.nblk <= 3; }
 
-// Walks one CTA's units.  Every role walks on its own.
+// Walks one CTA's run of units.  Every role walks on its own.
 struct Walker {
-  long long u, u1;
-  int b, head, t, j;
+  long long at, u0, u1;   // first unit of the item, the run
+  int b, head, t;
   Seq s;
-  __device__ void begin(const AttnParams& A, int tile_rows) { s = load_seq(A.B, b, tile_rows); }
-  __device__ bool next(const AttnParams& A, int tile_rows, Segment& g) {
-    if (u >= u1) return false;
-    g.b = b; g.head = head;
-    g.row0 = s.row0 + t * tile_rows;
-    g.ntok = min(tile_rows, s.n - t * tile_rows);
-    g.kv = s.kv;
-    g.lim0 = A.causal ? s.kv - s.n + t * tile_rows + 1 : s.kv;
-    g.nblk = tile_blocks(s, t, tile_rows, A.causal);
-    g.j0 = j;
-    g.j1 = (int)min((long long)g.nblk, j + (u1 - u));
-    g.start = u - j;
-    g.bad = s.bad;
-    u += g.j1 - g.j0;
-    g.more = u < u1;
-    j = 0;
-    if (u < u1 && ++t == s.tiles) {
+  __device__ bool any() const { return at < u1; }
+  __device__ void advance(const AttnParams& A, int tile_rows) {
+    if (++t == s.tiles) {
       t = 0;
       if (++head == A.kv_heads) {
         head = 0;
         do { s = load_seq(A.B, ++b, tile_rows); } while (s.tiles == 0 && b + 1 < A.B.n_seqs);
       }
     }
+  }
+  __device__ bool next(const AttnParams& A, int tile_rows, Segment& g) {
+    if (at >= u1) return false;
+    g.b = b; g.head = head;
+    g.row0 = s.row0 + t * tile_rows;
+    g.ntok = min(tile_rows, s.n - t * tile_rows);
+    g.kv = s.kv;
+    g.lim0 = A.causal ? s.kv - s.n + t * tile_rows + 1 : s.kv;
+    g.nblk = tile_blocks(s, t, tile_rows, A.causal);
+    g.start = at + SETUP;
+    g.j0 = (int)max(0ll, u0 - g.start);
+    g.j1 = (int)min((long long)g.nblk, u1 - g.start);
+    g.bad = s.bad;
+    at = g.start + g.nblk;
+    g.more = at < u1;
+    if (g.more) advance(A, tile_rows);
     return true;
   }
 };
@@ -378,14 +392,15 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   __syncthreads();
   long long units = 0;
   for (int w = 0; w < C::WARPS; ++w) units += red64[w];
-  Walker W;
   const long long ctas = min((long long)gridDim.x, max(1ll, units / MIN_RUN));
-  W.u = blockIdx.x < ctas ? units * blockIdx.x / ctas : 0;   // none without units
-  W.u1 = blockIdx.x < ctas ? units * (blockIdx.x + 1) / ctas : 0;
-  W.b = W.head = W.t = W.j = 0;
-  if (W.u < W.u1) {
+  Walker W;
+  W.at = W.u1 = 0;                                        // an empty run
+  W.b = W.head = W.t = 0;
+  if (blockIdx.x < ctas && units > 0) {
+    // the items that hold the run's two cuts; the last cut of all is the end
+    const long long cut[2] = {units * blockIdx.x / ctas, units * (blockIdx.x + 1) / ctas};
     long long before = 0;
-    for (int b0 = 0; b0 < A.B.n_seqs; b0 += NT) {         // the sequence that holds unit u
+    for (int b0 = 0; b0 < A.B.n_seqs && before <= cut[1]; b0 += NT) {   // their sequences
       const int b = b0 + tid;
       if (A.B.n_seqs > NT) {
         mine = 0;
@@ -410,35 +425,55 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         chunk += x;
       }
       const long long end = below + scan, begin = end - mine;
-      if (begin <= W.u && W.u < end) {
-        const unsigned per = (unsigned)(mine / A.kv_heads), at = (unsigned)(W.u - begin);
-        work[1] = b;
-        work[2] = (int)(at / per);
-        work[3] = (int)(at % per);
-      }
-      before += chunk;
-      if (before > W.u) break;                            // uniform
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (begin <= cut[e] && cut[e] < end) {
+          const unsigned per = (unsigned)(mine / A.kv_heads), at = (unsigned)(cut[e] - begin);
+          int* const found = work + 1 + 5 * e;            // sequence, head, unit within the head, tile, unit within the item
+          found[0] = b;
+          found[1] = (int)(at / per);
+          found[2] = (int)(at % per);
+        }
+      before += chunk;                                    // uniform
     }
+    __syncthreads();
+    long long to[2], from = 0;
+#pragma unroll
+    for (int e = 1; e >= 0; --e) {
+      int* const found = work + 1 + 5 * e;
+      to[e] = cut[e];
+      if (cut[e] == units) continue;
+      W.b = found[0]; W.head = found[1];
+      W.s = load_seq(A.B, W.b, tile_rows);
+      const int r = found[2];
+      for (int t = tid; t < W.s.tiles; t += NT) {
+        const long long lo = tiles_before(W.s, t, tile_rows, A.causal);
+        if (lo <= r && r < lo + SETUP + tile_blocks(W.s, t, tile_rows, A.causal)) {
+          found[3] = t;
+          found[4] = (int)(r - lo);
+        }
+      }
+      __syncthreads();
+      W.t = found[3];
+      const int in = found[4], size = SETUP + tile_blocks(W.s, W.t, tile_rows, A.causal);
+      from = cut[e] - in;
+      if (in <= SNAP) to[e] = from;
+      else if (size - in <= SNAP) to[e] = from + size;
+    }
+    W.u0 = to[0];
+    W.u1 = to[1];
+    W.at = from;
+    if (W.u0 < W.u1 && W.u0 > from && to[0] != cut[0]) {  // moved to the end of that item
+      W.at = W.u0;
+      W.advance(A, tile_rows);
+    }
+    if (W.u0 >= W.u1) W.at = W.u1;
   }
   tc_before();
   __syncthreads();
   tc_after();
   const uint32_t tmem = (uint32_t)work[0];
-  const bool busy = W.u < W.u1;
-  if (busy) {
-    W.b = work[1]; W.head = work[2];
-    W.begin(A, tile_rows);
-    const int r = work[3];                                // unit within the head: its tile and block
-    for (int t = tid; t < W.s.tiles; t += NT) {
-      const long long lo = tiles_before(W.s, t, tile_rows, A.causal);
-      if (lo <= r && r < lo + tile_blocks(W.s, t, tile_rows, A.causal)) {
-        work[4] = t;
-        work[5] = (int)(r - lo);
-      }
-    }
-    __syncthreads();
-    W.t = work[4]; W.j = work[5];
-  }
+  const bool busy = W.any();
   // tensor memory: scores (and weights over them) at 0 and 128, outputs at 256 and 384
   const uint32_t S_COL = tmem, O_COL = tmem + 256;
   constexpr bool BF = !C::FP8;
@@ -557,10 +592,10 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
                 }
               }
               if (!ok) break;
+              if (j + 2 == nb) tc_commit(q_empty);
               tc_commit(v_empty + 8 * (m % NV));
               if (more) {
                 tc_commit(k_empty + 8 * (n % NK));
-                if (j + 2 == nb) tc_commit(q_empty);
                 ++n;
               }
             }
@@ -609,6 +644,9 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           __syncwarp();
           if (elect_one()) {
             while (W.next(A, tile_rows, g)) {
+#pragma unroll
+              for (int i = 0; i < MT * C::HALVES; ++i)     // to L2 meanwhile
+                prefetch_3d(&map_q, (i % C::HALVES) * 64, g.head * A.group, g.row0 + (i / C::HALVES) * A.tile_tokens);
               if (!bar_wait1(q_empty, (segs & 1) ^ 1, flags)) break;
               runs[segs & 3] = g;                          // the softmax is at most two runs behind
               bar_expect(q_full, MT * C::HALVES * used * 128);
@@ -833,14 +871,14 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           tm_ld32(o_at + 32 * i, o);
           tc_wait_ld(o);
           if (have) {
-            uint4* const dst = (uint4*)(A.out + at * D + half * DH + 32 * i);
+            __nv_bfloat16* const dst = A.out + at * D + half * DH + 32 * i;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t w[4];
+            for (int e = 0; e < 2; ++e) {
+              uint32_t w[8];
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                w[y] = pack_bf16(__uint_as_float(o[8 * e + 2 * y]) * inv, __uint_as_float(o[8 * e + 2 * y + 1]) * inv);
-              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int y = 0; y < 8; ++y)
+                w[y] = pack_bf16(__uint_as_float(o[16 * e + 2 * y]) * inv, __uint_as_float(o[16 * e + 2 * y + 1]) * inv);
+              st_32(dst + 16 * e, w);
             }
           }
         }
@@ -867,16 +905,48 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
                      make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]), __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3])));
           }
         }
-        // runs that hold the item: CTA x has units [units x / ctas, units (x + 1) / ctas)
-        const int c0 = (int)(((g.start + 1) * ctas - 1) / units), c1 = (int)(((g.start + g.nblk) * ctas - 1) / units);
+        // runs that hold the item: cut x is at units x / ctas, or moved to the end of an item
+        const long long begin = g.start - SETUP;
+        const int c0 = (int)(((begin + SNAP + 1) * ctas - 1) / units), c1 = (int)(((g.start + g.nblk - SNAP) * ctas - 1) / units);
         __threadfence();
         group_sync(group_bar, NS);
-        if (ts == 0) work[8 + tile] = atomicAdd(A.counters + c0 * MT + tile, 1) == c1 - c0;
+        if (ts == 0) work[14 + tile] = atomicAdd(A.counters + c0 * MT + tile, 1) == c1 - c0;
         group_sync(group_bar, NS);
-        if (work[8 + tile]) {                              // the last to finish
+        if (work[14 + tile]) {                              // the last to finish
           __threadfence();
           if (ts == 0) A.counters[c0 * MT + tile] = 0;
           const int rows = min(A.tile_tokens, max(0, g.ntok - tile * A.tile_tokens)) * A.group;
+          if (c1 == c0 + 1) {
+            // two partials: every thread merges a half of its row
+            if (r < rows) {
+              const float *const p = part(c0, 1), *const q = part(c1, 0);
+              const float m0 = __ldcg(p + r), m1 = __ldcg(q + r), l0 = __ldcg(p + BM + r), l1 = __ldcg(q + BM + r),
+                          d0 = __ldcg(p + 2 * BM + r), d1 = __ldcg(q + 2 * BM + r);
+              const float4 *const po = (const float4*)(p + 3 * BM) + half * (DH / 4) * BM + r, *const qo = (const float4*)(q + 3 * BM) + half * (DH / 4) * BM + r;
+              const float m_top = fmaxf(m0, m1), ref = m_top == -INFINITY ? 0.0f : m_top;
+              const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref), sum = f0 * l0 + f1 * l1;
+              const float inv = sum == 0.0f ? 0.0f : 1.0f / (sum + f0 * d0 + f1 * d1), w0 = f0 * inv, w1 = f1 * inv;
+              const int rt = r / A.group;
+              const size_t to = (size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + r - rt * A.group;
+#pragma unroll
+              for (int i = 0; i < DH / 4; i += 4) {
+                float4 x[4], y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  x[e] = __ldcg(po + (i + e) * BM);
+                  y[e] = __ldcg(qo + (i + e) * BM);
+                }
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  w[2 * e] = pack_bf16(w0 * x[e].x + w1 * y[e].x, w0 * x[e].y + w1 * y[e].y);
+                  w[2 * e + 1] = pack_bf16(w0 * x[e].z + w1 * y[e].z, w0 * x[e].w + w1 * y[e].w);
+                }
+                st_32(A.out + to * D + half * DH + 4 * i, w);
+              }
+              if (A.lse && half == 0) A.lse[to] = (m_top + log2f(sum)) * LN2_F;
+            }
+          } else {
           // weight of every partial, left where its reference was
           if (ts < rows) {
             float m_top = -INFINITY, sum = 0.0f, fix = 0.0f;
@@ -941,6 +1011,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               const size_t to = (size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + rr[q] - rt * A.group;
               *(uint2*)(A.out + to * D + 4 * (at[q] / BM)) = make_uint2(pack_bf16(o[q].x, o[q].y), pack_bf16(o[q].z, o[q].w));
             }
+          }
           }
         }
       }
