@@ -197,7 +197,7 @@ __host__ __device__ constexpr uint32_t instr_desc(bool bf16, int n, bool b_mn_ma
 }
 
 // ------------------------------------------------------------------ planning
-// sum over i = 0 .. n-1 of floor((a i + b) / m), by the Euclidean reduction of lattice points
+// sum over i = 0 .. n-1 of floor((a i + b) / m), by the Euclidean reduction of lattice points; a n + b < 2^32
 __device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   unsigned long long s = 0;
   while (n > 0) {
@@ -205,10 +205,10 @@ __device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsign
     a %= m;
     s += (unsigned long long)n * (b / m);
     b %= m;
-    const unsigned long long y = (unsigned long long)a * n + b;
+    const unsigned y = a * n + b;
     if (y < m) break;
-    n = (unsigned)(y / m);
-    b = (unsigned)(y % m);
+    n = y / m;
+    b = y % m;
     const unsigned t = m;
     m = a;
     a = t;
@@ -437,24 +437,29 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       before += chunk;                                    // uniform
     }
     __syncthreads();
-    long long to[2], from = 0;
-#pragma unroll
-    for (int e = 1; e >= 0; --e) {
-      int* const found = work + 1 + 5 * e;
-      to[e] = cut[e];
-      if (cut[e] == units) continue;
-      W.b = found[0]; W.head = found[1];
-      W.s = load_seq(A.B, W.b, tile_rows);
+    // their tiles: half of the threads look for each
+    const int mine_e = tid >= NT / 2;
+    if (cut[mine_e] < units) {
+      int* const found = work + 1 + 5 * mine_e;
+      const Seq s = load_seq(A.B, found[0], tile_rows);
       const int r = found[2];
-      for (int t = tid; t < W.s.tiles; t += NT) {
-        const long long lo = tiles_before(W.s, t, tile_rows, A.causal);
-        if (lo <= r && r < lo + SETUP + tile_blocks(W.s, t, tile_rows, A.causal)) {
+      for (int t = tid - mine_e * (NT / 2); t < s.tiles; t += NT / 2) {
+        const long long lo = tiles_before(s, t, tile_rows, A.causal);
+        if (lo <= r && r < lo + SETUP + tile_blocks(s, t, tile_rows, A.causal)) {
           found[3] = t;
           found[4] = (int)(r - lo);
         }
       }
-      __syncthreads();
-      W.t = found[3];
+    }
+    __syncthreads();
+    long long to[2], from = 0;
+#pragma unroll
+    for (int e = 1; e >= 0; --e) {
+      const int* const found = work + 1 + 5 * e;
+      to[e] = cut[e];
+      if (cut[e] == units) continue;
+      W.b = found[0]; W.head = found[1]; W.t = found[3];
+      W.s = load_seq(A.B, W.b, tile_rows);
       const int in = found[4], size = SETUP + tile_blocks(W.s, W.t, tile_rows, A.causal);
       from = cut[e] - in;
       if (in <= SNAP) to[e] = from;
