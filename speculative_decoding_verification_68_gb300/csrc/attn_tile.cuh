@@ -330,7 +330,7 @@ struct Cfg {
   static constexpr int INFO = 8;                              // ring of block references (more than NK + 1)
 };
 // named barriers: pairs of softmax warps of a quarter of a tile's rows, tiles, converting warps
-enum { BAR_PAIR = 1, BAR_TILE = 9, BAR_CONV = 11 };
+enum { BAR_PAIR = 1, BAR_TILE = 9, BAR_CONV = 11 };      // the last: one for keys, one for values
 
 template <int D, int KIND, int MT>
 __global__ void __launch_bounds__(Cfg<D, KIND, MT>::THREADS, 1)
@@ -365,9 +365,9 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 
   // ---- set-up: barriers, tensor memory, and this CTA's run of units
   if (tid == 0) {
-    for (int i = 0; i < NK; ++i) { bar_init(k_full + 8 * i, C::FP8 ? C::CONV_WARPS : 1); bar_init(k_empty + 8 * i, 1); }
-    for (int i = 0; i < NV; ++i) { bar_init(v_full + 8 * i, C::FP8 ? C::CONV_WARPS : 1); bar_init(v_empty + 8 * i, 1); }
-    for (int i = 0; i < C::NRAW; ++i) { bar_init(raw_full + 8 * i, 1); bar_init(raw_empty + 8 * i, C::CONV_WARPS); }
+    for (int i = 0; i < NK; ++i) { bar_init(k_full + 8 * i, C::FP8 ? 4 : 1); bar_init(k_empty + 8 * i, 1); }
+    for (int i = 0; i < NV; ++i) { bar_init(v_full + 8 * i, C::FP8 ? 4 : 1); bar_init(v_empty + 8 * i, 1); }
+    for (int i = 0; i < C::NRAW; ++i) { bar_init(raw_full + 8 * i, 1); bar_init(raw_empty + 8 * i, 4); }
     for (int i = 0; i < 2; ++i) { bar_init(s_full + 8 * i, 1); bar_init(p_full + 8 * i, C::SOFT_WARPS); bar_init(o_done + 8 * i, 1); }
     bar_init(q_full, C::FP8 ? C::Q_WARPS : 1);
     bar_init(q_empty, 1);
@@ -669,16 +669,35 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         // as f16, normalised by a power of two: 16 bytes a thread, the threads of a row together
         constexpr int LR = D / 8, RP = C::Q_WARPS * 32 / LR;   // threads of a row, rows a pass
         const int t = tid - C::Q_WARP0 * 32, ch = t % LR;
+        const unsigned over_group = 65536u / A.group + 1;  // r / group = r * over_group >> 16 for r < 128
         while (ok && W.next(A, tile_rows, g)) {
+          const __nv_bfloat16* const rows = A.Q.ptr + g.row0 * A.Q.st + g.head * A.group * A.Q.sh;
+          const int n_tok = min(A.tile_tokens, g.ntok);
+          for (int r = t; r < BM; r += C::Q_WARPS * 32) {  // to L2 meanwhile
+            const int tok = (int)(r * over_group >> 16);
+            if (tok < n_tok) {
+              const char* const line = (const char*)(rows + tok * A.Q.st + (r - tok * A.group) * A.Q.sh);
+#pragma unroll
+              for (int o = 0; o < 2 * D; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + o));
+            }
+          }
           if (!(ok = bar_wait(q_empty, (segs & 1) ^ 1, flags))) break;
           uint8_t* const q = gbase + (ch / 8) * HALF_BYTES;
           if (t == 0) runs[segs & 3] = g;                  // the softmax is at most two runs behind
-#pragma unroll 8
-          for (int r0 = 0; r0 < BM; r0 += RP) {
-            const int r = r0 + t / LR, tok = r / A.group, head_in = r - tok * A.group;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (tok < min(A.tile_tokens, g.ntok))
-              x = __ldg((const uint4*)(A.Q.ptr + (g.row0 + tok) * A.Q.st + (g.head * A.group + head_in) * A.Q.sh) + ch);
+          constexpr int U = 16;                            // loads of a thread in flight
+#pragma unroll 1
+          for (int r0 = t / LR; r0 < BM; r0 += U * RP) {
+          uint4 xs[U];
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            const int r = r0 + i * RP, tok = (int)(r * over_group >> 16);
+            xs[i] = make_uint4(0, 0, 0, 0);
+            if (tok < n_tok) xs[i] = __ldg((const uint4*)(rows + tok * A.Q.st + (r - tok * A.group) * A.Q.sh) + ch);
+          }
+#pragma unroll
+          for (int i = 0; i < U; ++i) {
+            const int r = r0 + i * RP;
+            const uint4 x = xs[i];
             uint32_t w[4] = {x.x, x.y, x.z, x.w}, top = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
@@ -691,6 +710,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] = pack_f16(bf_lo(w[i]) * f, bf_hi(w[i]) * f);
             *(uint4*)(q + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
           }
           fence_async();
           __syncwarp();
@@ -1033,13 +1053,17 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     // values the reference M covers s_ij + e, so a weight times a block value
     // stays within range whatever the vectors' sizes.  e of the values is kept
     // within 2^64 of the run's largest so that the weights do not vanish.
-    // Two threads a key: raw lines are swizzled like the f16 ones, so that eight
-    // threads of eight keys reach eight different 16-byte columns.
-    const int t = tid - C::CONV_WARP0 * 32, key = t & 127, part = t >> 7;
-    constexpr int NTC = C::CONV_WARPS * 32;
-    static_assert(NTC == 2 * BN, "two converting threads per key");
-    int2* const wmax = (int2*)red;                         // [2][4]: maxima per quarter of the keys
-    unsigned n = 0, raw = 0;
+    // Four warps convert the keys, four the values, a thread a vector.  Raw lines
+    // are swizzled like the f16 ones, so that eight threads of eight keys reach
+    // eight different 16-byte columns.
+    const int key = tid & 127, kv = (warp - C::CONV_WARP0) >> 2, bar_id = BAR_CONV + kv;
+    static_assert(C::CONV_WARPS == 8 && C::CONV_WARP0 % 4 == 0, "one converting thread per key and per value");
+    int2* const wmax = (int2*)red + kv * 8;                // [2][4]: maxima per quarter of the keys
+    const uint32_t full0 = kv ? v_full : k_full, empty0 = kv ? v_empty : k_empty;
+    const unsigned ring = kv ? NV : NK;
+    uint8_t* const out0 = gbase + ((kv ? v_at : k_at) - base) + key * 128;
+    const uint8_t* const raw0 = gbase + (raw_at - base) + key * D;
+    unsigned n = 0;
     bool ok = true, stop = false;
     while (!stop && W.next(A, tile_rows, g)) {
       const int32_t* const tab = A.B.table + (size_t)g.b * A.B.max_pages;
@@ -1050,60 +1074,59 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const int page = __ldg(tab + (p >> A.B.page_shift));
         if ((unsigned)page >= (unsigned)A.B.num_pages) return make_int2(0, 0);
         const size_t at = ((size_t)(page * A.kv_heads + g.head) << A.B.page_shift) + (p & ((1 << A.B.page_shift) - 1));
-        return make_int2(__ldg(A.ks + at), __ldg(A.vs + at));
+        return make_int2(kv ? 0 : __ldg(A.ks + at), __ldg(A.vs + at));
       };
       int2 nxt = load_bytes(g.j0);
       for (int j = g.j0; j < g.j1; ++j, ++n) {
         const int2 cur = nxt;
-        if (j + 1 < g.j1) nxt = load_bytes(j + 1);
         const int ka = __reduce_max_sync(FULL, cur.x == BYTE_NAN ? 0 : cur.x), va = __reduce_max_sync(FULL, cur.y == BYTE_NAN ? 0 : cur.y);
         int2* const wm = wmax + (n & 1) * 4;
-        if (lane == 0 && part == 0) wm[warp & 3] = make_int2(ka, va);
-        if ((stop = group_or(BAR_CONV, NTC, !ok))) break;  // all warps leave, or none
-        int eb[2];
-        eb[0] = max(max(max(wm[0].x, wm[1].x), max(wm[2].x, wm[3].x)) - EXP_BIAS, EXP_MIN);
-        eb[1] = max(max(max(wm[0].y, wm[1].y), max(wm[2].y, wm[3].y)) - EXP_BIAS, run - 64);
-        run = max(run, eb[1]);
-        eb[1] = max(eb[1], run - 64);
-        if (t == 0) info[n % C::INFO] = make_float2(__int_as_float((eb[0] + EXP_BIAS) << 23), (float)eb[1]);
-        const bool valid = key < g.kv - j * BN;
+        if (lane == 0) wm[warp & 3] = make_int2(ka, va);
+        if ((stop = group_or(bar_id, BN, !ok))) break;     // all four warps leave, or none
+        if (j + 1 < g.j1) nxt = load_bytes(j + 1);
+        const int ek = max(max(max(wm[0].x, wm[1].x), max(wm[2].x, wm[3].x)) - EXP_BIAS, EXP_MIN);
+        int ev = max(max(max(wm[0].y, wm[1].y), max(wm[2].y, wm[3].y)) - EXP_BIAS, run - 64);
+        run = max(run, ev);
+        ev = max(ev, run - 64);
+        // both for the softmax, ahead of the keys and so of the block's scores
+        if (kv == 0 && key == 0) info[n % C::INFO] = make_float2(__int_as_float((ek + EXP_BIAS) << 23), (float)ev);
+        const bool valid = key < g.kv - j * BN;            // slots past the end may hold anything
+        const int by = kv ? cur.y : cur.x, d = by == BYTE_NAN ? 0 : by - EXP_BIAS - (kv ? ev : ek);   // <= 0
+        const uint32_t f1 = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u, f = f1 | (f1 << 16);
+        const unsigned raw = 2 * n + kv, rs = raw % C::NRAW, bs = n % ring;
+        ok = bar_wait(raw_full + 8 * rs, (raw / C::NRAW) & 1, flags) && bar_wait(empty0 + 8 * bs, ((n / ring) & 1) ^ 1, flags);
+        const uint8_t* const src = raw0 + rs * C::RAW;
+        uint8_t* const dst = out0 + bs * C::BUF;
+        if (ok) {
 #pragma unroll
-        for (int kv = 0; kv < 2 && ok; ++kv, ++raw) {
-          const unsigned rs = raw % C::NRAW, ring = kv ? NV : NK, bs = n % ring;
-          const uint32_t full = (kv ? v_full : k_full) + 8 * bs, empty = (kv ? v_empty : k_empty) + 8 * bs;
-          const int by = kv ? cur.y : cur.x, d = by == BYTE_NAN ? 0 : by - EXP_BIAS - eb[kv];   // <= 0
-          const uint32_t f1 = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u, f = f1 | (f1 << 16);
-          if (!(ok = bar_wait(raw_full + 8 * rs, (raw / C::NRAW) & 1, flags)) || !(ok = bar_wait(empty, ((n / ring) & 1) ^ 1, flags))) break;
-          const uint8_t* const src = gbase + (raw_at - base) + rs * C::RAW + key * D;
-          uint8_t* const dst = gbase + ((kv ? v_at : k_at) - base) + bs * C::BUF + key * 128;
-          constexpr int CH = D / 32;                       // 16-code chunks of this thread
-          uint4 xs[CH];
+          for (int h = 0; h < D / 64; ++h) {               // 64 codes: one line of the f16 block
+            uint4 xs[4];
 #pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            const int ch = part * CH + i;
-            xs[i] = *(const uint4*)(src + ((D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4));
-          }
-#pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            const int ch = part * CH + i, c0 = (ch % 4) * 2;
-            const uint32_t w[4] = {xs[i].x, xs[i].y, xs[i].z, xs[i].w};
-            uint32_t y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint32_t hcode = e4m3_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-              asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(hcode), "r"(f));
-              if (!valid) y[e] = 0;                        // slots past the end may hold anything
+            for (int i = 0; i < 4; ++i) {
+              const int ch = 4 * h + i;
+              xs[i] = *(const uint4*)(src + ((D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4));
+              if (!valid) xs[i] = make_uint4(0, 0, 0, 0);
             }
-            uint8_t* const line = dst + (ch / 4) * HALF_BYTES;
-            *(uint4*)(line + ((c0 ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-            *(uint4*)(line + (((c0 + 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w[4] = {xs[i].x, xs[i].y, xs[i].z, xs[i].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t hcode = e4m3_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(hcode), "r"(f));
+              }
+              uint8_t* const line = dst + h * HALF_BYTES;
+              *(uint4*)(line + (((2 * i) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *(uint4*)(line + (((2 * i + 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+            }
           }
-          fence_async();
-          __syncwarp();
-          if (lane == 0) {
-            bar_arrive(raw_empty + 8 * rs);
-            bar_arrive(full);
-          }
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(raw_empty + 8 * rs);
+          bar_arrive(full0 + 8 * bs);
         }
       }
     }
