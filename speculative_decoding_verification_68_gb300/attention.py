@@ -137,7 +137,15 @@ class SpecAttention:
         h = ctypes.c_void_p()
         check_status(self._lib.spec_attn_init(ctypes.byref(h), q_heads, kv_heads, head_dim, max_seqs), "spec_attn_init")
         self._h = h
-        self.device = torch.device("cuda", torch.cuda.current_device())   # the handle's GPU
+        index = torch.cuda.current_device()
+        self.device = torch.device("cuda", index)     # the handle's GPU
+        # the current stream's pointer; the public call builds a Stream object first
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        self._current = (lambda: raw(index)) if raw else (lambda: torch.cuda.current_stream(self.device).cuda_stream)
+        # argument blocks of the calls, refilled by each (a handle is not thread-safe)
+        self._batch_c, self._q_c, self._k_c, self._v_c = _CBatch(), _CRows(), _CRows(), _CRows()
+        self._batch_ref, self._q_ref, self._k_ref, self._v_ref = (
+            ctypes.byref(x) for x in (self._batch_c, self._q_c, self._k_c, self._v_c))
 
     def close(self):
         if getattr(self, "_h", None):
@@ -157,7 +165,7 @@ class SpecAttention:
             raise SpecVerifyError(code, where)
 
     def _stream(self, stream):
-        return (torch.cuda.current_stream(self.device) if stream is None else stream).cuda_stream
+        return self._current() if stream is None else stream.cuda_stream
 
     def alloc_pool(self, num_pages: int, page_size: int = 64, dtype=torch.bfloat16) -> KVPool:
         """An empty pool for this handle's heads."""
@@ -168,27 +176,51 @@ class SpecAttention:
         scales = [torch.full(shape[:3], 127, dtype=torch.uint8, device=self.device) for _ in range(2)]
         return KVPool(k.view(dtype), v.view(dtype), *scales)
 
-    def _check_pool(self, pool):
-        if pool.kv_heads != self.kv_heads or pool.head_dim != self.head_dim:
-            raise ValueError(f"pool of {pool.kv_heads} heads of {pool.head_dim}, expected {self.kv_heads} of {self.head_dim}")
-        if not _same_device(pool, self.device):
-            raise ValueError(f"pool is on {pool.device}, expected {self.device}")
+    # The checks below test everything in one expression and leave it to the
+    # functions above, which say what is wrong, to raise.
 
     def _batch(self, pool, n_tokens, cu, kv_len, page_table):
-        self._check_pool(pool)
-        n = check_sequences(cu, self.device, self.max_seqs, kv_len, page_table)
-        return ctypes.byref(_CBatch(cu.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), n, n_tokens, page_table.shape[1]))
+        device = self.device
+        if pool.kv_heads != self.kv_heads or pool.head_dim != self.head_dim:
+            raise ValueError(f"pool of {pool.kv_heads} heads of {pool.head_dim}, expected {self.kv_heads} of {self.head_dim}")
+        if pool.device != device:
+            raise ValueError(f"pool is on {pool.device}, expected {device}")
+        i32 = torch.int32
+        try:
+            n, width = page_table.shape
+            ok = (cu.shape == (n + 1,) and kv_len.shape == (n,) and n <= self.max_seqs
+                  and cu.dtype is i32 and kv_len.dtype is i32 and page_table.dtype is i32
+                  and cu.is_contiguous() and kv_len.is_contiguous() and page_table.is_contiguous()
+                  and cu.device == device and kv_len.device == device and page_table.device == device)
+        except (AttributeError, ValueError):
+            ok = False
+        if not ok:
+            check_sequences(cu, device, self.max_seqs, kv_len, page_table)
+        c = self._batch_c
+        c.cu, c.kv_len, c.page_table = cu.data_ptr(), kv_len.data_ptr(), page_table.data_ptr()
+        c.n_seqs, c.n_tokens, c.max_pages = n, n_tokens, width
+        return self._batch_ref
 
-    def _rows(self, t, name, heads, n_tokens=None):
-        check_rows(t, name, heads, self.head_dim, self.device, n_tokens)
-        stride = t.stride()
-        return ctypes.byref(_CRows(t.data_ptr(), stride[0], stride[1]))
+    def _rows(self, c, t, name, heads, n_tokens=None):
+        try:
+            n, h, d = t.shape
+            token, head, last = t.stride()
+            ptr = t.data_ptr()
+            ok = (h == heads and d == self.head_dim and (n_tokens is None or n == n_tokens) and t.dtype is torch.bfloat16
+                  and t.device == self.device and (n == 0 or last == 1 and not (token | head | ptr >> 1) & 7))
+        except (AttributeError, ValueError):
+            ok = False
+        if not ok:
+            check_rows(t, name, heads, self.head_dim, self.device, n_tokens)
+        c.ptr, c.token_stride, c.head_stride = ptr, token, head
+        return n
 
     def _outputs(self, n, want_lse, out):
         if out is None:
-            out = {"out": torch.empty((n, self.q_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)}
+            device = self.device
+            out = {"out": torch.empty((n, self.q_heads, self.head_dim), dtype=torch.bfloat16, device=device)}
             if want_lse:
-                out["lse"] = torch.empty((n, self.q_heads), dtype=torch.float32, device=self.device)
+                out["lse"] = torch.empty((n, self.q_heads), dtype=torch.float32, device=device)
             return out
         _check(out.get("out"), "output out", torch.bfloat16, (n, self.q_heads, self.head_dim), self.device)
         if out["out"].data_ptr() % 32:
@@ -209,10 +241,12 @@ class SpecAttention:
     def append(self, pool: KVPool, k, v, cu, kv_len, page_table, stream=None) -> None:
         """spec_attn_append: writes k and v [n_tokens, kv_heads, head_dim], the last
         tokens of their sequences, into the pool (asynchronous)."""
-        kr = self._rows(k, "k", self.kv_heads)
-        vr = self._rows(v, "v", self.kv_heads, k.shape[0])
-        batch = self._batch(pool, k.shape[0], cu, kv_len, page_table)
-        self._status(self._lib.spec_attn_append(self._h, pool._ref, batch, kr, vr, self._stream(stream)), "spec_attn_append")
+        n = self._rows(self._k_c, k, "k", self.kv_heads)
+        self._rows(self._v_c, v, "v", self.kv_heads, n)
+        rc = self._lib.spec_attn_append(self._h, pool._ref, self._batch(pool, n, cu, kv_len, page_table), self._k_ref,
+                                        self._v_ref, self._stream(stream))
+        if rc:
+            self._status(rc, "spec_attn_append")
 
     def read(self, pool: KVPool, cu, kv_len, page_table, n_tokens: int, out: dict | None = None, stream=None) -> dict:
         """spec_attn_read: positions kv_len[b] - n_b .. kv_len[b] - 1 of every sequence
@@ -221,14 +255,16 @@ class SpecAttention:
         batch = self._batch(pool, n_tokens, cu, kv_len, page_table)
         shape = (n_tokens, self.kv_heads, self.head_dim)
         if out is None:
-            out = {name: torch.empty(shape, dtype=torch.bfloat16, device=self.device) for name in ("k", "v")}
+            out = {"k": torch.empty(shape, dtype=torch.bfloat16, device=self.device),
+                   "v": torch.empty(shape, dtype=torch.bfloat16, device=self.device)}
         else:
             for name in ("k", "v"):
                 _check(out.get(name), f"output {name}", torch.bfloat16, shape, self.device)
                 if out[name].data_ptr() % 16:
                     raise ValueError(f"output {name} must be 16-byte aligned")
-        self._status(self._lib.spec_attn_read(self._h, pool._ref, batch, out["k"].data_ptr(), out["v"].data_ptr(),
-                                              self._stream(stream)), "spec_attn_read")
+        rc = self._lib.spec_attn_read(self._h, pool._ref, batch, out["k"].data_ptr(), out["v"].data_ptr(), self._stream(stream))
+        if rc:
+            self._status(rc, "spec_attn_read")
         return out
 
     def attend(self, pool: KVPool, q, cu, kv_len, page_table, causal: bool = True, scale: float | None = None,
@@ -237,30 +273,39 @@ class SpecAttention:
         over the pool, which holds their keys and values already.  Returns "out"
         (like q) and, if wanted, "lse" [n_tokens, q_heads].  scale defaults to
         head_dim ** -0.5; causal=False lets every new token see all kv_len entries."""
-        qr = self._rows(q, "q", self.q_heads)
-        batch = self._batch(pool, q.shape[0], cu, kv_len, page_table)
+        n = self._rows(self._q_c, q, "q", self.q_heads)
+        batch = self._batch(pool, n, cu, kv_len, page_table)
         scale = self._scale(scale)
-        out = self._outputs(q.shape[0], want_lse, out)
+        out = self._outputs(n, want_lse, out)
         lse = out.get("lse")
-        self._status(self._lib.spec_attn_chunk(self._h, pool._ref, batch, qr, int(causal), scale, out["out"].data_ptr(),
-                                               None if lse is None else lse.data_ptr(), self._stream(stream)),
-                     "spec_attn_chunk")
+        rc = self._lib.spec_attn_chunk(self._h, pool._ref, batch, self._q_ref, int(causal), scale, out["out"].data_ptr(),
+                                       None if lse is None else lse.data_ptr(), self._stream(stream))
+        if rc:
+            self._status(rc, "spec_attn_chunk")
         return out
 
     def prompt(self, q, k, v, cu, scale: float | None = None, want_lse: bool = False, out: dict | None = None,
                stream=None) -> dict:
         """spec_attn_prompt: causal attention over packed prompts, q [n_tokens, q_heads,
         head_dim], k and v [n_tokens, kv_heads, head_dim].  Returns as attend."""
-        qr = self._rows(q, "q", self.q_heads)
-        n = q.shape[0]
-        kr, vr = self._rows(k, "k", self.kv_heads, n), self._rows(v, "v", self.kv_heads, n)
-        n_seqs = check_sequences(cu, self.device, self.max_seqs, paged=False)
+        n = self._rows(self._q_c, q, "q", self.q_heads)
+        self._rows(self._k_c, k, "k", self.kv_heads, n)
+        self._rows(self._v_c, v, "v", self.kv_heads, n)
+        try:
+            n_seqs = cu.shape[0] - 1
+            ok = (cu.dtype is torch.int32 and cu.dim() == 1 and 0 <= n_seqs <= self.max_seqs and cu.is_contiguous()
+                  and cu.device == self.device)
+        except (AttributeError, IndexError):
+            ok = False
+        if not ok:
+            n_seqs = check_sequences(cu, self.device, self.max_seqs, paged=False)
         scale = self._scale(scale)
         out = self._outputs(n, want_lse, out)
         lse = out.get("lse")
-        self._status(self._lib.spec_attn_prompt(self._h, n_seqs, n, cu.data_ptr(), qr, kr, vr, scale, out["out"].data_ptr(),
-                                                None if lse is None else lse.data_ptr(), self._stream(stream)),
-                     "spec_attn_prompt")
+        rc = self._lib.spec_attn_prompt(self._h, n_seqs, n, cu.data_ptr(), self._q_ref, self._k_ref, self._v_ref, scale,
+                                        out["out"].data_ptr(), None if lse is None else lse.data_ptr(), self._stream(stream))
+        if rc:
+            self._status(rc, "spec_attn_prompt")
         return out
 
     def get_error(self) -> int:
