@@ -98,7 +98,7 @@ int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_
 
 /* Copy the batch's tokens (positions kv_len[b] - n_b .. kv_len[b] - 1) out of
  * the pool into k_out and v_out, [n_tokens, kv_heads, head_dim] contiguous
- * bf16 (e4m3 values times their power of two, rounded to nearest even where
+ * bf16, 32-byte aligned (e4m3 values times their power of two, rounded to nearest even where
  * bf16 is not exact: only below its normal range).  One kernel launch. */
 int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch,
                    void* k_out, void* v_out, void* cuda_stream);

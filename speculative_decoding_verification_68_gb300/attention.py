@@ -260,8 +260,8 @@ class SpecAttention:
         else:
             for name in ("k", "v"):
                 _check(out.get(name), f"output {name}", torch.bfloat16, shape, self.device)
-                if out[name].data_ptr() % 16:
-                    raise ValueError(f"output {name} must be 16-byte aligned")
+                if out[name].data_ptr() % 32:
+                    raise ValueError(f"output {name} must be 32-byte aligned")
         rc = self._lib.spec_attn_read(self._h, pool._ref, batch, out["k"].data_ptr(), out["v"].data_ptr(), self._stream(stream))
         if rc:
             self._status(rc, "spec_attn_read")

@@ -74,41 +74,8 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   return v;
 }
 
-// The sequence that holds packed token t, or -1.  cu need not be trusted: the
-// search stays in range whatever it holds, and the result is checked.
-__device__ __forceinline__ int find_seq(const Batch& B, int t) {
-  int lo = 0, hi = B.n_seqs;                      // largest b with cu[b] <= t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(B.cu + mid) <= t) lo = mid; else hi = mid;
-  }
-  const int a = __ldg(B.cu + lo), e = __ldg(B.cu + lo + 1);
-  return (a >= 0 && a <= t && t < e && e <= B.n_tokens) ? lo : -1;
-}
-// Slot index (page * page_size + slot, the head still to be added) of position
-// pos; -1 where it has none, -2 where the metadata is invalid (flagged).
-__device__ __forceinline__ long long find_slot(const Batch& B, int b, int pos) {
-  if (pos < 0) return -1;
-  const int page = __ldg(B.table + (size_t)b * B.max_pages + (pos >> B.page_shift));
-  if ((unsigned)page >= (unsigned)B.num_pages) return -2;
-  return ((long long)page << B.page_shift) | (pos & ((1 << B.page_shift) - 1));
-}
 __device__ __forceinline__ bool len_valid(const Batch& B, int len) {
   return len >= 0 && (long long)len <= ((long long)B.max_pages << B.page_shift);
-}
-// Position of packed token t; false where the sequence is invalid.
-__device__ __forceinline__ bool token_place(const Batch& B, int t, int& b, int& pos) {
-  b = find_seq(B, t);
-  if (b < 0) return false;
-  const int len = __ldg(B.kv_len + b);
-  if (!len_valid(B, len)) return false;
-  pos = len - __ldg(B.cu + b + 1) + t;
-  return true;
-}
-// index of the vector of (slot, head) in a pool [page, head, slot, D]
-__device__ __forceinline__ long long vec_index(long long slot, int head, int heads, int page_shift) {
-  const long long page = slot >> page_shift;
-  return ((page * heads + head) << page_shift) + (slot & ((1 << page_shift) - 1));
 }
 // Whether sequence b's row range and length are within the call's limits.
 __device__ __forceinline__ bool seq_valid(const Batch& B, int b) {

@@ -14,59 +14,110 @@
 
 namespace {
 
+// ------------------------------------------------------- where a token lives
+// A warp works on one token at a time, all its heads: the search of its
+// sequence and page is paid once for 2 * heads vectors, whose 16-byte pieces
+// the lanes then hold, several in flight each.
+
+// The sequence that holds packed token t, or -1: 32 probes a step.  cu need not
+// be trusted: the search stays in range whatever it holds, and the result is
+// checked.
+__device__ __forceinline__ int find_seq(const Batch& B, int t, int lane) {
+  int lo = 0, hi = B.n_seqs;                      // largest b with cu[b] <= t
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) >> 5, probe = lo + lane * step;
+    const int below = __popc(__ballot_sync(FULL, probe < hi && __ldg(B.cu + min(probe, hi)) <= t));
+    lo += max(0, below - 1) * step;
+    hi = min(hi, lo + step);
+    lo = min(lo, hi - 1);
+  }
+  const int a = __ldg(B.cu + lo), e = __ldg(B.cu + lo + 1);
+  return (a >= 0 && a <= t && t < e && e <= B.n_tokens) ? lo : -1;
+}
+// Page of token t, and its slot there.  NO_ROW: in no sequence; INVALID: in one whose length or page
+// is not valid (both are reported); NO_SLOT: before the first position.
+enum { NO_SLOT = -1, INVALID = -2, NO_ROW = -3 };
+__device__ __forceinline__ int find_page(const Batch& B, int t, int lane, int& slot) {
+  const int b = find_seq(B, t, lane);
+  int page = NO_ROW;
+  if (b >= 0) {
+    const int len = __ldg(B.kv_len + b), pos = len - __ldg(B.cu + b + 1) + t;
+    if (!len_valid(B, len)) {
+      page = INVALID;
+    } else if (pos < 0) {
+      page = NO_SLOT;
+    } else {
+      page = __ldg(B.table + (size_t)b * B.max_pages + (pos >> B.page_shift));
+      if ((unsigned)page >= (unsigned)B.num_pages) page = INVALID;
+      slot = pos & ((1 << B.page_shift) - 1);
+    }
+  }
+  if (page <= INVALID && lane == 0) B.flags[0] = 1;
+  return page;
+}
+constexpr int U = 2;                              // pieces of a lane in flight
+// A piece is 16 bytes of the pool: 8 bf16 values or 16 codes, D / piece of them a vector.
+template <bool FP8> constexpr int piece_of = FP8 ? 16 : 8;
+
 // -------------------------------------------------------------------- append
-// One 16-byte lane-load per 8 elements: D / 8 lanes hold one vector, so its
-// largest magnitude is a few shuffles away and the codes leave as 8-byte
-// stores.  Bound by memory: 2 D bytes read and D + 1 written per vector.
+// The lanes of a vector find its largest magnitude by a few shuffles.  Bound by
+// memory: 2 D bytes read and D + 1 (e4m3) or 2 D written per vector.
 template <int D, bool FP8>
-__global__ void __launch_bounds__(256) sa_append_kernel(Batch B, Pool P, Rows K, Rows V, int heads) {
-  constexpr int LV = D / 8;
+__global__ void __launch_bounds__(128) sa_append_kernel(Batch B, Pool P, Rows K, Rows V, int heads) {
+  constexpr int E = piece_of<FP8>, LV = D / E, NL = E / 8;
   flag_invalid_seqs(B);
-  const long long n = (long long)B.n_tokens * heads;
-  const int lane = threadIdx.x % LV;
-  const long long step = (long long)gridDim.x * (256 / LV);
-  // every lane of a warp makes the same number of turns: the shuffles below are warp-wide
-  for (long long base = (long long)blockIdx.x * (256 / LV); base < n; base += step) {
-    const long long i = base + threadIdx.x / LV;
-    const bool in = i < n;
-    const int t = in ? (int)(i / heads) : 0, head = in ? (int)(i - (long long)t * heads) : 0;
-    int b = -1, pos = -1;
-    long long slot = -1;
-    if (in) {
-      if (token_place(B, t, b, pos)) slot = find_slot(B, b, pos);
-      else slot = -2;
-      if (slot == -2 && lane == 0) B.flags[0] = 1;
-    }
-    uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (slot >= 0) {
-      x[0] = ldg_stream(K.ptr + t * K.st + head * K.sh + lane * 8);
-      x[1] = ldg_stream(V.ptr + t * V.st + head * V.sh + lane * 8);
-    }
-    const long long vec = slot >= 0 ? vec_index(slot, head, heads, B.page_shift) : 0;
+  const int lane = threadIdx.x & 31, piece = lane % LV;
+  const int pieces = 2 * heads * LV;              // keys, then values
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (t < B.n_tokens) {
+    int slot = 0;
+    const int page = find_page(B, t, lane, slot);
+    if (page < 0) return;
+    const __nv_bfloat16 *const k = K.ptr + t * K.st + piece * E, *const v = V.ptr + t * V.st + piece * E;
+    const long long vec0 = (((long long)page * heads) << B.page_shift) + slot;
+    for (int c0 = lane; c0 - lane < pieces; c0 += 32 * U) {   // as often in every lane: the shuffles are warp-wide
+      uint4 x[U][NL];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      char* dst = (char*)(s ? P.v : P.k);
-      if constexpr (!FP8) {
-        if (slot >= 0) *(uint4*)(dst + (vec * D + lane * 8) * 2) = x[s];
-      } else {
-        // magnitudes as bf16 bit patterns order like the values, infinities and NaN above all
-        const uint32_t w[4] = {x[s].x, x[s].y, x[s].z, x[s].w};
-        uint32_t top = 0;
+      for (int u = 0; u < U; ++u) {
+        const int vi = (c0 + 32 * u) / LV;
+        const __nv_bfloat16* const src = vi < heads ? k + vi * K.sh : v + (vi - heads) * V.sh;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+        for (int i = 0; i < NL; ++i) x[u][i] = vi < 2 * heads ? ldg_stream(src + 8 * i) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-        for (int o = LV / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(FULL, top, o));
-        // least e with max <= 448 * 2^e = 1.75 * 2^(e + 8)
-        const int e = max(EXP_MIN, (int)(top >> 7) - EXP_BIAS - 8 + ((top & 0x7fu) > 0x60u));
-        const bool bad = top >= 0x7f80u;
-        const float inv = __int_as_float((EXP_BIAS - e) << 23);
-        uint2 c;
-        c.x = pack_e4m3(bf_lo(w[0]) * inv, bf_hi(w[0]) * inv, bf_lo(w[1]) * inv, bf_hi(w[1]) * inv);
-        c.y = pack_e4m3(bf_lo(w[2]) * inv, bf_hi(w[2]) * inv, bf_lo(w[3]) * inv, bf_hi(w[3]) * inv);
-        if (bad) c = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-        if (slot >= 0) {
-          *(uint2*)(dst + vec * D + lane * 8) = c;
-          if (lane == 0) (s ? P.vs : P.ks)[vec] = (uint8_t)(bad ? BYTE_NAN : e + EXP_BIAS);
+      for (int u = 0; u < U; ++u) {
+        const int vi = (c0 + 32 * u) / LV;
+        const bool in = vi < 2 * heads, is_v = vi >= heads;
+        const long long vec = vec0 + ((long long)(is_v ? vi - heads : vi) << B.page_shift);
+        char* const dst = (char*)(is_v ? P.v : P.k);
+        if constexpr (!FP8) {
+          if (in) *(uint4*)(dst + (vec * D + piece * E) * 2) = x[u][0];
+        } else {
+          // magnitudes as bf16 bit patterns order like the values, infinities and NaN above all
+          uint32_t top = 0, c[4];
+#pragma unroll
+          for (int i = 0; i < NL; ++i) {
+            const uint32_t w[4] = {x[u][i].x, x[u][i].y, x[u][i].z, x[u][i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+          }
+#pragma unroll
+          for (int o = LV / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(FULL, top, o));
+          // least e with max <= 448 * 2^e = 1.75 * 2^(e + 8)
+          const int e = max(EXP_MIN, (int)(top >> 7) - EXP_BIAS - 8 + ((top & 0x7fu) > 0x60u));
+          const bool bad = top >= 0x7f80u;
+          const float inv = __int_as_float((EXP_BIAS - e) << 23);
+#pragma unroll
+          for (int i = 0; i < NL; ++i) {
+            const uint4 w = x[u][i];
+            c[2 * i] = pack_e4m3(bf_lo(w.x) * inv, bf_hi(w.x) * inv, bf_lo(w.y) * inv, bf_hi(w.y) * inv);
+            c[2 * i + 1] = pack_e4m3(bf_lo(w.z) * inv, bf_hi(w.z) * inv, bf_lo(w.w) * inv, bf_hi(w.w) * inv);
+          }
+          if (bad) c[0] = c[1] = c[2] = c[3] = 0x7f7f7f7fu;
+          if (in) {
+            *(uint4*)(dst + vec * D + piece * E) = make_uint4(c[0], c[1], c[2], c[3]);
+            if (piece == 0) (is_v ? P.vs : P.ks)[vec] = (uint8_t)(bad ? BYTE_NAN : e + EXP_BIAS);
+          }
         }
       }
     }
@@ -74,50 +125,55 @@ __global__ void __launch_bounds__(256) sa_append_kernel(Batch B, Pool P, Rows K,
 }
 
 // ---------------------------------------------------------------------- read
-// The reverse of append, one 16-byte store per lane.
+// The reverse of append.
 template <int D, bool FP8>
-__global__ void __launch_bounds__(256) sa_read_kernel(Batch B, Pool P, uint4* ko, uint4* vo, int heads) {
-  constexpr int LV = D / 8;
+__global__ void __launch_bounds__(128) sa_read_kernel(Batch B, Pool P, __nv_bfloat16* ko, __nv_bfloat16* vo, int heads) {
+  constexpr int E = piece_of<FP8>, LV = D / E;
   flag_invalid_seqs(B);
-  const long long n = (long long)B.n_tokens * heads * LV;
-  const uint32_t nan2 = 0x7fc07fc0u;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
-    const int lane = (int)(i % LV);
-    const long long th = i / LV;
-    const int t = (int)(th / heads), head = (int)(th - (long long)t * heads);
-    int b, pos;
-    if (!token_place(B, t, b, pos)) {
-      if (lane == 0) B.flags[0] = 1;
-      if (find_seq(B, t) >= 0) ko[i] = vo[i] = make_uint4(nan2, nan2, nan2, nan2);
-      continue;
+  const int lane = threadIdx.x & 31, piece = lane % LV;
+  const int pieces = 2 * heads * LV;              // keys, then values
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (t < B.n_tokens) {
+    int slot = 0;
+    const int page = find_page(B, t, lane, slot);
+    if (page == NO_ROW) return;
+    __nv_bfloat16 *const kt = ko + (size_t)t * heads * D, *const vt = vo + (size_t)t * heads * D;
+    if (page < 0) {
+      const uint32_t f = page == INVALID ? 0x7fc07fc0u : 0;
+      for (int c = lane; c < heads * (D / 8); c += 32) ((uint4*)kt)[c] = ((uint4*)vt)[c] = make_uint4(f, f, f, f);
+      return;
     }
-    const long long slot = find_slot(B, b, pos);
-    if (slot < 0) {
-      if (slot == -2 && lane == 0) B.flags[0] = 1;
-      const uint32_t f = slot == -2 ? nan2 : 0;
-      ko[i] = vo[i] = make_uint4(f, f, f, f);
-      continue;
-    }
-    const long long vec = vec_index(slot, head, heads, B.page_shift);
+    const long long vec0 = (((long long)page * heads) << B.page_shift) + slot;
+    for (int c0 = lane; c0 < pieces; c0 += 32 * U) {
+      uint4 x[U];
+      float f[U];
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const char* src = (const char*)(s ? P.v : P.k);
-      uint4 y;
-      if constexpr (!FP8) {
-        y = ldg_stream(src + (vec * D + lane * 8) * 2);
-      } else {
-        const uint2 c = __ldg((const uint2*)(src + vec * D + lane * 8));
-        const float f = scale_of(__ldg((s ? P.vs : P.ks) + vec));
-        const uint32_t w[2] = {c.x, c.y};
-        uint32_t r[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 z = f16x2_to_f32(e4m3_to_f16x2((uint16_t)(w[j >> 1] >> (16 * (j & 1)))));
-          r[j] = pack_bf16(z.x * f, z.y * f);
-        }
-        y = make_uint4(r[0], r[1], r[2], r[3]);
+      for (int u = 0; u < U; ++u) {
+        const int vi = (c0 + 32 * u) / LV;
+        const bool is_v = vi >= heads;
+        const long long vec = vec0 + ((long long)(is_v ? vi - heads : vi) << B.page_shift);
+        if (vi >= 2 * heads) continue;
+        x[u] = ldg_stream((const char*)(is_v ? P.v : P.k) + (vec * D + piece * E) * (FP8 ? 1 : 2));
+        if constexpr (FP8) f[u] = scale_of(__ldg((is_v ? P.vs : P.ks) + vec));
       }
-      (s ? vo : ko)[i] = y;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int vi = (c0 + 32 * u) / LV;
+        if (vi >= 2 * heads) continue;
+        uint4* const dst = (uint4*)((vi < heads ? kt + vi * D : vt + (vi - heads) * D) + piece * E);
+        if constexpr (!FP8) {
+          *dst = x[u];
+        } else {
+          const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+          uint32_t r[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 z = f16x2_to_f32(e4m3_to_f16x2((uint16_t)(w[j >> 1] >> (16 * (j & 1)))));
+            r[j] = pack_bf16(z.x * f[u], z.y * f[u]);
+          }
+          st_32(dst, r);
+        }
+      }
     }
   }
 }
@@ -190,15 +246,13 @@ extern "C" int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const
   const cudaStream_t s = (cudaStream_t)cuda_stream;
   const Batch B = batch_of(h, batch, pool);
   const Pool P = pool_of(pool);
-  const int per = 256 / (h->D / 8);
-  const long long n = ((long long)B.n_tokens * h->kv_heads + per - 1) / per;
-  const int grid = (int)(n < h->n_sm * 16 ? n : h->n_sm * 16);
+  const int grid = (B.n_tokens + 3) / 4;           // four warps a block, a token each
   if (h->D == 128) {
-    if (pool->dtype == SV_E4M3) sa_append_kernel<128, true><<<grid, 256, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
-    else sa_append_kernel<128, false><<<grid, 256, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
+    if (pool->dtype == SV_E4M3) sa_append_kernel<128, true><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
+    else sa_append_kernel<128, false><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
   } else {
-    if (pool->dtype == SV_E4M3) sa_append_kernel<64, true><<<grid, 256, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
-    else sa_append_kernel<64, false><<<grid, 256, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
+    if (pool->dtype == SV_E4M3) sa_append_kernel<64, true><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
+    else sa_append_kernel<64, false><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
   }
   return launched();
 }
@@ -209,19 +263,18 @@ extern "C" int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const s
   int rc;
   if ((rc = check_pool(h, pool)) || (rc = check_batch(h, batch))) return rc;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return SV_OK;
-  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return SV_ERR_ARG;
+  if (!k_out || !v_out || ((uintptr_t)k_out | (uintptr_t)v_out) & 31) return SV_ERR_ARG;   // 32-byte stores
   const cudaStream_t s = (cudaStream_t)cuda_stream;
   const Batch B = batch_of(h, batch, pool);
   const Pool P = pool_of(pool);
-  const long long n = ((long long)B.n_tokens * h->kv_heads * (h->D / 8) + 255) / 256;
-  const int grid = (int)(n < h->n_sm * 16 ? n : h->n_sm * 16);
-  uint4 *ko = (uint4*)k_out, *vo = (uint4*)v_out;
+  const int grid = (B.n_tokens + 3) / 4;           // four warps a block, a token each
+  __nv_bfloat16 *ko = (__nv_bfloat16*)k_out, *vo = (__nv_bfloat16*)v_out;
   if (h->D == 128) {
-    if (pool->dtype == SV_E4M3) sa_read_kernel<128, true><<<grid, 256, 0, s>>>(B, P, ko, vo, h->kv_heads);
-    else sa_read_kernel<128, false><<<grid, 256, 0, s>>>(B, P, ko, vo, h->kv_heads);
+    if (pool->dtype == SV_E4M3) sa_read_kernel<128, true><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
+    else sa_read_kernel<128, false><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
   } else {
-    if (pool->dtype == SV_E4M3) sa_read_kernel<64, true><<<grid, 256, 0, s>>>(B, P, ko, vo, h->kv_heads);
-    else sa_read_kernel<64, false><<<grid, 256, 0, s>>>(B, P, ko, vo, h->kv_heads);
+    if (pool->dtype == SV_E4M3) sa_read_kernel<64, true><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
+    else sa_read_kernel<64, false><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
   }
   return launched();
 }
