@@ -52,6 +52,7 @@ constexpr int SMEM_LIMIT = 232448;
 constexpr int SETUP = 3;            // units of an item besides its blocks
 constexpr int SNAP = 3;             // units that a run gives up or takes on to end with an item (SETUP at least)
 constexpr int MIN_RUN = 3;          // units of a CTA at least
+constexpr int ODD_NONE = 0x7f7f7f7f;
 constexpr int EV_MIN = -100;        // least exponent of a value block's reference (see convert)
 
 struct AttnParams {
@@ -66,6 +67,7 @@ struct AttnParams {
   float* lse;
   float* ws;                        // partials: [cta][2][MT] of PART floats
   int* counters;                    // [cta][MT], zero between calls
+  int* odd;                         // [cta][4][3][D] first keys with values that are not finite (see mask_values), else ODD_NONE
 };
 
 // Floats of one partial: M, l and its correction per row, then O as [D / 4][128] float4
@@ -304,6 +306,34 @@ struct Walker {
   }
 };
 
+// --------------------------------------------- values that are not finite
+// Causal rows see a prefix of the keys, so what such values do to a row follows
+// from three keys per column: the first with NaN, +inf and -inf.  Only blocks
+// that some rows see in part, and those whose weights come in two parts, need
+// this; elsewhere the products carry it.
+template <int D, bool FP8, typename Piece>
+__device__ __forceinline__ void note_odd(int* odd, int* flag, Piece piece, int half, int key) {
+#pragma unroll 1
+  for (int i = 0; i < D / 16; ++i) {
+    uint16_t* const v = (uint16_t*)piece(i);
+#pragma unroll 1
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t w = v[e], inf = FP8 ? 0x7c00u : 0x7f80u;
+      if ((w & inf) != inf) continue;
+      v[e] = 0;
+      const int kind = (w & 0x7fffu) != inf ? 0 : w >> 15 ? 2 : 1;
+      atomicMin(odd + kind * D + half * (D / 2) + 8 * i + e, key);
+    }
+  }
+  __threadfence();
+  *(volatile int*)flag = 1;
+}
+// What a row that sees keys 0 .. lim-1 has in a column (0: nothing)
+template <int D> __device__ __forceinline__ float odd_value(const int* odd, int col, int lim) {
+  const bool nan = __ldcg(odd + col) < lim, pos = __ldcg(odd + D + col) < lim, neg = __ldcg(odd + 2 * D + col) < lim;
+  return nan || (pos && neg) ? quiet_nan() : pos ? INFINITY : neg ? -INFINITY : 0.0f;
+}
+
 // -------------------------------------------------------------------- kernel
 template <int D, int KIND, int MT>
 struct Cfg {
@@ -351,6 +381,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
                  q_full = o_done + 16, q_empty = q_full + 8, drain = q_empty + 8;
   static_assert(8 * (2 * NK + 2 * NV + 2 * C::NRAW + 9) <= 320, "barrier area");
   int* const work = (int*)(small + 320);                  // tensor-memory base, plan, merge flags [16]
+  int* const odd_flag = (int*)(small + 640);              // whether a run has values that are not finite in such a block [4]
   float2* const info = (float2*)(small + 384);            // block references of an e4m3 cache [INFO]
   int* const red = (int*)(small + 448);                   // planning (20 sums of 8 bytes), then the converters' maxima
   Segment* const runs = (Segment*)(small + 768);          // runs as the query warps announce them [4]
@@ -372,6 +403,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     bar_init(q_full, C::FP8 ? C::Q_WARPS : 1);
     bar_init(q_empty, 1);
     bar_init(drain, 1);
+    for (int i = 0; i < 4; ++i) odd_flag[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -745,6 +777,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       wait_scores();
       if (group_or(group_bar, NS, !ok)) break;             // all warps of the tile leave, or none
       const Segment& g = runs[segs & 3];                   // announced before its first scores
+      const unsigned slot = segs & 3;
       const int j0 = g.j0, j1 = g.j1, lim = A.causal ? g.lim0 + tk : g.kv;
       float c = A.c;
       float M = -INFINITY, l = 0.0f, off = 0.0f;
@@ -802,16 +835,33 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           M = up;
           if (group_or(pair, 64, !ok)) { ok = false; break; }   // both have read; both leave, or none
         }
-        if (!C::FP8 && tile == 0 && (j + 1) * BN > g.kv) {
-          // slots past the sequence's end may hold anything, and a weight of 0 does not clear NaN:
-          // the threads of row r clear value row r
+        const bool split = two_parts<KIND>(g);
+        if (tile == 0 && (split || (j + 1) * BN > (A.causal ? min(g.lim0, g.kv) : g.kv))) {
+          // Some rows do not see all of these keys (or the second part of a weight may be 0), and a weight
+          // of 0 does not clear an infinity or NaN.
+          // The threads of row r look after value row r: slots past the sequence's end, which may hold
+          // anything, become 0, and so does what is not finite, after its key is noted in its column.
           ok = bar_wait(v_full + 8 * (n % NV), (n / NV) & 1, flags);
-          if (ok && j * BN + r >= g.kv) {
+          if (ok) {
+            const int key = j * BN + r;
             uint8_t* const line = gbase + (v_at - base) + (n % NV) * C::BUF + r * 128;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
+            auto piece = [&](int i) {                      // 16-byte piece i of this half row, 8 values
               const int ch = half * (D / 16) + i;
-              *(uint4*)(line + (ch / 8) * HALF_BYTES + (ch % 8) * 16) = make_uint4(0, 0, 0, 0);
+              return (uint4*)(line + (ch / 8) * HALF_BYTES + (((ch % 8) ^ (r & 7)) << 4));
+            };
+            if (key >= g.kv) {
+              if (!C::FP8)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) *piece(i) = make_uint4(0, 0, 0, 0);
+            } else {
+              constexpr uint32_t EXP = C::FP8 ? 0x7c007c00u : 0x7f807f80u;
+              uint32_t found = 0;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint4 w = *piece(i);
+                found |= __vcmpeq2(w.x & EXP, EXP) | __vcmpeq2(w.y & EXP, EXP) | __vcmpeq2(w.z & EXP, EXP) | __vcmpeq2(w.w & EXP, EXP);
+              }
+              if (found) note_odd<D, C::FP8>(A.odd + (blockIdx.x * 4 + slot) * 3 * D, odd_flag + slot, piece, half, key);
             }
           }
           fence_async();
@@ -819,7 +869,6 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const float neg = ev - (M == -INFINITY ? 0.0f : M);
         const u64 c2 = pk(cb, cb), n2 = pk(neg, neg);
         u64 acc[2] = {0, 0};
-        const bool split = two_parts<KIND>(g);
         // exponentials, their sum, and the weights in 16 bits in place of their scores: 32 scores become 16
         // columns of weights and 16 of what rounding left of them
 #pragma unroll
@@ -907,6 +956,13 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             }
           }
         }
+        if (*(volatile int*)(odd_flag + slot) && have) {
+#pragma unroll 1
+          for (int col = half * DH; col < half * DH + DH; ++col) {
+            const float x = odd_value<D>(A.odd + (blockIdx.x * 4 + slot) * 3 * D, col, lim);
+            if (x != 0.0f) A.out[at * D + col] = __float2bfloat16(x + 0.0f * l);   // NaN rows stay NaN
+          }
+        }
         if (A.lse && have && half == 0) A.lse[at] = (M + log2f(l)) * LN2_F;
       } else {
         // partial: slot 1 of this CTA holds an item's beginning, slot 0 a later part
@@ -931,6 +987,13 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           }
         }
         // runs that hold the item: cut x is at units x / ctas, or moved to the end of an item
+        if (*(volatile int*)(odd_flag + slot) && have) {
+#pragma unroll 1
+          for (int col = half * DH; col < half * DH + DH; ++col) {
+            const float x = odd_value<D>(A.odd + (blockIdx.x * 4 + slot) * 3 * D, col, lim);
+            if (x != 0.0f) __stcg(dst + 3 * BM + (col / 4 * BM + r) * 4 + col % 4, x);
+          }
+        }
         const long long begin = g.start - SETUP;
         const int c0 = (int)(((begin + SNAP + 1) * ctas - 1) / units), c1 = (int)(((g.start + g.nblk - SNAP) * ctas - 1) / units);
         __threadfence();
@@ -1040,6 +1103,13 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           }
         }
       }
+      const unsigned past = (slot + 2) & 3;                // the run before the last: both tiles are past it
+      if (tile == 0 && *(volatile int*)(odd_flag + past)) {
+        for (int i = ts; i < 3 * D; i += NS) __stcg(A.odd + (blockIdx.x * 4 + past) * 3 * D + i, ODD_NONE);
+        __threadfence();
+        group_sync(group_bar, NS);
+        if (ts == 0) *(volatile int*)(odd_flag + past) = 0;
+      }
       tc_before();
       if (!g.more) break;
     } while (true);
@@ -1133,6 +1203,8 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   }
   tc_before();
   __syncthreads();
+  for (int i = tid; i < 4 * 3 * D; i += NT)                // the last runs' notes
+    if (odd_flag[i / (3 * D)]) A.odd[blockIdx.x * 4 * 3 * D + i] = ODD_NONE;
   if (warp == 1) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));

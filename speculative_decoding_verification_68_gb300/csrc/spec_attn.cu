@@ -187,11 +187,12 @@ struct spec_attn_ctx {
   int* d_flags;
   float* ws;                         // partial results of the split attention
   int* counters;
+  int* odd;                          // notes on values that are not finite
 };
 
 static void free_ctx(spec_attn_ctx* h) {
   if (!h) return;
-  void* ptrs[] = {h->d_flags, h->ws, h->counters};
+  void* ptrs[] = {h->d_flags, h->ws, h->counters, h->odd};
   for (void* p : ptrs)
     if (p) cudaFree(p);
   free(h);
@@ -283,6 +284,8 @@ extern "C" int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const s
 constexpr int MT_MAX = 2;
 static size_t ws_bytes(int n_sm, int D) { return (size_t)n_sm * 2 * MT_MAX * (D == 128 ? part_floats<128>() : part_floats<64>()) * sizeof(float); }
 
+static size_t odd_bytes(const spec_attn_ctx* h) { return (size_t)h->n_sm * 4 * 3 * h->D * sizeof(int); }
+
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 static EncodeTiled encode_tiled() {
@@ -341,7 +344,7 @@ static AttnParams attn_params(const spec_attn_ctx* h, const Batch& B, const Rows
   A.causal = causal != 0;
   A.c = fmaxf(scale * LOG2E_F, 1.17549435e-38f);
   A.out = (__nv_bfloat16*)out; A.lse = lse;
-  A.ws = h->ws; A.counters = h->counters;
+  A.ws = h->ws; A.counters = h->counters; A.odd = h->odd;
   return A;
 }
 
@@ -367,6 +370,7 @@ extern "C" int spec_attn_init(spec_attn_t* out, int q_heads, int kv_heads, int h
   const size_t counters = (size_t)h->n_sm * MT_MAX * sizeof(int);
   if (cudaMalloc(&h->d_flags, 4 * sizeof(int)) != cudaSuccess || cudaMemset(h->d_flags, 0, 4 * sizeof(int)) != cudaSuccess ||
       cudaMalloc(&h->counters, counters) != cudaSuccess || cudaMemset(h->counters, 0, counters) != cudaSuccess ||
+      cudaMalloc(&h->odd, odd_bytes(h)) != cudaSuccess || cudaMemset(h->odd, ODD_NONE & 0xff, odd_bytes(h)) != cudaSuccess ||
       cudaMalloc(&h->ws, ws_bytes(h->n_sm, head_dim)) != cudaSuccess) {
     cudaGetLastError();
     free_ctx(h);
@@ -425,8 +429,9 @@ extern "C" int spec_attn_get_error(spec_attn_t h) {
   int f[2] = {0, 0};
   if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(f, h->d_flags, sizeof f, cudaMemcpyDeviceToHost) != cudaSuccess ||
       cudaMemset(h->d_flags, 0, sizeof f) != cudaSuccess ||
-      // a call whose wait expired may have left its merge counters behind
-      (f[1] && cudaMemset(h->counters, 0, (size_t)h->n_sm * MT_MAX * sizeof(int)) != cudaSuccess)) {
+      // a call whose wait expired may have left its merge counters and notes behind
+      (f[1] && (cudaMemset(h->counters, 0, (size_t)h->n_sm * MT_MAX * sizeof(int)) != cudaSuccess ||
+                cudaMemset(h->odd, ODD_NONE & 0xff, odd_bytes(h)) != cudaSuccess))) {
     cudaGetLastError();
     return SV_ERR_CUDA;
   }

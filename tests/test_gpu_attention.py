@@ -228,6 +228,60 @@ def test_one_path_from_prompt_to_verification_step(lib):
     assert ((got - whole[is_new]).abs().float() <= 2.0 ** -6 * vv.abs().amax().float()).all()
 
 
+# ------------------------------------------- what a row does not see is not there
+@pytest.mark.parametrize("hq, hkv, d, dtype", [(16, 2, 128, BF16), (10, 2, 64, BF16), (8, 8, 128, BF16), (16, 2, 128, E4M3), (6, 2, 64, E4M3)])
+@pytest.mark.parametrize("new, old", [([150, 3], [40, 300]), ([8, 8], [250, 500]), ([400], [700])])
+def test_later_tokens_that_are_not_finite_leave_earlier_rows_alone(lib, new, old, hq, hkv, d, dtype):
+    w = World(new, old, hq, hkv, d, 32, dtype, seed=14)
+    expected = w.expect_attention()
+    attn, pool, where = setup(lib, w)
+    at = [max(1, n // 2) for n in new]                       # new token of each sequence with bad vectors
+    cols = {5: float("nan"), 6: float("inf"), d - 1: float("-inf")}
+    q = w.q.cuda()
+    for b, i in enumerate(at):
+        pos = w.kv[b] - new[b] + i
+        page, slot = w.table[b, pos // 32], pos % 32
+        if dtype == BF16:
+            pool.k[page, :, slot, 3] = float("nan")
+            for col, x in cols.items():
+                pool.v[page, :, slot, col] = x
+        else:
+            pool.k_scale[page, :, slot] = pool.v_scale[page, :, slot] = 255
+            pool.k.view(torch.uint8)[page, :, slot] = pool.v.view(torch.uint8)[page, :, slot] = 0x7f
+    got = attn.attend(pool, q, *where, want_lse=True)
+    again = attn.attend(pool, q, *where, want_lse=True)
+    assert attn.get_error() == lib.SV_OK
+    assert torch.equal(got["out"].view(torch.int16), again["out"].view(torch.int16))
+    for b, i in enumerate(at):
+        clean = slice(w.cu[b], w.cu[b] + i)
+        assert_attention(got["out"][clean], got["lse"][clean], [x[clean] for x in expected])
+        assert torch.isnan(got["out"][w.cu[b] + i:w.cu[b + 1]]).all()      # they see a key of NaN
+
+
+@pytest.mark.parametrize("hq, hkv, d", [(8, 2, 128), (4, 4, 64)])
+@pytest.mark.parametrize("n", [100, 300, 900])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them(lib, n, hq, hkv, d):
+    w = World([n], [0], hq, hkv, d, 16, BF16, seed=15)
+    bad = {3: (n // 3, float("nan")), 4: (n // 2, float("inf")), 5: (n - 1, float("-inf")), d - 2: (0, float("inf"))}
+    v = w.v_new.clone()
+    for col, (i, x) in bad.items():
+        v[i, :, col] = x
+    w.kc[0], w.vc[0] = w.k_new.double().numpy(), w.v_new.double().numpy()
+    attn = lib.SpecAttention(hq, hkv, d, 1)
+    got = attn.prompt(w.q.cuda(), w.k_new.cuda(), v.cuda(), torch.from_numpy(w.cu).cuda(), want_lse=True)
+    assert attn.get_error() == lib.SV_OK
+    out = got["out"].float().cpu()
+    for col, (i, x) in bad.items():
+        seen = out[i:, :, col]
+        assert torch.isnan(seen).all() if x != x else (seen == x).all()
+        assert torch.isfinite(out[:i, :, col]).all()
+    ref = w.expect_attention()
+    keep = np.ones(d, bool)
+    keep[list(bad)] = False
+    fixed = np.where(keep, got["out"].double().cpu().numpy(), ref[0])
+    assert_attention(torch.from_numpy(fixed), got["lse"], ref)
+
+
 # --------------------------------------------------- streams, graphs, repeats
 def test_calls_repeat_bit_for_bit_and_in_a_graph_on_another_stream(lib):
     w = World([8, 1, 30], [900, 2500, 33], 16, 2, 128, 32, BF16, seed=11)
