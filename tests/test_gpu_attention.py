@@ -308,6 +308,50 @@ def test_calls_repeat_bit_for_bit_and_in_a_graph_on_another_stream(lib):
     assert attn.get_error() == lib.SV_OK
 
 
+@pytest.mark.parametrize("dtype, hq, n", [(BF16, 64, 8), (E4M3, 64, 16), (BF16, 32, 1), (BF16, 32, 200)])
+def test_long_ragged_contexts_from_cold_memory(lib, dtype, hq, n):
+    """Runs of dozens of blocks whose copies keep the products waiting, against a
+    float64 softmax on the GPU, twice with the same bits."""
+    seqs, hkv, d, page = (24 if n < 100 else 3), 8, 128, 32
+    g = torch.Generator(device="cuda").manual_seed(16)
+    r = np.random.default_rng(16)
+    kv = [int(x) for x in r.integers(max(300, n), 5000, seqs)]
+    need = [-(-x // page) for x in kv]
+    order = torch.randperm(sum(need), generator=g, device="cuda").int()
+    table = torch.zeros((seqs, max(need)), dtype=torch.int32, device="cuda")
+    for b, c in enumerate(need):
+        table[b, :c] = order[sum(need[:b]):sum(need[:b]) + c]
+    attn = lib.SpecAttention(hq, hkv, d, seqs)
+    pool = attn.alloc_pool(sum(need), page, dtype)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(kv)]), dtype=torch.int32, device="cuda")
+    kv_len = torch.tensor(kv, dtype=torch.int32, device="cuda")
+    k, v = (torch.randn((sum(kv), hkv, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    attn.append(pool, k, v, cu, kv_len, table)
+    back = attn.read(pool, cu, kv_len, table, n_tokens=sum(kv))          # as the cache holds them
+    q = torch.randn((seqs * n, hq, d), generator=g, device="cuda").bfloat16()
+    new = torch.arange(0, seqs * n + 1, n, dtype=torch.int32, device="cuda")
+    cold = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    got = []
+    for _ in range(3):
+        cold.zero_()
+        got.append(attn.attend(pool, q, new, kv_len, table, want_lse=True))
+    assert attn.get_error() == lib.SV_OK
+    assert all(torch.equal(x[name], got[0][name]) for x in got for name in x)
+    for b in range(seqs):
+        rows, lo, hi = slice(b * n, b * n + n), sum(kv[:b]), sum(kv[:b + 1])
+        kk, vv = (back[x][lo:hi].double().repeat_interleave(hq // hkv, 1) for x in ("k", "v"))
+        s = torch.einsum("nhd,lhd->nhl", q[rows].double(), kk) * d ** -0.5
+        last = kv[b] - n + torch.arange(n, device="cuda")
+        s.masked_fill_(torch.arange(kv[b], device="cuda")[None, None] > last[:, None, None], -float("inf"))
+        lse = torch.logsumexp(s, -1)
+        p = torch.exp(s - lse[..., None])
+        ref, spread = torch.einsum("nhl,lhd->nhd", p, vv), torch.einsum("nhl,lhd->nhd", p, vv.abs())
+        # the bounds of tests/_attn.py
+        assert ((got[0]["out"][rows].double() - ref).abs() <= 2.0 ** -9 * ref.abs() + 2.0 ** -8 * spread).all()
+        reach = torch.einsum("nhd,lhd->nhl", q[rows].double().abs(), kk.abs()).amax(-1) * d ** -0.5
+        assert ((got[0]["lse"][rows].double() - lse).abs() <= 2.0 ** -16 * (1 + reach)).all()
+
+
 def test_offsets_beyond_32_bits(lib):
     """Pages whose byte and element offsets pass 2^32 and 2^31."""
     hkv, d, page = 8, 128, 128
