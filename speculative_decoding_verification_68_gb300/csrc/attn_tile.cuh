@@ -50,7 +50,7 @@ constexpr float LAZY = 8.0f;        // log2 of how far scores may pass the refer
 constexpr int POLLS = 1 << 18;      // of a bounded wait (about 1 s)
 constexpr int SMEM_LIMIT = 232448;
 constexpr int SETUP = 3;            // units of an item besides its blocks
-constexpr int SNAP = 3;             // units that a run gives up or takes on to end with an item (SETUP at least)
+constexpr int SNAP = 4;             // units that a run gives up or takes on to end with an item (SETUP at least)
 constexpr int MIN_RUN = 3;          // units of a CTA at least
 constexpr int ODD_NONE = 0x7f7f7f7f;
 constexpr int EV_MIN = -100;        // least exponent of a value block's reference (see convert)

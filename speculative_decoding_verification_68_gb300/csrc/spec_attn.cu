@@ -328,7 +328,7 @@ static bool allow_smem() {
 }
 template <int D>
 static bool allow_smem_all() {
-  return allow_smem<D, KIND_BF16, 1>() && allow_smem<D, KIND_BF16, 2>() && allow_smem<D, KIND_E4M3, 1>() && allow_smem<D, KIND_PACKED, 2>();
+  return allow_smem<D, KIND_BF16, 1>() && allow_smem<D, KIND_BF16, 2>() && allow_smem<D, KIND_E4M3, 1>() && allow_smem<D, KIND_PACKED, 1>() && allow_smem<D, KIND_PACKED, 2>();
 }
 template <int D, int KIND, int MT>
 static int launch_attention(const spec_attn_ctx* h, const AttnParams& A, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
@@ -346,6 +346,19 @@ static AttnParams attn_params(const spec_attn_ctx* h, const Batch& B, const Rows
   A.out = (__nv_bfloat16*)out; A.lse = lse;
   A.ws = h->ws; A.counters = h->counters; A.odd = h->odd;
   return A;
+}
+
+// Two tiles of rows per CTA share every key block, which pays where rows are many and the products bound; one
+// tile makes twice as many items.  Measured, one tile against two: 4 chunks of 300-512 tokens over 6000-16000
+// cached 298 against 244 us; 8 prompts of 100-2048 tokens 89 against 79 us; but 64 sequences of 8 tokens over
+// 500-8000 188 against 230 us, one chunk of 113 over 6096 39 against 75 us, prompts of 25 and 15 tokens 10.6
+// against 13.8 us.  The rule: more rows per sequence and head than one tile holds, and at least 12 blocks of two
+// tiles for every SM (between 9, where one tile still won, and 14).  `keys`: how many a row sees, about.
+constexpr int TWO_TILE_UNITS = 12;
+static bool two_tiles(const spec_attn_ctx* h, const AttnParams& A, long long keys) {
+  const long long rows = ((long long)A.B.n_tokens * A.group + A.B.n_seqs - 1) / A.B.n_seqs;   // of a sequence and head
+  const long long units = A.B.n_seqs * A.kv_heads * ((rows + 2 * BM - 1) / (2 * BM)) * (keys / BN + 1);
+  return rows > BM && units >= (long long)TWO_TILE_UNITS * h->n_sm;
 }
 
 extern "C" int spec_attn_init(spec_attn_t* out, int q_heads, int kv_heads, int head_dim, int max_seqs) {
@@ -398,7 +411,7 @@ extern "C" int spec_attn_chunk(spec_attn_t h, const spec_attn_pool* pool, const 
     A.ks = pool->k_scale; A.vs = pool->v_scale;
     return h->D == 128 ? launch_attention<128, KIND_E4M3, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E4M3, 1>(h, A, mq, mk, mv, s);
   }
-  const bool two = (long long)B.n_tokens * A.group > (long long)B.n_seqs * BM;   // more rows per sequence and head than one tile holds
+  const bool two = two_tiles(h, A, (long long)B.max_pages << B.page_shift);
   if (h->D == 128) return two ? launch_attention<128, KIND_BF16, 2>(h, A, mq, mk, mv, s) : launch_attention<128, KIND_BF16, 1>(h, A, mq, mk, mv, s);
   return two ? launch_attention<64, KIND_BF16, 2>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_BF16, 1>(h, A, mq, mk, mv, s);
 }
@@ -421,7 +434,9 @@ extern "C" int spec_attn_prompt(spec_attn_t h, int n_seqs, int n_tokens, const i
   if (!map_queries(&mq, h, A) || !map_rows(&mk, h->D, h->kv_heads, rows_of(k), n_tokens, 1, BN) ||
       !map_rows(&mv, h->D, h->kv_heads, rows_of(v), n_tokens, 1, BN))
     return SV_ERR_ARG;
-  return h->D == 128 ? launch_attention<128, KIND_PACKED, 2>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_PACKED, 2>(h, A, mq, mk, mv, s);
+  const bool two = two_tiles(h, A, n_tokens / n_seqs / 2);
+  if (h->D == 128) return two ? launch_attention<128, KIND_PACKED, 2>(h, A, mq, mk, mv, s) : launch_attention<128, KIND_PACKED, 1>(h, A, mq, mk, mv, s);
+  return two ? launch_attention<64, KIND_PACKED, 2>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_PACKED, 1>(h, A, mq, mk, mv, s);
 }
 
 extern "C" int spec_attn_get_error(spec_attn_t h) {
