@@ -47,6 +47,7 @@ constexpr int BN = 128;             // keys per block
 constexpr int BM = 128;             // rows per tile (tensor-memory lanes)
 constexpr int HALF_BYTES = BN * 128;  // 64 of the D columns of a block: 128 rows of one swizzled 128-byte line
 constexpr float LAZY = 8.0f;        // log2 of how far scores may pass the reference
+constexpr float ABOVE = 1.0f + 1.0f / 65536.0f;
 constexpr int POLLS = 1 << 18;      // of a bounded wait (about 1 s)
 constexpr int SMEM_LIMIT = 232448;
 constexpr int SETUP = 3;            // units of an item besides its blocks
@@ -269,8 +270,9 @@ struct Segment {      // a run of blocks of one item
 
 // Rounding the weights to bf16 costs little where many keys share the error.
 // An item of few blocks has its weights in two bf16 parts and takes the product
-// with the values twice.
-template <int KIND> __device__ __forceinline__ bool two_parts(const Segment& g) { return KIND != KIND_E4M3 && g.nblk <= 3; }
+// with the values twice: up to 1152 keys where copies bound (one tile: 1% of the
+// time over the range, 2% up to 2048), up to 384 where the products do.
+template <int KIND, int MT> __device__ __forceinline__ bool two_parts(const Segment& g) { return KIND != KIND_E4M3 && g.nblk <= (MT == 1 ? 9 : 3); }
 
 // Walks one CTA's run of units.  Every role walks on its own.
 struct Walker {
@@ -309,8 +311,7 @@ struct Walker {
 // --------------------------------------------- values that are not finite
 // Causal rows see a prefix of the keys, so what such values do to a row follows
 // from three keys per column: the first with NaN, +inf and -inf.  Only blocks
-// that some rows see in part, and those whose weights come in two parts, need
-// this; elsewhere the products carry it.
+// that some rows see in part need this; elsewhere the products carry it.
 template <int D, bool FP8, typename Piece>
 __device__ __forceinline__ void note_odd(int* odd, int* flag, Piece piece, int half, int key) {
 #pragma unroll 1
@@ -600,7 +601,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         auto wait_v = [&](unsigned i) { return bar_wait1(v_full + 8 * (i % NV), (i / NV) & 1, flags); };
         while (ok && W.next(A, tile_rows, g)) {
           const int nb = g.j1 - g.j0;
-          const bool split = two_parts<KIND>(g);
+          const bool split = two_parts<KIND, MT>(g);
           if (!(ok = bar_wait1(q_full, segs++ & 1, flags))) break;
           if constexpr (MT == 2) {
             if (!(ok = wait_k(n))) break;
@@ -781,6 +782,38 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       const int j0 = g.j0, j1 = g.j1, lim = A.causal ? g.lim0 + tk : g.kv;
       float c = A.c;
       float M = -INFINITY, l = 0.0f, off = 0.0f;
+      const bool split = two_parts<KIND, MT>(g);
+      // Some rows do not see all of a block's keys, and a weight of 0 does not clear an infinity or NaN.
+      auto care = [&](int j) {
+        if (tile == 0 && (j + 1) * BN > (A.causal ? min(g.lim0, g.kv) : g.kv)) {
+          // The threads of row r look after value row r: slots past the sequence's end, which may hold
+          // anything, become 0, and so does what is not finite, after its key is noted in its column.
+          if (ok) ok = bar_wait(v_full + 8 * (n % NV), (n / NV) & 1, flags);
+          if (ok) {
+            const int key = j * BN + r;
+            uint8_t* const line = gbase + (v_at - base) + (n % NV) * C::BUF + r * 128;
+            auto piece = [&](int i) {                      // 16-byte piece i of this half row, 8 values
+              const int ch = half * (D / 16) + i;
+              return (uint4*)(line + (ch / 8) * HALF_BYTES + (((ch % 8) ^ (r & 7)) << 4));
+            };
+            if (key >= g.kv) {
+              if (!C::FP8)
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) *piece(i) = make_uint4(0, 0, 0, 0);
+            } else {
+              constexpr uint32_t EXP = C::FP8 ? 0x7c007c00u : 0x7f807f80u;
+              uint32_t found = 0;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) {
+                const uint4 w = *piece(i);
+                found |= __vcmpeq2(w.x & EXP, EXP) | __vcmpeq2(w.y & EXP, EXP) | __vcmpeq2(w.z & EXP, EXP) | __vcmpeq2(w.w & EXP, EXP);
+              }
+              if (found) note_odd<D, C::FP8>(A.odd + (blockIdx.x * 4 + slot) * 3 * D, odd_flag + slot, piece, half, key);
+            }
+          }
+          fence_async();
+        }
+      };
       for (int j = j0; j < j1; ++j, ++n) {
         const unsigned buf = MT == 2 ? tile : n & 1;
         const uint32_t s_at = S_COL + buf * 128 + lane_at + half * 64;
@@ -835,37 +868,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           M = up;
           if (group_or(pair, 64, !ok)) { ok = false; break; }   // both have read; both leave, or none
         }
-        const bool split = two_parts<KIND>(g);
-        if (tile == 0 && (split || (j + 1) * BN > (A.causal ? min(g.lim0, g.kv) : g.kv))) {
-          // Some rows do not see all of these keys (or the second part of a weight may be 0), and a weight
-          // of 0 does not clear an infinity or NaN.
-          // The threads of row r look after value row r: slots past the sequence's end, which may hold
-          // anything, become 0, and so does what is not finite, after its key is noted in its column.
-          ok = bar_wait(v_full + 8 * (n % NV), (n / NV) & 1, flags);
-          if (ok) {
-            const int key = j * BN + r;
-            uint8_t* const line = gbase + (v_at - base) + (n % NV) * C::BUF + r * 128;
-            auto piece = [&](int i) {                      // 16-byte piece i of this half row, 8 values
-              const int ch = half * (D / 16) + i;
-              return (uint4*)(line + (ch / 8) * HALF_BYTES + (((ch % 8) ^ (r & 7)) << 4));
-            };
-            if (key >= g.kv) {
-              if (!C::FP8)
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) *piece(i) = make_uint4(0, 0, 0, 0);
-            } else {
-              constexpr uint32_t EXP = C::FP8 ? 0x7c007c00u : 0x7f807f80u;
-              uint32_t found = 0;
-#pragma unroll
-              for (int i = 0; i < D / 16; ++i) {
-                const uint4 w = *piece(i);
-                found |= __vcmpeq2(w.x & EXP, EXP) | __vcmpeq2(w.y & EXP, EXP) | __vcmpeq2(w.z & EXP, EXP) | __vcmpeq2(w.w & EXP, EXP);
-              }
-              if (found) note_odd<D, C::FP8>(A.odd + (blockIdx.x * 4 + slot) * 3 * D, odd_flag + slot, piece, half, key);
-            }
-          }
-          fence_async();
-        }
+        care(j);
         const float neg = ev - (M == -INFINITY ? 0.0f : M);
         const u64 c2 = pk(cb, cb), n2 = pk(neg, neg);
         u64 acc[2] = {0, 0};
@@ -887,13 +890,20 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               x[32 * h + 2 * i + 1] = __float_as_uint(b);
             }
           }
-          tm_st16(s_at + 32 * h, w);
           if (!C::FP8 && split) {
+            // the first part rounded towards 0, the second with 2^-16 of the weight on top: it is positive
+            // where the weight is, and an infinite value stays one
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w[i] = pack_bf16(__uint_as_float(x[32 * h + 2 * i]) - bf_lo(w[i]), __uint_as_float(x[32 * h + 2 * i + 1]) - bf_hi(w[i]));
-            tm_st16(s_at + 32 * h + 16, w);
+            for (int i = 0; i < 16; ++i) {
+              const uint32_t first = pack_bf16_down(__uint_as_float(x[32 * h + 2 * i]), __uint_as_float(x[32 * h + 2 * i + 1]));
+              float a, b;
+              upk(fma2(pk(__uint_as_float(x[32 * h + 2 * i]), __uint_as_float(x[32 * h + 2 * i + 1])), pk(ABOVE, ABOVE), pk(-bf_lo(first), -bf_hi(first))), a, b);
+              w[i] = first;
+              x[32 * h + i] = pack_bf16(a, b);
+            }
+            tm_st16(s_at + 32 * h + 16, x + 32 * h);
           }
+          tm_st16(s_at + 32 * h, w);
         }
         float s0, s1, s2, s3;
         upk(acc[0], s0, s1);
