@@ -271,8 +271,9 @@ struct Segment {      // a run of blocks of one item
 // Rounding the weights to bf16 costs little where many keys share the error.
 // An item of few blocks has its weights in two bf16 parts and takes the product
 // with the values twice: up to 1152 keys where copies bound (one tile: 1% of the
-// time over the range, 2% up to 2048), up to 384 where the products do.
-template <int KIND, int MT> __device__ __forceinline__ bool two_parts(const Segment& g) { return KIND != KIND_E4M3 && g.nblk <= (MT == 1 ? 9 : 3); }
+// time over the range, 2% up to 2048), up to 128 where the products do (a block of
+// two tiles takes 2.5 instead of 1.6 us).
+template <int KIND, int MT> __device__ __forceinline__ bool two_parts(const Segment& g) { return KIND != KIND_E4M3 && g.nblk <= (MT == 1 ? 9 : 1); }
 
 // Walks one CTA's run of units.  Every role walks on its own.
 struct Walker {
