@@ -184,17 +184,16 @@ __global__ void __launch_bounds__(128) sa_read_kernel(Batch B, Pool P, __nv_bflo
 struct spec_attn_ctx {
   int device, q_heads, kv_heads, D, max_seqs;
   int n_sm;
-  int* d_flags;
-  float* ws;                         // partial results of the split attention
-  int* counters;
+  char* memory;                      // one allocation, of
   int* odd;                          // notes on values that are not finite
+  int* d_flags;
+  int* counters;                     // of the merges
+  float* ws;                         // partial results of the split attention
 };
 
 static void free_ctx(spec_attn_ctx* h) {
   if (!h) return;
-  void* ptrs[] = {h->d_flags, h->ws, h->counters, h->odd};
-  for (void* p : ptrs)
-    if (p) cudaFree(p);
+  if (h->memory) cudaFree(h->memory);
   free(h);
 }
 
@@ -285,6 +284,7 @@ constexpr int MT_MAX = 2;
 static size_t ws_bytes(int n_sm, int D) { return (size_t)n_sm * 2 * MT_MAX * (D == 128 ? part_floats<128>() : part_floats<64>()) * sizeof(float); }
 
 static size_t odd_bytes(const spec_attn_ctx* h) { return (size_t)h->n_sm * 4 * 3 * h->D * sizeof(int); }
+static size_t small_bytes(const spec_attn_ctx* h) { return 256 + ((size_t)h->n_sm * MT_MAX * sizeof(int) + 255) / 256 * 256; }   // flags, counters
 
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -380,15 +380,18 @@ extern "C" int spec_attn_init(spec_attn_t* out, int q_heads, int kv_heads, int h
     free_ctx(h);
     return SV_ERR_CUDA;
   }
-  const size_t counters = (size_t)h->n_sm * MT_MAX * sizeof(int);
-  if (cudaMalloc(&h->d_flags, 4 * sizeof(int)) != cudaSuccess || cudaMemset(h->d_flags, 0, 4 * sizeof(int)) != cudaSuccess ||
-      cudaMalloc(&h->counters, counters) != cudaSuccess || cudaMemset(h->counters, 0, counters) != cudaSuccess ||
-      cudaMalloc(&h->odd, odd_bytes(h)) != cudaSuccess || cudaMemset(h->odd, ODD_NONE & 0xff, odd_bytes(h)) != cudaSuccess ||
-      cudaMalloc(&h->ws, ws_bytes(h->n_sm, head_dim)) != cudaSuccess) {
+  // notes at ODD_NONE, flags and counters at 0, both multiples of 256 bytes; the partials need no initial value
+  const size_t odd = odd_bytes(h), small = small_bytes(h);
+  if (cudaMalloc(&h->memory, odd + small + ws_bytes(h->n_sm, head_dim)) != cudaSuccess || cudaMemset(h->memory, ODD_NONE & 0xff, odd) != cudaSuccess ||
+      cudaMemset(h->memory + odd, 0, small) != cudaSuccess) {
     cudaGetLastError();
     free_ctx(h);
     return SV_ERR_ALLOC;
   }
+  h->odd = (int*)h->memory;
+  h->d_flags = (int*)(h->memory + odd);
+  h->counters = h->d_flags + 64;
+  h->ws = (float*)(h->memory + odd + small);
   *out = h;
   return SV_OK;
 }
@@ -443,10 +446,9 @@ extern "C" int spec_attn_get_error(spec_attn_t h) {
   if (!h) return SV_ERR_ARG;
   int f[2] = {0, 0};
   if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(f, h->d_flags, sizeof f, cudaMemcpyDeviceToHost) != cudaSuccess ||
-      cudaMemset(h->d_flags, 0, sizeof f) != cudaSuccess ||
       // a call whose wait expired may have left its merge counters and notes behind
-      (f[1] && (cudaMemset(h->counters, 0, (size_t)h->n_sm * MT_MAX * sizeof(int)) != cudaSuccess ||
-                cudaMemset(h->odd, ODD_NONE & 0xff, odd_bytes(h)) != cudaSuccess))) {
+      cudaMemset(h->d_flags, 0, small_bytes(h)) != cudaSuccess ||
+      (f[1] && cudaMemset(h->odd, ODD_NONE & 0xff, odd_bytes(h)) != cudaSuccess)) {
     cudaGetLastError();
     return SV_ERR_CUDA;
   }
