@@ -18,24 +18,35 @@
 // The units of all items in order are cut into equal runs, one per CTA (one CTA
 // per SM), so few long sequences fill the GPU as well as many short ones.  A cut
 // within SNAP units of an item's end moves there: splitting an item has a price
-// too.  An item that lies in
-// several runs leaves partial (M, l, O) in the workspace and the last CTA to
-// finish merges them, in order: nothing waits, and results do not depend on
-// the order of arrival.
+// too.  An item that lies in several runs leaves partial (M, l, O) in the
+// workspace and the last CTA to finish merges them, in order: nothing waits,
+// and results do not depend on the order of arrival.
 //
 // Roles of a CTA's warps: one copies key and value blocks into shared memory
 // (TMA), one issues the matrix products, two load the query rows of the next
 // run, and eight per tile do the softmax, two threads a row (a warp reaches
 // only the 32 tensor-memory lanes of its place in its warpgroup).  For an e4m3
 // cache eight more turn the codes into f16 (see below).
+//
+// Tiles.  Two tiles of rows share a CTA's key blocks and take turns: the
+// products of one (about 1,100 cycles a block) run under the softmax of the
+// other.  With one tile two score buffers take turns instead.
+//
+// What bounds it, measured on GB300 (152 SMs, 6.70 TB/s, 1,937 TFLOP/s bf16):
+//   one tile, bf16    memory: 64 sequences of 8 tokens over 500-8000 cached, 64
+//                     query and 8 key-value heads of 128, 188 us, 6.1 TB/s
+//   one tile, e4m3    shared memory and instruction issue: 64 sequences of 16 over
+//                     1000-16000, 292 us, 3.5 TB/s and 865 TFLOP/s
+//   two tiles         a tile's softmax, about 1,600 cycles, where the other's
+//                     products take 1,100: 3 prompts of 4000-6450 tokens, 32 and 8
+//                     heads of 128, 687 us, 1,363 TFLOP/s
+//   few blocks        latency: a call of 3 prompts of up to 21 tokens takes 10.5 us
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
-
-#include <type_traits>
 
 #include "attn_common.cuh"
 
@@ -46,15 +57,18 @@ enum { KIND_BF16 = 0, KIND_E4M3 = 1, KIND_PACKED = 2 };
 constexpr int BN = 128;             // keys per block
 constexpr int BM = 128;             // rows per tile (tensor-memory lanes)
 constexpr int HALF_BYTES = BN * 128;  // 64 of the D columns of a block: 128 rows of one swizzled 128-byte line
-constexpr float LAZY = 8.0f;        // log2 of how far scores may pass the reference
-constexpr float ABOVE = 1.0f + 1.0f / 65536.0f;
+constexpr float LAZY = 8.0f;        // log2 of how far scores may pass the reference: f16 weights hold 2^15
+constexpr float ABOVE = 1.0f + 1.0f / 65536.0f;   // see the weights in two parts
 constexpr int POLLS = 1 << 18;      // of a bounded wait (about 1 s)
 constexpr int SMEM_LIMIT = 232448;
+// Of the run schedule, in units (about 1.6 us with two tiles, 1.2 with one).  Time over 30 cases of all sizes
+// against the values chosen: SETUP and SNAP 2, +2%; SNAP 3, +1%; SNAP 6, +0.4%; SETUP 4, +0.3%; MIN_RUN 2, 5 and
+// 8, +1, +7 and +15%.  Without SETUP and SNAP 8 prompts of 100-2048 tokens take 114 instead of 77 us.
 constexpr int SETUP = 3;            // units of an item besides its blocks
 constexpr int SNAP = 4;             // units that a run gives up or takes on to end with an item (SETUP at least)
 constexpr int MIN_RUN = 3;          // units of a CTA at least
 constexpr int ODD_NONE = 0x7f7f7f7f;
-constexpr int EV_MIN = -100;        // least exponent of a value block's reference (see convert)
+constexpr int EV_MIN = -100;        // least exponent of a value block's reference (see the e4m3 conversion)
 
 struct AttnParams {
   Batch B;
@@ -68,7 +82,7 @@ struct AttnParams {
   float* lse;
   float* ws;                        // partials: [cta][2][MT] of PART floats
   int* counters;                    // [cta][MT], zero between calls
-  int* odd;                         // [cta][4][3][D] first keys with values that are not finite (see mask_values), else ODD_NONE
+  int* odd;                         // [cta][4][3][D] first keys with values that are not finite (see note_odd), else ODD_NONE
 };
 
 // Floats of one partial: M, l and its correction per row, then O as [D / 4][128] float4

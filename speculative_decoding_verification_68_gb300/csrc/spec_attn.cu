@@ -55,13 +55,19 @@ __device__ __forceinline__ int find_page(const Batch& B, int t, int lane, int& s
   if (page <= INVALID && lane == 0) B.flags[0] = 1;
   return page;
 }
-constexpr int U = 2;                              // pieces of a lane in flight
+// Pieces of a lane in flight, and warps of a block.  36K tokens appended to e4m3 pools take 40.1 us with 2
+// pieces, 47.3 with 4, 40.9 with 1 (8 tokens of 256 sequences 4.8, 5.0, 5.0); 39.1 us with 4 warps a block, 40.8
+// with 8, 42.2 with 16.  More loads in flight spread the stores over more pages at once.
+constexpr int U = 2;
 // A piece is 16 bytes of the pool: 8 bf16 values or 16 codes, D / piece of them a vector.
 template <bool FP8> constexpr int piece_of = FP8 ? 16 : 8;
 
 // -------------------------------------------------------------------- append
+// x becomes round(x / 2^e) in e4m3, e the least exponent with max|x| <= 448 * 2^e.
 // The lanes of a vector find its largest magnitude by a few shuffles.  Bound by
-// memory: 2 D bytes read and D + 1 (e4m3) or 2 D written per vector.
+// memory, 2 D bytes read and D + 1 (e4m3) or 2 D written per vector: 35,894
+// tokens of 8 heads of 128 to e4m3 take 39.1 us, 5.65 TB/s; a few tokens 2.7 us,
+// a launch and the chain of search, page, vector and store.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(128) sa_append_kernel(Batch B, Pool P, Rows K, Rows V, int heads) {
   constexpr int E = piece_of<FP8>, LV = D / E, NL = E / 8;
@@ -125,7 +131,10 @@ __global__ void __launch_bounds__(128) sa_append_kernel(Batch B, Pool P, Rows K,
 }
 
 // ---------------------------------------------------------------------- read
-// The reverse of append.
+// The reverse of append: code * 2^e, exact in bf16 but below its normal range.
+// Bound by memory: 42,403 tokens of 8 heads of 128 from e4m3 take 45.4 us,
+// 5.75 TB/s.  A lane's 16 codes leave as one 32-byte store: as two of 16 bytes,
+// which fill half a sector each, the same call took 60 us.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(128) sa_read_kernel(Batch B, Pool P, __nv_bfloat16* ko, __nv_bfloat16* vo, int heads) {
   constexpr int E = piece_of<FP8>, LV = D / E;
