@@ -31,7 +31,9 @@
  * asynchronous on `cuda_stream`, status codes, argument errors found on the
  * host before any launch, no exception crosses the interface, one handle per
  * stream.  Token tensors are bf16 with a contiguous last dimension, 16-byte
- * aligned, token and head strides (in elements) multiples of 8.  Metadata
+ * aligned, token and head strides (in elements) multiples of 8; the attention
+ * calls refuse (SV_ERR_ARG) strides their copies cannot express, such as 0
+ * over several heads.  n_tokens * q_heads stays below 2^31.  Metadata
  * (cu, kv_len, page_table) is int32 on the device and is checked there: a
  * sequence with a decreasing or out-of-range cu, a kv_len outside [0,
  * max_pages * page_size] or a page outside [0, num_pages) makes no access
