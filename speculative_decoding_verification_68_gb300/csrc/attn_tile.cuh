@@ -68,7 +68,10 @@ constexpr int SETUP = 3;            // units of an item besides its blocks
 constexpr int SNAP = 4;             // units that a run gives up or takes on to end with an item (SETUP at least)
 constexpr int MIN_RUN = 3;          // units of a CTA at least
 constexpr int ODD_NONE = 0x7f7f7f7f;
-constexpr int EV_MIN = -100;        // least exponent of a value block's reference (see the e4m3 conversion)
+// Least and largest exponent of a value block's reference (see the e4m3 conversion).  The sum of weights is
+// taken in units of 2^-e, and a weight reaches 2^LAZY: at -90 the sum of 2^29 keys stays below 2^128 (at the
+// -120 of a block of zero vectors 256 keys passed it), and at 126 its unit is still a normal number.
+constexpr int EV_MIN = -90, EV_MAX = 126;
 
 struct AttnParams {
   Batch B;
@@ -343,6 +346,13 @@ __device__ __forceinline__ void note_odd(int* odd, int* flag, Piece piece, int h
   }
   __threadfence();
   *(volatile int*)flag = 1;
+}
+// A sum of weights times 2^x, x <= 0.  That of an e4m3 cache may be as large as 2^126 (see EV_MIN), so that the
+// product is a normal number where 2^x alone is not: two steps.
+template <bool FP8> __device__ __forceinline__ float scaled(float l, float x) {
+  if (!FP8) return ex2(x) * l;
+  const float h = ex2(0.5f * x);
+  return h * l * h;
 }
 // What a row that sees keys 0 .. lim-1 has in a column (0: nothing)
 template <int D> __device__ __forceinline__ float odd_value(const int* odd, int col, int lim) {
@@ -869,7 +879,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               tc_after();
             }
             const float f = up == -INFINITY ? 1.0f : ex2(M - up);
-            l *= f;
+            l = scaled<C::FP8>(l, up == -INFINITY ? 0.0f : M - up);
             off *= f;
 #pragma unroll 1
             for (int i = 0; i < DH; i += 16) {             // few at a time: the scores hold most registers
@@ -1037,7 +1047,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
                           d0 = __ldcg(p + 2 * BM + r), d1 = __ldcg(q + 2 * BM + r);
               const float4 *const po = (const float4*)(p + 3 * BM) + half * (DH / 4) * BM + r, *const qo = (const float4*)(q + 3 * BM) + half * (DH / 4) * BM + r;
               const float m_top = fmaxf(m0, m1), ref = m_top == -INFINITY ? 0.0f : m_top;
-              const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref), sum = f0 * l0 + f1 * l1;
+              const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref), sum = scaled<C::FP8>(l0, m0 - ref) + scaled<C::FP8>(l1, m1 - ref);
               const float inv = sum == 0.0f ? 0.0f : 1.0f / (sum + f0 * d0 + f1 * d1), w0 = f0 * inv, w1 = f1 * inv;
               const int rt = r / A.group;
               const size_t to = (size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + r - rt * A.group;
@@ -1074,9 +1084,9 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 #pragma unroll 2
             for (int x = c0; x <= c1; ++x) {
               float* const p = part(x, x == c0);
-              const float f = ex2(__ldcg(p + ts) - ref);
-              sum += f * __ldcg(p + BM + ts);
-              fix += f * __ldcg(p + 2 * BM + ts);
+              const float x2 = __ldcg(p + ts) - ref;
+              sum += scaled<C::FP8>(__ldcg(p + BM + ts), x2);
+              fix += ex2(x2) * __ldcg(p + 2 * BM + ts);
             }
             const float inv = nan ? quiet_nan() : sum == 0.0f ? 0.0f : 1.0f / (sum + fix);
 #pragma unroll 4
@@ -1180,13 +1190,12 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         if ((stop = group_or(bar_id, BN, !ok))) break;     // all four warps leave, or none
         if (j + 1 < g.j1) nxt = load_bytes(j + 1);
         const int ek = max(max(max(wm[0].x, wm[1].x), max(wm[2].x, wm[3].x)) - EXP_BIAS, EXP_MIN);
-        int ev = max(max(max(wm[0].y, wm[1].y), max(wm[2].y, wm[3].y)) - EXP_BIAS, run - 64);
+        const int ev = min(max(max(max(wm[0].y, wm[1].y), max(wm[2].y, wm[3].y)) - EXP_BIAS, max(run - 64, EV_MIN)), EV_MAX);
         run = max(run, ev);
-        ev = max(ev, run - 64);
         // both for the softmax, ahead of the keys and so of the block's scores
         if (kv == 0 && key == 0) info[n % C::INFO] = make_float2(__int_as_float((ek + EXP_BIAS) << 23), (float)ev);
         const bool valid = key < g.kv - j * BN;            // slots past the end may hold anything
-        const int by = kv ? cur.y : cur.x, d = by == BYTE_NAN ? 0 : by - EXP_BIAS - (kv ? ev : ek);   // <= 0
+        const int by = kv ? cur.y : cur.x, d = by == BYTE_NAN ? 0 : by - EXP_BIAS - (kv ? ev : ek);   // <= 0 (1 above EV_MAX)
         const uint32_t f1 = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u, f = f1 | (f1 << 16);
         const unsigned raw = 2 * n + kv, rs = raw % C::NRAW, bs = n % ring;
         ok = bar_wait(raw_full + 8 * rs, (raw / C::NRAW) & 1, flags) && bar_wait(empty0 + 8 * bs, ((n / ring) & 1) ^ 1, flags);
