@@ -69,9 +69,12 @@ constexpr int SNAP = 4;             // units that a run gives up or takes on to 
 constexpr int MIN_RUN = 3;          // units of a CTA at least
 constexpr int ODD_NONE = 0x7f7f7f7f;
 // Least and largest exponent of a value block's reference (see the e4m3 conversion).  The sum of weights is
-// taken in units of 2^-e, and a weight reaches 2^LAZY: at -90 the sum of 2^29 keys stays below 2^128 (at the
+// taken in units of 2^-e, and a weight reaches 2^LAZY: at -97 the sum of 2^23 keys stays below 2^128 (at the
 // -120 of a block of zero vectors 256 keys passed it), and at 126 its unit is still a normal number.
-constexpr int EV_MIN = -90, EV_MAX = 126;
+constexpr int EV_MIN = -97, EV_MAX = 126;
+constexpr int BYTE_ZERO = 15;       // vectors of this scale (below 2^-103) and less count as zero beside others
+constexpr int SPREAD = 14;          // exponents apart that a block's vectors may be to share one scale
+constexpr float WIDE = 1.2676506e30f;   // 2^100, in place of the exponent of a block's values: vectors have their own
 
 struct AttnParams {
   Batch B;
@@ -347,6 +350,19 @@ __device__ __forceinline__ void note_odd(int* odd, int* flag, Piece piece, int h
   __threadfence();
   *(volatile int*)flag = 1;
 }
+// A factor of scores: above 0, where a masked score's -inf would make NaN, and finite, where a score of 0 would
+__device__ __forceinline__ float positive(float x) { return fminf(fmaxf(x, 1.17549435e-38f), 3.40282347e38f); }
+// The scale bytes of a cached token's key and, in bits 8 to 15, value; 0 where there is none
+__device__ __forceinline__ int scale_bytes(const AttnParams& A, const Segment& g, int p) {
+  if (p >= g.kv) return 0;
+  const int page = __ldg(A.B.table + (size_t)g.b * A.B.max_pages + (p >> A.B.page_shift));
+  if ((unsigned)page >= (unsigned)A.B.num_pages) return 0;
+  const size_t at = ((size_t)(page * A.kv_heads + g.head) << A.B.page_shift) + (p & ((1 << A.B.page_shift) - 1));
+  const int k = __ldg(A.ks + at), v = __ldg(A.vs + at);
+  return (k == BYTE_NAN ? EXP_BIAS : k) | (v == BYTE_NAN ? EXP_BIAS : v) << 8;
+}
+// Exponent, as the weights have it, of a value vector that has its own
+__device__ __forceinline__ int value_exponent(int byte) { return min(max(byte - EXP_BIAS, EV_MIN), EV_MAX); }
 // A sum of weights times 2^x, x <= 0.  That of an e4m3 cache may be as large as 2^126 (see EV_MIN), so that the
 // product is a normal number where 2^x alone is not: two steps.
 template <bool FP8> __device__ __forceinline__ float scaled(float l, float x) {
@@ -379,10 +395,11 @@ struct Cfg {
   static constexpr int CONV_WARPS = FP8 ? 8 : 0;
   static constexpr int WARPS = CONV_WARP0 + CONV_WARPS;
   static constexpr int THREADS = WARPS * 32;
-  // Registers: five warpgroups start with 96 each; the first one, which copies and issues, gives up
-  // what the softmax needs to hold half a row of scores.
-  static constexpr int REGS_SOFT = MT == 2 ? 104 : 0, REGS_WORK = 64;
-  static_assert(REGS_SOFT == 0 || 128 * REGS_WORK + SOFT_WARPS * MT * 32 * REGS_SOFT <= THREADS * 96, "register split");
+  // Registers: five warpgroups start with 96 each; the first one, which copies and issues, or for e4m3 the
+  // converting ones give up what the softmax needs to hold half a row of scores (64 sequences of 16 tokens over
+  // 1000-16000 e4m3: 327 us with 96 for all, 297 with 120 and 72, 299 with 112 and 80).
+  static constexpr int REGS_SOFT = MT == 2 ? 104 : FP8 ? 120 : 0, REGS_WORK = FP8 ? 96 : 64, REGS_CONV = 72;
+  static_assert(REGS_SOFT == 0 || 128 * REGS_WORK + SOFT_WARPS * MT * 32 * REGS_SOFT + CONV_WARPS * 32 * REGS_CONV <= THREADS * 96, "register split");
   static constexpr int INFO = 8;                              // ring of block references (more than NK + 1)
 };
 // named barriers: pairs of softmax warps of a quarter of a tile's rows, tiles, converting warps
@@ -860,14 +877,54 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 #pragma unroll
           for (int i = 0; i < 64; ++i) x[i] = i < rel ? x[i] : 0xff800000u;
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto largest = [&]() {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 0; i < 64; i += 8)
+          for (int i = 0; i < 64; i += 8)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + 4 + e]));
-        const float best = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), top = fmaf(best, cb, ev);
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], __uint_as_float(x[i + e]), __uint_as_float(x[i + 4 + e]));
+          return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        };
+        float best = largest(), top = fmaf(best, cb, ev);
         if (group_or(pair, 64, j == j0 || top > M + LAZY || !ok)) {
           // Set or raise the reference, the same for both threads of the row.
+          float l_wide = 0.0f, m_wide = -INFINITY;         // sum of weights of a wide block, its reference
+          if (C::FP8 && ev == WIDE) {
+            // The block's vectors are too far apart for one scale (no score is so low that top misses WIDE):
+            // s_ij + e_j, with each vector's own exponents, in place of the scores; the sum is without e_j.
+            const float x_all = info[n % C::INFO].x;       // keys' factor if positive, else their own and maybe -256 - the values' exponent
+#pragma unroll 1
+            for (int i = 0; i < 64; i += 16) {
+              uint32_t o[16];
+              const int own = scale_bytes(A, g, j * BN + half * 64 + i + (lane & 15));
+              tm_ld16(s_at + i, o);
+              float m = m_wide;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int w = __shfl_sync(FULL, own, e);
+                const float s = __uint_as_float(o[e]) * positive(c * (x_all > 0.0f ? x_all : scale_of(w & 255)));
+                const float t = i + e < rel ? s + (x_all < -1.0f ? -256.0f - x_all : (float)value_exponent(w >> 8)) : -INFINITY;
+                m = fmaxf(m, t);
+                o[e] = __float_as_uint(t);
+              }
+              l_wide *= m == -INFINITY ? 0.0f : ex2(m_wide - m);
+              m_wide = m;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                const int w = __shfl_sync(FULL, own, e);
+                // the difference first: it is what the weight has, however large the scores
+                l_wide += ex2(__uint_as_float(o[e]) - (m == -INFINITY ? 0.0f : m) - (x_all < -1.0f ? -256.0f - x_all : (float)value_exponent(w >> 8)));
+              }
+              tm_st16(s_at + i, o);
+            }
+            tc_wait_st();
+            tm_ld32(s_at, x);
+            tm_ld32(s_at + 32, x + 32);
+            tc_wait_ld(x);
+            tc_wait_ld(x + 32);
+            cb = 1.0f;
+            top = largest();
+          }
           *to_pair = top;
           group_sync(pair, 64);
           const float up = fmaxf(fmaxf(M, top), *from_pair);
@@ -879,7 +936,8 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               tc_after();
             }
             const float f = up == -INFINITY ? 1.0f : ex2(M - up);
-            l = scaled<C::FP8>(l, up == -INFINITY ? 0.0f : M - up);
+            if (C::FP8 && f == 0.0f && l > 0.0f) l = scaled<true>(l, M - up);
+            else l *= f;
             off *= f;
 #pragma unroll 1
             for (int i = 0; i < DH; i += 16) {             // few at a time: the scores hold most registers
@@ -891,6 +949,10 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             }
           }
           M = up;
+          if (C::FP8 && ev == WIDE) {
+            l += scaled<true>(l_wide, M == -INFINITY ? 0.0f : m_wide - M);
+            ev = 0.0f;
+          }
           if (group_or(pair, 64, !ok)) { ok = false; break; }   // both have read; both leave, or none
         }
         care(j);
@@ -934,7 +996,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         upk(acc[0], s0, s1);
         upk(acc[1], s2, s3);
         const float add = (s0 + s1) + (s2 + s3);
-        l += C::FP8 ? add * __int_as_float((EXP_BIAS - (int)ev) << 23) : add;
+        l += C::FP8 ? add * ex2(-info[n % C::INFO].y) : add;   // 0 where it has been added already
         if (!C::FP8 && !split) {
           // what rounding to bf16 did to the largest of these weights (see the run's result)
           const float p = ex2(fmaf(best, cb, neg));
@@ -1149,15 +1211,20 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       if (!g.more) break;
     } while (true);
     }
-  } else if constexpr (C::FP8) if (busy) {
+  } else if constexpr (C::FP8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONV));
+    if (busy) {
     // ---------------------------------------------- e4m3 codes to f16 blocks
     // A code is exact in f16, and so is its product with 2^(e_j - e), e the
-    // largest exponent among the block's vectors, unless the vector is 2^15
-    // times smaller than that one (then what is lost is 2^-25 of the largest).
-    // The softmax applies e once per block: key scores times 2^e, and for the
-    // values the reference M covers s_ij + e, so a weight times a block value
-    // stays within range whatever the vectors' sizes.  e of the values is kept
-    // within 2^64 of the run's largest so that the weights do not vanish.
+    // largest exponent among the block's vectors, down to e - SPREAD.  The softmax
+    // applies e once per block: key scores times 2^e, and for the values the
+    // reference M covers s_ij + e, so a weight times a block value stays within
+    // range whatever the vectors' sizes.  e of the values is kept within 2^64 of
+    // the run's largest so that the weights do not vanish.  Where a vector is
+    // smaller than that (a token of another size that some rows may not even see)
+    // the codes stay as they are and the softmax applies each vector's own
+    // exponent: a cold path, a few hundred instructions a block.  Vectors of scale
+    // BYTE_ZERO and less, which zeros have, do not count for that.
     // Four warps convert the keys, four the values, a thread a vector.  Raw lines
     // are swizzled like the f16 ones, so that eight threads of eight keys reach
     // eight different 16-byte columns.
@@ -1173,36 +1240,48 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     while (!stop && W.next(A, tile_rows, g)) {
       const int32_t* const tab = A.B.table + (size_t)g.b * A.B.max_pages;
       int run = EV_MIN;
-      auto load_bytes = [&](int j) {                       // scale bytes of this thread's key and value (0: none)
+      // page of this thread's key in block j (loaded a block before its scale bytes, those a block before their use)
+      auto page_of = [&](int j) {
         const int p = j * BN + key;
-        if (p >= g.kv) return make_int2(0, 0);
-        const int page = __ldg(tab + (p >> A.B.page_shift));
+        return p < g.kv ? __ldg(tab + (p >> A.B.page_shift)) : -1;
+      };
+      auto load_bytes = [&](int j, int page) {             // scale bytes of this thread's key and value (0: none)
         if ((unsigned)page >= (unsigned)A.B.num_pages) return make_int2(0, 0);
-        const size_t at = ((size_t)(page * A.kv_heads + g.head) << A.B.page_shift) + (p & ((1 << A.B.page_shift) - 1));
+        const size_t at = ((size_t)(page * A.kv_heads + g.head) << A.B.page_shift) + ((j * BN + key) & ((1 << A.B.page_shift) - 1));
         return make_int2(kv ? 0 : __ldg(A.ks + at), __ldg(A.vs + at));
       };
-      int2 nxt = load_bytes(g.j0);
+      // largest byte of a warp's vectors, and in the upper half 255 - the smallest that counts
+      auto extremes = [&](int byte) {
+        const int most = __reduce_max_sync(FULL, byte == BYTE_NAN ? 0 : byte);
+        return most | __reduce_max_sync(FULL, byte == BYTE_NAN || byte <= BYTE_ZERO ? 0 : 255 - byte) << 16;
+      };
+      int2 nxt = load_bytes(g.j0, page_of(g.j0));
+      int page = page_of(g.j0 + 1);
       for (int j = g.j0; j < g.j1; ++j, ++n) {
         const int2 cur = nxt;
-        const int ka = __reduce_max_sync(FULL, cur.x == BYTE_NAN ? 0 : cur.x), va = __reduce_max_sync(FULL, cur.y == BYTE_NAN ? 0 : cur.y);
+        const int ka = kv ? 0 : extremes(cur.x), va = extremes(cur.y);
         int2* const wm = wmax + (n & 1) * 4;
         if (lane == 0) wm[warp & 3] = make_int2(ka, va);
         if ((stop = group_or(bar_id, BN, !ok))) break;     // all four warps leave, or none
-        if (j + 1 < g.j1) nxt = load_bytes(j + 1);
-        const int ek = max(max(max(wm[0].x, wm[1].x), max(wm[2].x, wm[3].x)) - EXP_BIAS, EXP_MIN);
-        const int ev = min(max(max(max(wm[0].y, wm[1].y), max(wm[2].y, wm[3].y)) - EXP_BIAS, max(run - 64, EV_MIN)), EV_MAX);
+        nxt = load_bytes(j + 1, page);
+        page = page_of(j + 2);
+        const unsigned kx = __vmaxu2(__vmaxu2(wm[0].x, wm[1].x), __vmaxu2(wm[2].x, wm[3].x));
+        const unsigned vx = __vmaxu2(__vmaxu2(wm[0].y, wm[1].y), __vmaxu2(wm[2].y, wm[3].y));
+        const int ek = max((int)(kx & 0xffff) - EXP_BIAS, EXP_MIN);
+        const int ev = min(max((int)(vx & 0xffff) - EXP_BIAS, max(run - 64, EV_MIN)), EV_MAX);
         run = max(run, ev);
-        // both for the softmax, ahead of the keys and so of the block's scores
-        if (kv == 0 && key == 0) info[n % C::INFO] = make_float2(__int_as_float((ek + EXP_BIAS) << 23), (float)ev);
+        const bool wide_k = ek - (255 - (int)(kx >> 16) - EXP_BIAS) > SPREAD, wide_v = ev - (255 - (int)(vx >> 16) - EXP_BIAS) > SPREAD;
         const bool valid = key < g.kv - j * BN;            // slots past the end may hold anything
-        const int by = kv ? cur.y : cur.x, d = by == BYTE_NAN ? 0 : by - EXP_BIAS - (kv ? ev : ek);   // <= 0 (1 above EV_MAX)
-        const uint32_t f1 = d >= -14 ? (uint32_t)(15 + d) << 10 : d >= -24 ? 1u << (24 + d) : 0u, f = f1 | (f1 << 16);
+        const int by = kv ? cur.y : cur.x;
+        int d = by - EXP_BIAS - (kv ? ev : ek);            // <= 0 (1 above EV_MAX)
+        if (kv ? wide_v : wide_k) d = kv ? by - EXP_BIAS - value_exponent(by) : 0;
+        const uint32_t f1 = (uint32_t)max(15 + d, 0) << 10, f = f1 | (f1 << 16);
         const unsigned raw = 2 * n + kv, rs = raw % C::NRAW, bs = n % ring;
         ok = bar_wait(raw_full + 8 * rs, (raw / C::NRAW) & 1, flags) && bar_wait(empty0 + 8 * bs, ((n / ring) & 1) ^ 1, flags);
         const uint8_t* const src = raw0 + rs * C::RAW;
         uint8_t* const dst = out0 + bs * C::BUF;
         if (ok) {
-#pragma unroll
+#pragma unroll 1
           for (int h = 0; h < D / 64; ++h) {               // 64 codes: one line of the f16 block
             uint4 xs[4];
 #pragma unroll
@@ -1226,6 +1305,8 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             }
           }
         }
+        // both for the softmax, ahead of the keys and so of the block's scores
+        if (kv == 0 && key == 0) info[n % C::INFO] = make_float2(!wide_k ? __int_as_float((ek + EXP_BIAS) << 23) : wide_v ? -1.0f : -256.0f - ev, wide_k || wide_v ? WIDE : (float)ev);
         fence_async();
         __syncwarp();
         if (lane == 0) {
@@ -1234,6 +1315,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         }
       }
     }
+  }
   }
   tc_before();
   __syncthreads();

@@ -1,4 +1,5 @@
-"""Attention over e4m3 caches whose values are zero, or at the ends of the format's range."""
+"""Attention over e4m3 caches whose vectors differ far in size: zero values, vectors at the
+ends of the format's range, and outsized tokens that a row does not see or hardly weighs."""
 import numpy as np
 import pytest
 
@@ -99,3 +100,66 @@ def test_largest_scales(lib):
         ref = _attn.attention(q.double().numpy(), kc[0], np.ones_like(vc[0]), d ** -0.5, [n])
         assert (np.abs(got["out"].double().cpu().numpy() / value - 1) <= 2.0 ** -7).all()
         assert (np.abs(got["lse"].double().cpu().numpy() - ref[1]) <= ref[3]).all()
+
+
+# ------------------------------------------------------------ outsized tokens
+def shifted(x, at, shift):
+    x = x.clone()
+    x[at] *= 2.0 ** shift
+    return x
+
+
+@pytest.mark.parametrize("d, hq, hkv", [(64, 4, 2), (128, 8, 1), (128, 15, 3)])
+@pytest.mark.parametrize("shift", [13, 15, 20, 30, 60, 100])
+@pytest.mark.parametrize("which", ["k", "v", "kv"])
+def test_later_tokens_of_another_size_leave_earlier_rows_alone(lib, which, shift, d, hq, hkv):
+    g = np.random.default_rng(4)
+    q, k, v = [], [], []
+    for n, old in ((8, 100), (150, 40), (5, 260)):
+        kk, vv = normal(g, old + n, hkv, d), normal(g, old + n, hkv, d)
+        for at in (old + n - 1, old + n // 2):
+            kk = shifted(kk, at, shift) if "k" in which else kk
+            vv = shifted(vv, at, shift) if "v" in which else vv
+        q.append(normal(g, n, hq, d)), k.append(kk), v.append(vv)
+    check(lib, hq, q, k, v)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shift", [20, 40, 70, 100])
+@pytest.mark.parametrize("n, at", [(100, 7), (500, 3), (500, 499), (500, 200), (9000, 1000)])
+def test_outsized_values_that_hardly_weigh(lib, n, at, shift, d):
+    """One token's value is 2^shift times the others', its weight e^-100: what the others give remains."""
+    g = np.random.default_rng(6)
+    q, k, v = normal(g, 1, 1, d), normal(g, n, 1, d) * 0.3, shifted(normal(g, n, 1, d), at, shift)
+    u = q[0, 0].double()
+    k[at, 0] = (-100.0 * d ** 0.5 / (u @ u) * u).bfloat16()
+    check(lib, 1, [q], [k], [v])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shift", [20, 40, 100])
+@pytest.mark.parametrize("n, at", [(100, 7), (500, 200), (9000, 1000)])
+def test_outsized_keys_whose_scores_are_far_below(lib, n, at, shift, d):
+    g = np.random.default_rng(7)
+    q, k, v = normal(g, 1, 1, d), normal(g, n, 1, d), normal(g, n, 1, d)
+    u = q[0, 0].double()
+    k[at, 0] = (-(2.0 ** shift) * u / (u @ u) ** 0.5).bfloat16()
+    attn, pool, kv_len, table, kc, vc = cache(lib, 1, [k], [v])
+    got = attn.attend(pool, q.cuda(), torch.tensor([0, 1], dtype=torch.int32, device="cuda"), kv_len, table, want_lse=True)
+    assert attn.get_error() == lib.SV_OK
+    # that key's weight is 0 in float64 too; without it the bound on a score is that of the others
+    kept = [np.delete(x[0], at, 0) for x in (kc, vc)]
+    _attn.assert_attention(got["out"], got["lse"], _attn.attention(q.double().numpy(), *kept, d ** -0.5, [n - 1]))
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_sizes_spread_over_the_whole_range(lib, causal):
+    """Every vector its own size, keys and values: 2^-60 to 2^60."""
+    g = np.random.default_rng(8)
+    q, k, v = [], [], []
+    for n, old in ((7, 300), (40, 1000), (1, 2)):
+        kk, vv = normal(g, old + n, 2, 64), normal(g, old + n, 2, 64)
+        for x, hi in ((kk, 0), (vv, 60)):
+            x *= torch.from_numpy(2.0 ** g.integers(-60, hi + 1, (old + n, 2, 1)).astype(np.float32)).bfloat16()
+        q.append(normal(g, n, 8, 64)), k.append(kk), v.append(vv)
+    check(lib, 8, q, k, v, causal=causal)
