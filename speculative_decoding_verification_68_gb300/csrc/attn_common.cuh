@@ -71,7 +71,7 @@ __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
   asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(r.x), "=f"(r.y) : "r"(h));
   return r;
 }
-// 2^e for the exponents a scale byte can hold; NaN for BYTE_NAN
+// 2^e for the exponents a scale byte can hold (0 for byte 0, see sa_read_kernel); NaN for BYTE_NAN
 __device__ __forceinline__ float scale_of(int byte) { return byte == BYTE_NAN ? quiet_nan() : __int_as_float(byte << 23); }
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;

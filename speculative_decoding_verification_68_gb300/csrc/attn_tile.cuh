@@ -1275,7 +1275,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const int by = kv ? cur.y : cur.x;
         int d = by - EXP_BIAS - (kv ? ev : ek);            // <= 0 (1 above EV_MAX)
         if (kv ? wide_v : wide_k) d = kv ? by - EXP_BIAS - value_exponent(by) : 0;
-        const uint32_t f1 = (uint32_t)max(15 + d, 0) << 10, f = f1 | (f1 << 16);
+        const uint32_t f1 = by == BYTE_NAN ? 0x7e00u : (uint32_t)max(15 + d, 0) << 10, f = f1 | (f1 << 16);   // NaN whatever the codes
         const unsigned raw = 2 * n + kv, rs = raw % C::NRAW, bs = n % ring;
         ok = bar_wait(raw_full + 8 * rs, (raw / C::NRAW) & 1, flags) && bar_wait(empty0 + 8 * bs, ((n / ring) & 1) ^ 1, flags);
         const uint8_t* const src = raw0 + rs * C::RAW;

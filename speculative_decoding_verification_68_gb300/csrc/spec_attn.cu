@@ -163,7 +163,10 @@ __global__ void __launch_bounds__(128) sa_read_kernel(Batch B, Pool P, __nv_bflo
         const long long vec = vec0 + ((long long)(is_v ? vi - heads : vi) << B.page_shift);
         if (vi >= 2 * heads) continue;
         x[u] = ldg_stream((const char*)(is_v ? P.v : P.k) + (vec * D + piece * E) * (FP8 ? 1 : 2));
-        if constexpr (FP8) f[u] = scale_of(__ldg((is_v ? P.vs : P.ks) + vec));
+        if constexpr (FP8) {
+          const int byte = __ldg((is_v ? P.vs : P.ks) + vec);
+          f[u] = byte == 0 ? __int_as_float(1 << 22) : scale_of(byte);   // 2^-127 is subnormal
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {

@@ -163,3 +163,38 @@ def test_sizes_spread_over_the_whole_range(lib, causal):
             x *= torch.from_numpy(2.0 ** g.integers(-60, hi + 1, (old + n, 2, 1)).astype(np.float32)).bfloat16()
         q.append(normal(g, n, 8, 64)), k.append(kk), v.append(vv)
     check(lib, 8, q, k, v, causal=causal)
+
+
+# -------------------------------------------- scale bytes of another program
+@pytest.mark.parametrize("d", [64, 128])
+def test_scale_byte_255_is_nan_whatever_the_codes(lib, d):
+    """read and attend agree on a vector whose byte is 255 and whose codes are numbers."""
+    g = np.random.default_rng(9)
+    n, new, at, page = 300, 20, 290, 32
+    q, k, v = normal(g, new, 4, d), normal(g, n, 2, d), normal(g, n, 2, d)
+    cu = torch.tensor([0, new], dtype=torch.int32, device="cuda")
+    for name in ("k", "v"):
+        attn, pool, kv_len, table, kc, vc = cache(lib, 4, [k], [v], page)
+        where = table[0, at // page].item(), slice(None), at % page
+        getattr(pool, name + "_scale")[where] = 255
+        back = attn.read(pool, cu, kv_len, table, n_tokens=new)[name]
+        assert torch.isnan(back[at - (n - new)]).all() and torch.isfinite(back).sum().item() == (new - 1) * 2 * d
+        got = attn.attend(pool, q.cuda(), cu, kv_len, table, want_lse=True)
+        assert attn.get_error() == lib.SV_OK
+        clean = at - (n - new)                       # rows that do not see the token
+        expected = _attn.attention(q.double().numpy(), kc[0], vc[0], d ** -0.5, [n - new + i + 1 for i in range(new)])
+        _attn.assert_attention(got["out"][:clean], got["lse"][:clean], [x[:clean] for x in expected])
+        assert torch.isnan(got["out"][clean:]).all()
+
+
+def test_scale_byte_0_is_read_as_2_to_the_minus_127(lib):
+    g = np.random.default_rng(10)
+    n, d = 40, 64
+    attn, pool, kv_len, table, _, _ = cache(lib, 2, [normal(g, n, 1, d)], [normal(g, n, 1, d)])
+    pool.k_scale.fill_(0), pool.v_scale.fill_(0)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    got = attn.read(pool, cu, kv_len, table, n_tokens=n)
+    for name in ("k", "v"):
+        codes = getattr(pool, name).view(torch.uint8).cpu().numpy()
+        ref = np.stack([_attn.e4m3_value(codes[table[0, p // 32].item(), :, p % 32]) for p in range(n)]) * 2.0 ** -127
+        assert torch.equal(got[name].float().cpu(), torch.from_numpy(ref).float().bfloat16().float())
