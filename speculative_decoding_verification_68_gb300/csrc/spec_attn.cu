@@ -34,8 +34,9 @@ __device__ __forceinline__ int find_seq(const Batch& B, int t, int lane) {
   const int a = __ldg(B.cu + lo), e = __ldg(B.cu + lo + 1);
   return (a >= 0 && a <= t && t < e && e <= B.n_tokens) ? lo : -1;
 }
-// Page of token t, and its slot there.  NO_ROW: in no sequence; INVALID: in one whose length or page
-// is not valid (both are reported); NO_SLOT: before the first position.
+// Page of token t, and its slot there.  NO_ROW: in no sequence, as the rows that pad a batch are (a wrong cu
+// is reported by flag_invalid_seqs); INVALID: in one whose length or page is not valid, which is reported;
+// NO_SLOT: before the first position.
 enum { NO_SLOT = -1, INVALID = -2, NO_ROW = -3 };
 __device__ __forceinline__ int find_page(const Batch& B, int t, int lane, int& slot) {
   const int b = find_seq(B, t, lane);
@@ -52,7 +53,7 @@ __device__ __forceinline__ int find_page(const Batch& B, int t, int lane, int& s
       slot = pos & ((1 << B.page_shift) - 1);
     }
   }
-  if (page <= INVALID && lane == 0) B.flags[0] = 1;
+  if (page == INVALID && lane == 0) B.flags[0] = 1;
   return page;
 }
 // Pieces of a lane in flight, and warps of a block.  36K tokens appended to e4m3 pools take 40.1 us with 2
