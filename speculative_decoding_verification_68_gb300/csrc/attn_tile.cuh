@@ -49,24 +49,17 @@
 #include <stdint.h>
 
 #include "attn_common.cuh"
+#include "attn_plan.cuh"
 
 namespace {
 
 enum { KIND_BF16 = 0, KIND_E4M3 = 1, KIND_PACKED = 2 };
 
-constexpr int BN = 128;             // keys per block
-constexpr int BM = 128;             // rows per tile (tensor-memory lanes)
 constexpr int HALF_BYTES = BN * 128;  // 64 of the D columns of a block: 128 rows of one swizzled 128-byte line
 constexpr float LAZY = 8.0f;        // log2 of how far scores may pass the reference: f16 weights hold 2^15
 constexpr float ABOVE = 1.0f + 1.0f / 65536.0f;   // see the weights in two parts
 constexpr int POLLS = 1 << 18;      // of a bounded wait (about 1 s)
 constexpr int SMEM_LIMIT = 232448;
-// Of the run schedule, in units (about 1.6 us with two tiles, 1.2 with one).  Time over 30 cases of all sizes
-// against the values chosen: SETUP and SNAP 2, +2%; SNAP 3, +1%; SNAP 6, +0.4%; SETUP 4, +0.3%; MIN_RUN 2, 5 and
-// 8, +1, +7 and +15%.  Without SETUP and SNAP 8 prompts of 100-2048 tokens take 114 instead of 77 us.
-constexpr int SETUP = 3;            // units of an item besides its blocks
-constexpr int SNAP = 4;             // units that a run gives up or takes on to end with an item (SETUP at least)
-constexpr int MIN_RUN = 3;          // units of a CTA at least
 constexpr int ODD_NONE = 0x7f7f7f7f;
 // Least and largest exponent of a value block's reference (see the e4m3 conversion).  The sum of weights is
 // taken in units of 2^-e, and a weight reaches 2^LAZY: at -97 the sum of 2^23 keys stays below 2^128 (at the
@@ -220,31 +213,6 @@ __host__ __device__ constexpr uint32_t instr_desc(bool bf16, int n, bool b_mn_ma
 }
 
 // ------------------------------------------------------------------ planning
-// sum over i = 0 .. n-1 of floor((a i + b) / m), by the Euclidean reduction of lattice points; a n + b < 2^32
-__device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-  unsigned long long s = 0;
-  while (n > 0) {
-    s += (unsigned long long)(n - 1) * n / 2 * (a / m);
-    a %= m;
-    s += (unsigned long long)n * (b / m);
-    b %= m;
-    const unsigned y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const unsigned t = m;
-    m = a;
-    a = t;
-  }
-  return (long long)s;
-}
-
-struct Seq {          // one sequence as the kernel sees it
-  int row0, n;        // packed rows
-  int kv;             // cached tokens (0 where the length is invalid)
-  int tiles;
-  bool bad;
-};
 __device__ __forceinline__ Seq load_seq(const Batch& B, int b, int tile_rows) {
   Seq s;
   const int a = __ldg(B.cu + b), e = __ldg(B.cu + b + 1);
@@ -258,26 +226,6 @@ __device__ __forceinline__ Seq load_seq(const Batch& B, int b, int tile_rows) {
   s.bad |= !range;
   return s;
 }
-// key blocks of tile t (at least one, so that its rows are written)
-__device__ __forceinline__ int tile_blocks(const Seq& s, int t, int tile_rows, int causal) {
-  const int len = causal ? s.kv - s.n + min(s.n, (t + 1) * tile_rows) : s.kv;
-  return max(1, (len + BN - 1) / BN);
-}
-// units of tiles 0 .. t-1
-__device__ inline long long tiles_before(const Seq& s, int t, int tile_rows, int causal) {
-  if (t == 0) return 0;
-  if (!causal) return (long long)t * (SETUP + tile_blocks(s, 0, tile_rows, causal));
-  long long last = (long long)t * SETUP;
-  if (t == s.tiles) {                   // the last tile may be short
-    last += tile_blocks(s, t - 1, tile_rows, causal);
-    if (--t == 0) return last;
-  }
-  const int base = s.kv - s.n;          // tile i (from 1) ends at key base + i * tile_rows
-  const int ones = base >= BN ? 0 : min(t, (BN - base) / tile_rows);
-  if (ones == t) return last + t;
-  return last + ones + floor_sum((unsigned)(t - ones), BN, (unsigned)tile_rows, (unsigned)(base + (ones + 1) * tile_rows + BN - 1));
-}
-
 struct Segment {      // a run of blocks of one item
   int b, head;
   int row0, ntok;     // packed rows of the tile's tokens
@@ -422,11 +370,12 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
                  p_full = s_full + 16,
                  o_done = p_full + 16,   // a run's last product, per tile; with one tile, also every product (second barrier)
                  q_full = o_done + 16, q_empty = q_full + 8, drain = q_empty + 8;
+  static_assert(C::WARPS <= 20, "planning sums");
   static_assert(8 * (2 * NK + 2 * NV + 2 * C::NRAW + 9) <= 320, "barrier area");
   int* const work = (int*)(small + 320);                  // tensor-memory base, plan, merge flags [16]
   int* const odd_flag = (int*)(small + 640);              // whether a run has values that are not finite in such a block [4]
   float2* const info = (float2*)(small + 384);            // block references of an e4m3 cache [INFO]
-  int* const red = (int*)(small + 448);                   // planning (20 sums of 8 bytes), then the converters' maxima
+  int* const red = (int*)(small + 448);                   // planning (20 sums and 2 places of 8 bytes), then the converters' maxima
   Segment* const runs = (Segment*)(small + 768);          // runs as the query warps announce them [4]
   static_assert(sizeof(Segment) <= 64, "ring of runs");
   float* const swap = (float*)(small + 1024);             // [tile][half][row]: between the two threads of a row
@@ -473,7 +422,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   W.b = W.head = W.t = 0;
   if (blockIdx.x < ctas && units > 0) {
     // the items that hold the run's two cuts; the last cut of all is the end
-    const long long cut[2] = {units * blockIdx.x / ctas, units * (blockIdx.x + 1) / ctas};
+    const long long cut[2] = {cut_at(units, ctas, blockIdx.x), cut_at(units, ctas, blockIdx.x + 1)};
     long long before = 0;
     for (int b0 = 0; b0 < A.B.n_seqs && before <= cut[1]; b0 += NT) {   // their sequences
       const int b = b0 + tid;
@@ -503,11 +452,11 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 #pragma unroll
       for (int e = 0; e < 2; ++e)
         if (begin <= cut[e] && cut[e] < end) {
-          const unsigned per = (unsigned)(mine / A.kv_heads), at = (unsigned)(cut[e] - begin);
-          int* const found = work + 1 + 5 * e;            // sequence, head, unit within the head, tile, unit within the item
+          const Spot at = locate(cut[e] - begin, mine / A.kv_heads);
+          int* const found = work + 1 + 5 * e;            // sequence, head, tile, unit within the item
           found[0] = b;
-          found[1] = (int)(at / per);
-          found[2] = (int)(at % per);
+          found[1] = at.head;
+          red64[20 + e] = at.unit;
         }
       before += chunk;                                    // uniform
     }
@@ -517,12 +466,12 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     if (cut[mine_e] < units) {
       int* const found = work + 1 + 5 * mine_e;
       const Seq s = load_seq(A.B, found[0], tile_rows);
-      const int r = found[2];
+      const long long r = red64[20 + mine_e];
       for (int t = tid - mine_e * (NT / 2); t < s.tiles; t += NT / 2) {
         const long long lo = tiles_before(s, t, tile_rows, A.causal);
         if (lo <= r && r < lo + SETUP + tile_blocks(s, t, tile_rows, A.causal)) {
-          found[3] = t;
-          found[4] = (int)(r - lo);
+          found[2] = t;
+          found[3] = (int)(r - lo);
         }
       }
     }
@@ -533,12 +482,11 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       const int* const found = work + 1 + 5 * e;
       to[e] = cut[e];
       if (cut[e] == units) continue;
-      W.b = found[0]; W.head = found[1]; W.t = found[3];
+      W.b = found[0]; W.head = found[1]; W.t = found[2];
       W.s = load_seq(A.B, W.b, tile_rows);
-      const int in = found[4], size = SETUP + tile_blocks(W.s, W.t, tile_rows, A.causal);
+      const int in = found[3], size = SETUP + tile_blocks(W.s, W.t, tile_rows, A.causal);
       from = cut[e] - in;
-      if (in <= SNAP) to[e] = from;
-      else if (size - in <= SNAP) to[e] = from + size;
+      to[e] = moved_cut(cut[e], in, size);
     }
     W.u0 = to[0];
     W.u1 = to[1];
@@ -1091,8 +1039,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             if (x != 0.0f) __stcg(dst + 3 * BM + (col / 4 * BM + r) * 4 + col % 4, x);
           }
         }
-        const long long begin = g.start - SETUP;
-        const int c0 = (int)(((begin + SNAP + 1) * ctas - 1) / units), c1 = (int)(((g.start + g.nblk - SNAP) * ctas - 1) / units);
+        const int c0 = first_run(g.start - SETUP, units, ctas), c1 = last_run(g.start - SETUP, SETUP + g.nblk, units, ctas);
         __threadfence();
         group_sync(group_bar, NS);
         if (ts == 0) work[14 + tile] = atomicAdd(A.counters + c0 * MT + tile, 1) == c1 - c0;
