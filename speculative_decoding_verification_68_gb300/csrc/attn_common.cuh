@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "attn_plan.cuh"
+
 namespace {
 
 constexpr unsigned FULL = 0xffffffffu;
@@ -80,7 +82,7 @@ __device__ __forceinline__ uint4 ldg_stream(const void* p) {
 }
 
 __device__ __forceinline__ bool len_valid(const Batch& B, int len) {
-  return len >= 0 && (long long)len <= ((long long)B.max_pages << B.page_shift);
+  return len >= 0 && len <= LEN_MAX && (long long)len <= ((long long)B.max_pages << B.page_shift);
 }
 // Whether sequence b's row range and length are within the call's limits.
 __device__ __forceinline__ bool seq_valid(const Batch& B, int b) {

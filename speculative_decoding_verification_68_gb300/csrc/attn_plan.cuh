@@ -19,6 +19,7 @@ constexpr int BM = 128;             // rows per tile (tensor-memory lanes)
 constexpr int SETUP = 3;            // units of an item besides its blocks
 constexpr int SNAP = 4;             // units that a run gives up or takes on to end with an item (SETUP at least)
 constexpr int MIN_RUN = 3;          // units of a CTA at least
+constexpr int LEN_MAX = 0x7fffffff - 511;   // tokens of a sequence, cached or packed: positions up to three blocks on fit 32 bits
 // sum over i = 0 .. n-1 of floor((a i + b) / m), by the Euclidean reduction that counts the lattice points under a
 // line (Graham, Knuth and Patashnik, Concrete Mathematics, section 3.5); a n + b < 2^32
 __host__ __device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {

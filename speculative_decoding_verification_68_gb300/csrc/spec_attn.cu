@@ -223,7 +223,7 @@ static int check_pool(const spec_attn_ctx* h, const spec_attn_pool* p) {
 static int check_batch(const spec_attn_ctx* h, const spec_attn_batch* b) {
   if (!b || b->n_seqs < 0 || b->n_tokens < 0 || b->max_pages < 0 || b->n_seqs > h->max_seqs) return SV_ERR_ARG;
   if (b->n_seqs > 0 && (!b->cu || !b->kv_len || (!b->page_table && b->max_pages > 0))) return SV_ERR_ARG;
-  if ((long long)b->n_tokens * h->q_heads >= (1ll << 31)) return SV_ERR_SIZE;
+  if (b->n_tokens > LEN_MAX || (long long)b->n_tokens * h->q_heads >= (1ll << 31)) return SV_ERR_SIZE;
   return SV_OK;
 }
 static int check_rows(const spec_attn_rows* r) {
@@ -436,7 +436,7 @@ extern "C" int spec_attn_prompt(spec_attn_t h, int n_seqs, int n_tokens, const i
                                 const spec_attn_rows* q, const spec_attn_rows* k, const spec_attn_rows* v,
                                 float scale, void* out, float* lse, void* cuda_stream) {
   if (!h || !(scale > 0.0f) || !isfinite(scale) || n_seqs < 0 || n_tokens < 0 || n_seqs > h->max_seqs) return SV_ERR_ARG;
-  if ((long long)n_tokens * h->q_heads >= (1ll << 31)) return SV_ERR_SIZE;
+  if (n_tokens > LEN_MAX || (long long)n_tokens * h->q_heads >= (1ll << 31)) return SV_ERR_SIZE;
   if (n_seqs == 0 || n_tokens == 0) return SV_OK;
   int rc;
   if (!cu) return SV_ERR_ARG;

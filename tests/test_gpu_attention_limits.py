@@ -1,0 +1,56 @@
+"""The limits of the cache and attention calls: lengths near 2^31, factors at the ends of a float's
+range, and handles of another GPU."""
+import ctypes
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
+SV_ERR_SIZE = 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_decoding_verification_68_gb300 as sv
+    sv.build()
+    return sv
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_lengths_near_2_31_are_invalid_data(lib, dtype):
+    attn = lib.SpecAttention(2, 1, 64, 1)
+    pool = attn.alloc_pool(2, 128, dtype)
+    table = torch.zeros((1, 1 << 24), dtype=torch.int32, device="cuda")    # pages enough for 2^31 tokens
+    q = torch.ones((1, 2, 64), dtype=BF16, device="cuda")
+    got = attn.attend(pool, q, ints(0, 1), ints(2 ** 31 - 511), table, want_lse=True)
+    assert attn.get_error() == lib.SV_ERR_DATA
+    assert torch.isnan(got["out"]).all() and torch.isnan(got["lse"]).all()
+    back = attn.read(pool, ints(0, 1), ints(2 ** 31 - 511), table, n_tokens=1)
+    assert attn.get_error() == lib.SV_ERR_DATA
+    assert torch.isnan(back["k"]).all()
+    attn.read(pool, ints(0, 1), ints(2 ** 31 - 512), table, n_tokens=1)
+    assert attn.get_error() == lib.SV_OK
+
+
+def test_token_counts_near_2_31_are_refused(lib):
+    from speculative_decoding_verification_68_gb300 import attention
+    attn = lib.SpecAttention(1, 1, 64, 1)
+    pool = attn.alloc_pool(1, 16)
+    batch, rows, cu = attention._CBatch(), attention._CRows(), ints(0, 0)
+    batch.cu = batch.kv_len = batch.page_table = cu.data_ptr()
+    batch.n_seqs, batch.max_pages, batch.n_tokens = 1, 1, 2 ** 31 - 511
+    rows.ptr, rows.token_stride, rows.head_stride = pool.k.data_ptr(), 64, 64
+    b, r, out = ctypes.byref(batch), ctypes.byref(rows), pool.v.data_ptr()
+    assert attn._lib.spec_attn_append(attn._h, pool._ref, b, r, r, None) == SV_ERR_SIZE
+    assert attn._lib.spec_attn_read(attn._h, pool._ref, b, out, out, None) == SV_ERR_SIZE
+    assert attn._lib.spec_attn_chunk(attn._h, pool._ref, b, r, 1, 1.0, out, None, None) == SV_ERR_SIZE
+    assert attn._lib.spec_attn_prompt(attn._h, 1, batch.n_tokens, batch.cu, r, r, r, 1.0, out, None, None) == SV_ERR_SIZE
+    assert attn.get_error() == lib.SV_OK
