@@ -72,7 +72,7 @@ class Server:
         lengths = torch.tensor([len(p) for p in prompts], dtype=torch.int32, device="cuda")
         cu = torch.nn.functional.pad(lengths.cumsum(0), (1, 0)).int()
         tokens = torch.tensor([t for p in prompts for t in p], device="cuda")
-        self.kv_len = lengths
+        self.kv_len, self.longest = lengths, max(len(p) for p in prompts)
 
         def attention(layer, q, k, v):
             self.attn.append(self.pools[layer], k, v, cu, lengths, self.table)
@@ -96,11 +96,11 @@ class Server:
             rows.append(logits)
         drafts = torch.stack(drafts, 1)
         tokens = torch.cat([self.last[:, None], drafts], 1).flatten()
-        length = self.kv_len + k + 1
+        length, self.longest = self.kv_len + k + 1, self.longest + k + 1         # on the device, and a bound here
 
         def attention(layer, q, key, v):
             self.attn.append(self.pools[layer], key, v, self.step_cu, length, self.table)
-            return self.attn.attend(self.pools[layer], q, self.step_cu, length, self.table)["out"]
+            return self.attn.attend(self.pools[layer], q, self.step_cu, length, self.table, max_kv=self.longest)["out"]
 
         target = self.model.forward(tokens, attention).view(B, k + 1, -1)
         out = self.verifier.verify(target, torch.stack(rows, 1), drafts.int(), temperature, uniforms)

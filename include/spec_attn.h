@@ -77,6 +77,9 @@ typedef struct spec_attn_batch {
   int32_t n_seqs;
   int32_t n_tokens;           /* rows of the token tensors; cu[n_seqs] <= n_tokens */
   int32_t max_pages;
+  int32_t max_kv;             /* no kv_len is above this, as far as the caller knows; 0: max_pages * page_size
+                               * stands for it.  Decides only which kernel spec_attn_chunk launches: give it
+                               * where page_table is wider than the batch needs.  >= 0 */
 } spec_attn_batch;
 
 /* A token tensor [n_tokens, heads, head_dim] of bf16. */

@@ -32,7 +32,7 @@ class _CPool(ctypes.Structure):
 
 class _CBatch(ctypes.Structure):
     _fields_ = [("cu", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
-                ("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
+                ("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_kv", ctypes.c_int32)]
 
 
 class _CRows(ctypes.Structure):
@@ -179,7 +179,7 @@ class SpecAttention:
     # The checks below test everything in one expression and leave it to the
     # functions above, which say what is wrong, to raise.
 
-    def _batch(self, pool, n_tokens, cu, kv_len, page_table):
+    def _batch(self, pool, n_tokens, cu, kv_len, page_table, max_kv=0):
         device = self.device
         if pool.kv_heads != self.kv_heads or pool.head_dim != self.head_dim:
             raise ValueError(f"pool of {pool.kv_heads} heads of {pool.head_dim}, expected {self.kv_heads} of {self.head_dim}")
@@ -198,7 +198,7 @@ class SpecAttention:
             check_sequences(cu, device, self.max_seqs, kv_len, page_table)
         c = self._batch_c
         c.cu, c.kv_len, c.page_table = cu.data_ptr(), kv_len.data_ptr(), page_table.data_ptr()
-        c.n_seqs, c.n_tokens, c.max_pages = n, n_tokens, width
+        c.n_seqs, c.n_tokens, c.max_pages, c.max_kv = n, n_tokens, width, max_kv
         return self._batch_ref
 
     def _rows(self, c, t, name, heads, n_tokens=None):
@@ -268,13 +268,17 @@ class SpecAttention:
         return out
 
     def attend(self, pool: KVPool, q, cu, kv_len, page_table, causal: bool = True, scale: float | None = None,
-               want_lse: bool = False, out: dict | None = None, stream=None) -> dict:
+               want_lse: bool = False, out: dict | None = None, stream=None, max_kv: int = 0) -> dict:
         """spec_attn_chunk: attention of the new tokens q [n_tokens, q_heads, head_dim]
         over the pool, which holds their keys and values already.  Returns "out"
         (like q) and, if wanted, "lse" [n_tokens, q_heads].  scale defaults to
-        head_dim ** -0.5; causal=False lets every new token see all kv_len entries."""
+        head_dim ** -0.5; causal=False lets every new token see all kv_len entries.
+        max_kv: a host-side bound of kv_len (0: unknown), which chooses the faster kernel
+        for chunks where page_table is wider than the batch needs."""
         n = self._rows(self._q_c, q, "q", self.q_heads)
-        batch = self._batch(pool, n, cu, kv_len, page_table)
+        if not 0 <= max_kv < 1 << 31:
+            raise ValueError(f"max_kv must be 0 or a length, not {max_kv}")
+        batch = self._batch(pool, n, cu, kv_len, page_table, max_kv)
         scale = self._scale(scale)
         out = self._outputs(n, want_lse, out)
         lse = out.get("lse")

@@ -221,7 +221,7 @@ static int check_pool(const spec_attn_ctx* h, const spec_attn_pool* p) {
   return SV_OK;
 }
 static int check_batch(const spec_attn_ctx* h, const spec_attn_batch* b) {
-  if (!b || b->n_seqs < 0 || b->n_tokens < 0 || b->max_pages < 0 || b->n_seqs > h->max_seqs) return SV_ERR_ARG;
+  if (!b || b->n_seqs < 0 || b->n_tokens < 0 || b->max_pages < 0 || b->max_kv < 0 || b->n_seqs > h->max_seqs) return SV_ERR_ARG;
   if (b->n_seqs > 0 && (!b->cu || !b->kv_len || (!b->page_table && b->max_pages > 0))) return SV_ERR_ARG;
   if (b->n_tokens > LEN_MAX || (long long)b->n_tokens * h->q_heads >= (1ll << 31)) return SV_ERR_SIZE;
   return SV_OK;
@@ -364,7 +364,7 @@ static AttnParams attn_params(const spec_attn_ctx* h, const Batch& B, const Rows
 // Two tiles of rows per CTA share every key block, which pays where rows are many and the products bound; one
 // tile makes twice as many items.  Measured, one tile against two: 4 chunks of 300-512 tokens over 6000-16000
 // cached 298 against 244 us; 8 prompts of 100-2048 tokens 89 against 79 us; but 64 sequences of 8 tokens over
-// 500-8000 188 against 230 us, one chunk of 113 over 6096 39 against 75 us, prompts of 25 and 15 tokens 10.6
+// 500-8000 188 against 230 us, one chunk of 113 over 6096 39 against 51 us, prompts of 25 and 15 tokens 10.6
 // against 13.8 us.  The rule: more rows per sequence and head than one tile holds, and at least 12 blocks of two
 // tiles for every SM (between 9, where one tile still won, and 14).  `keys`: how many a row sees, about.
 constexpr int TWO_TILE_UNITS = 12;
@@ -427,7 +427,10 @@ extern "C" int spec_attn_chunk(spec_attn_t h, const spec_attn_pool* pool, const 
     A.ks = pool->k_scale; A.vs = pool->v_scale;
     return h->D == 128 ? launch_attention<128, KIND_E4M3, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E4M3, 1>(h, A, mq, mk, mv, s);
   }
-  const bool two = two_tiles(h, A, (long long)B.max_pages << B.page_shift);
+  // The table's width is a poor bound where it has room for the longest sequence of all: a chunk of 113 tokens over
+  // 6096 with 64/8 heads of 128 and a table for 131,072 takes 51 us on two tiles, 39 with max_kv given.
+  const long long room = (long long)B.max_pages << B.page_shift;
+  const bool two = two_tiles(h, A, batch->max_kv > 0 && batch->max_kv < room ? batch->max_kv : room);
   if (h->D == 128) return two ? launch_attention<128, KIND_BF16, 2>(h, A, mq, mk, mv, s) : launch_attention<128, KIND_BF16, 1>(h, A, mq, mk, mv, s);
   return two ? launch_attention<64, KIND_BF16, 2>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_BF16, 1>(h, A, mq, mk, mv, s);
 }
@@ -443,7 +446,7 @@ extern "C" int spec_attn_prompt(spec_attn_t h, int n_seqs, int n_tokens, const i
   if ((rc = check_rows(q)) || (rc = check_rows(k)) || (rc = check_rows(v))) return rc;
   if (!out || ((uintptr_t)out & 31)) return SV_ERR_ARG;   // rows leave in 32-byte stores
   const cudaStream_t s = (cudaStream_t)cuda_stream;
-  const spec_attn_batch batch = {cu, nullptr, nullptr, n_seqs, n_tokens, 0};
+  const spec_attn_batch batch = {cu, nullptr, nullptr, n_seqs, n_tokens, 0, 0};
   const Batch B = batch_of(h, &batch, nullptr);
   const AttnParams A = attn_params(h, B, rows_of(q), 1, scale, out, lse);
   CUtensorMap mq, mk, mv;

@@ -207,3 +207,33 @@ def test_keys_that_are_nan_reach_only_later_rows(lib, cached):
         clean = slice(at[b], at[b] + m // 2)
         assert_rows(got, clean, q, k[clean], v[clean], 0)
         assert torch.isnan(got["out"][at[b] + m // 2:at[b + 1]]).all()
+
+
+@pytest.mark.parametrize("new, old, hq, hkv, d", [
+    ([113], [5983], 64, 8, 128),                     # one tile: few blocks
+    ([113], [5983], 64, 8, 64),
+    ([400, 512], [6000, 2000], 32, 8, 128),          # two tiles
+    ([900, 1], [30, 0], 64, 8, 64),
+])
+def test_with_a_bound_of_the_lengths_the_tables_width_changes_nothing(lib, new, old, hq, hkv, d):
+    """A server's table has room for its longest sequence; max_kv decides how a chunk runs."""
+    page, lens = 64, [a + b for a, b in zip(new, old)]
+    _, k, v = tensors(35, sum(lens), 1, hkv, d)
+    q, _, _ = tensors(36, sum(new), hq, 1, d)
+    attn = lib.SpecAttention(hq, hkv, d, len(new))
+    pool, kv_len, table = paged(attn, k, v, lens, page)
+    cu, at = starts(new), starts(lens).tolist()
+    got = attn.attend(pool, q, cu, kv_len, table, want_lse=True, max_kv=max(lens))
+    for width in (table.shape[1] + 1, 131072 // page, 1 << 20):
+        wide = torch.full((len(new), width), -1, dtype=torch.int32, device="cuda")
+        wide[:, :table.shape[1]] = table
+        again = attn.attend(pool, q, cu, kv_len, wide, want_lse=True, max_kv=max(lens))
+        assert torch.equal(got["out"], again["out"]) and torch.equal(got["lse"], again["lse"])
+    low = attn.attend(pool, q, cu, kv_len, table, want_lse=True, max_kv=1)     # a wrong bound costs time only
+    assert attn.get_error() == lib.SV_OK
+    for b in range(len(new)):
+        rows, keys = slice(cu[b].item(), cu[b + 1].item()), slice(at[b], at[b + 1])
+        assert_rows(got, rows, q, k[keys], v[keys], old[b])
+        assert_rows(low, rows, q, k[keys], v[keys], old[b])
+    with pytest.raises(ValueError, match="max_kv"):
+        attn.attend(pool, q, cu, kv_len, table, max_kv=-1)
