@@ -30,16 +30,17 @@
  * Conventions are those of spec_verify.h: device pointers, caller's buffers,
  * asynchronous on `cuda_stream`, status codes, argument errors found on the
  * host before any launch, no exception crosses the interface, one handle per
- * stream.  Token tensors are bf16 with a contiguous last dimension, 16-byte
- * aligned, token and head strides (in elements) multiples of 8; the attention
- * calls refuse (SV_ERR_ARG) strides their copies cannot express, such as 0
- * over several heads.  n_tokens * q_heads stays below 2^31, n_tokens and every
- * kv_len below 2^31 - 511.  Metadata (cu, kv_len, page_table) is int32 on the
- * device and is checked there: a sequence with a decreasing or out-of-range cu,
- * a kv_len outside [0, max_pages * page_size] or past that limit, or a page
- * outside [0, num_pages) makes no access out of bounds; spec_attn_get_error
- * reports SV_ERR_DATA, append skips the token, and rows of read and of attention
- * that cannot be computed are NaN.
+ * stream.  Calls need the device that was current at spec_attn_init to be
+ * current (SV_ERR_ARG otherwise; spec_attn_destroy does not).  Token tensors are
+ * bf16 with a contiguous last dimension, 16-byte aligned, token and head strides
+ * (in elements) multiples of 8; the attention calls refuse (SV_ERR_ARG) strides
+ * their copies cannot express, such as 0 over several heads.  n_tokens * q_heads
+ * stays below 2^31, n_tokens and every kv_len below 2^31 - 511.  Metadata (cu,
+ * kv_len, page_table) is int32 on the device and is checked there: a sequence
+ * with a decreasing or out-of-range cu, a kv_len outside [0, max_pages *
+ * page_size] or past that limit, or a page outside [0, num_pages) makes no
+ * access out of bounds; spec_attn_get_error reports SV_ERR_DATA, append skips
+ * the token, and rows of read and of attention that cannot be computed are NaN.
  * Rows outside every sequence's range are not written.
  */
 #ifndef SPEC_ATTN_H

@@ -210,6 +210,16 @@ static void free_ctx(spec_attn_ctx* h) {
   free(h);
 }
 
+// Launches, maps and streams are the current device's, the buffers the handle's: the two have to be the same.
+static int check_device(const spec_attn_ctx* h) {
+  int device;
+  if (!h) return SV_ERR_ARG;
+  if (cudaGetDevice(&device) != cudaSuccess) {
+    cudaGetLastError();
+    return SV_ERR_CUDA;
+  }
+  return device == h->device ? SV_OK : SV_ERR_ARG;
+}
 static bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 static int check_pool(const spec_attn_ctx* h, const spec_attn_pool* p) {
@@ -251,9 +261,8 @@ static int launched() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ER
 
 extern "C" int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch,
                                 const spec_attn_rows* k, const spec_attn_rows* v, void* cuda_stream) {
-  if (!h) return SV_ERR_ARG;
   int rc;
-  if ((rc = check_pool(h, pool)) || (rc = check_batch(h, batch))) return rc;
+  if ((rc = check_device(h)) || (rc = check_pool(h, pool)) || (rc = check_batch(h, batch))) return rc;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return SV_OK;
   if ((rc = check_rows(k)) || (rc = check_rows(v))) return rc;
   const cudaStream_t s = (cudaStream_t)cuda_stream;
@@ -272,9 +281,8 @@ extern "C" int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const
 
 extern "C" int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch,
                               void* k_out, void* v_out, void* cuda_stream) {
-  if (!h) return SV_ERR_ARG;
   int rc;
-  if ((rc = check_pool(h, pool)) || (rc = check_batch(h, batch))) return rc;
+  if ((rc = check_device(h)) || (rc = check_pool(h, pool)) || (rc = check_batch(h, batch))) return rc;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return SV_OK;
   if (!k_out || !v_out || ((uintptr_t)k_out | (uintptr_t)v_out) & 31) return SV_ERR_ARG;   // 32-byte stores
   const cudaStream_t s = (cudaStream_t)cuda_stream;
@@ -413,7 +421,7 @@ extern "C" int spec_attn_chunk(spec_attn_t h, const spec_attn_pool* pool, const 
                                const spec_attn_rows* q, int causal, float scale, void* out, float* lse, void* cuda_stream) {
   if (!h || !(scale > 0.0f) || !isfinite(scale)) return SV_ERR_ARG;
   int rc;
-  if ((rc = check_pool(h, pool)) || (rc = check_batch(h, batch))) return rc;
+  if ((rc = check_device(h)) || (rc = check_pool(h, pool)) || (rc = check_batch(h, batch))) return rc;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return SV_OK;
   if ((rc = check_rows(q))) return rc;
   if (!out || ((uintptr_t)out & 31)) return SV_ERR_ARG;   // rows leave in 32-byte stores
@@ -440,8 +448,9 @@ extern "C" int spec_attn_prompt(spec_attn_t h, int n_seqs, int n_tokens, const i
                                 float scale, void* out, float* lse, void* cuda_stream) {
   if (!h || !(scale > 0.0f) || !isfinite(scale) || n_seqs < 0 || n_tokens < 0 || n_seqs > h->max_seqs) return SV_ERR_ARG;
   if (n_tokens > LEN_MAX || (long long)n_tokens * h->q_heads >= (1ll << 31)) return SV_ERR_SIZE;
-  if (n_seqs == 0 || n_tokens == 0) return SV_OK;
   int rc;
+  if ((rc = check_device(h))) return rc;
+  if (n_seqs == 0 || n_tokens == 0) return SV_OK;
   if (!cu) return SV_ERR_ARG;
   if ((rc = check_rows(q)) || (rc = check_rows(k)) || (rc = check_rows(v))) return rc;
   if (!out || ((uintptr_t)out & 31)) return SV_ERR_ARG;   // rows leave in 32-byte stores
@@ -459,8 +468,8 @@ extern "C" int spec_attn_prompt(spec_attn_t h, int n_seqs, int n_tokens, const i
 }
 
 extern "C" int spec_attn_get_error(spec_attn_t h) {
-  if (!h) return SV_ERR_ARG;
-  int f[2] = {0, 0};
+  int rc, f[2] = {0, 0};
+  if ((rc = check_device(h))) return rc;
   if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(f, h->d_flags, sizeof f, cudaMemcpyDeviceToHost) != cudaSuccess ||
       // a call whose wait expired may have left its merge counters and notes behind
       cudaMemset(h->d_flags, 0, small_bytes(h)) != cudaSuccess ||

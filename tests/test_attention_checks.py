@@ -141,3 +141,28 @@ def test_reference_attention_is_a_softmax():
     s = 0.5 * k[:, 1] @ q[2, 3]
     assert np.allclose(lse[2, 3], np.log(np.exp(s).sum()))
     assert np.allclose(out[2, 3], (np.exp(s) / np.exp(s).sum()) @ v[:, 1])
+
+
+class _FakeHandle(ctypes.Structure):
+    """A handle's first members; zeros behind them."""
+    _fields_ = [("device", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int), ("D", ctypes.c_int),
+                ("max_seqs", ctypes.c_int), ("rest", ctypes.c_byte * 256)]
+
+
+def calls_of_another_devices_handle(lib):
+    """Status of each call with a handle whose device is not the current one.  The batch has no
+    sequences, so that nothing would be launched either way."""
+    fake = _FakeHandle(device=7, q_heads=4, kv_heads=2, D=64, max_seqs=8)
+    memory = (ctypes.c_byte * 64)()
+    at = ctypes.addressof(memory) + 32 - ctypes.addressof(memory) % 32
+    pool, batch, rows = _CPool(k=at, v=at, dtype=1, num_pages=1, page_size=16), _CBatch(), _CRows(ptr=at, token_stride=64, head_stride=64)
+    h, p, b, r = (ctypes.byref(x) for x in (fake, pool, batch, rows))
+    return [lib.spec_attn_append(h, p, b, r, r, None), lib.spec_attn_read(h, p, b, at, at, None),
+            lib.spec_attn_chunk(h, p, b, r, 1, 1.0, at, None, None), lib.spec_attn_prompt(h, 0, 0, at, r, r, r, 1.0, at, None, None),
+            lib.spec_attn_get_error(h)]
+
+
+def test_a_handle_of_another_device_is_refused(lib):
+    # without a GPU there is no current device at all: every call says so, and none succeeds
+    want = sv.SV_ERR_ARG if torch.cuda.is_available() else 4            # SV_ERR_CUDA
+    assert calls_of_another_devices_handle(lib) == [want] * 5

@@ -54,3 +54,8 @@ def test_token_counts_near_2_31_are_refused(lib):
     assert attn._lib.spec_attn_chunk(attn._h, pool._ref, b, r, 1, 1.0, out, None, None) == SV_ERR_SIZE
     assert attn._lib.spec_attn_prompt(attn._h, 1, batch.n_tokens, batch.cu, r, r, r, 1.0, out, None, None) == SV_ERR_SIZE
     assert attn.get_error() == lib.SV_OK
+
+
+def test_a_handle_of_another_device_is_refused(lib):
+    from tests.test_attention_checks import calls_of_another_devices_handle
+    assert calls_of_another_devices_handle(lib._native.load()) == [lib.SV_ERR_ARG] * 5
