@@ -404,7 +404,7 @@ extern "C" int spec_attn_init(spec_attn_t* out, int q_heads, int kv_heads, int h
   // notes at ODD_NONE, flags and counters at 0, both multiples of 256 bytes; the partials need no initial value
   const size_t odd = odd_bytes(h), small = small_bytes(h);
   if (cudaMalloc(&h->memory, odd + small + ws_bytes(h->n_sm, head_dim)) != cudaSuccess || cudaMemset(h->memory, ODD_NONE & 0xff, odd) != cudaSuccess ||
-      cudaMemset(h->memory + odd, 0, small) != cudaSuccess) {
+      cudaMemset(h->memory + odd, 0, small) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) {
     cudaGetLastError();
     free_ctx(h);
     return SV_ERR_ALLOC;
@@ -472,8 +472,9 @@ extern "C" int spec_attn_get_error(spec_attn_t h) {
   if ((rc = check_device(h))) return rc;
   if (cudaDeviceSynchronize() != cudaSuccess || cudaMemcpy(f, h->d_flags, sizeof f, cudaMemcpyDeviceToHost) != cudaSuccess ||
       // a call whose wait expired may have left its merge counters and notes behind
-      cudaMemset(h->d_flags, 0, small_bytes(h)) != cudaSuccess ||
-      (f[1] && cudaMemset(h->odd, ODD_NONE & 0xff, odd_bytes(h)) != cudaSuccess)) {
+      ((f[0] || f[1]) && cudaMemset(h->d_flags, 0, f[1] ? small_bytes(h) : sizeof f) != cudaSuccess) ||
+      (f[1] && cudaMemset(h->odd, ODD_NONE & 0xff, odd_bytes(h)) != cudaSuccess) ||
+      cudaDeviceSynchronize() != cudaSuccess) {           // streams that do not wait for the default one may follow
     cudaGetLastError();
     return SV_ERR_CUDA;
   }

@@ -59,3 +59,28 @@ def test_token_counts_near_2_31_are_refused(lib):
 def test_a_handle_of_another_device_is_refused(lib):
     from tests.test_attention_checks import calls_of_another_devices_handle
     assert calls_of_another_devices_handle(lib._native.load()) == [lib.SV_ERR_ARG] * 5
+
+
+def test_calls_on_a_stream_that_waits_for_no_other_right_after_init_and_get_error(lib):
+    """What init and get_error clear is clear when they return: a call whose items are split over the
+    GPU's SMs, merged by counters, follows at once on a non-blocking stream."""
+    g = torch.Generator(device="cuda").manual_seed(40)
+    lens, page = [3000, 700], 64
+    kv_len, cu = ints(*lens), ints(0, 2, 4)
+    table = torch.arange(2 * 47, dtype=torch.int32, device="cuda").view(2, 47)
+    q = torch.randn((4, 8, 128), generator=g, device="cuda").bfloat16()
+    pool = lib.SpecAttention(8, 2, 128, 2).alloc_pool(94, page)
+    pool.k.normal_(generator=g), pool.v.normal_(generator=g)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [torch.empty_like(q) for _ in range(60)]
+    for i, out in enumerate(outs):
+        if i % 20 == 0:
+            attn = lib.SpecAttention(8, 2, 128, 2)
+        bad = i % 3 == 1                               # a flag to clear
+        attn.attend(pool, q, cu, ints(-1, -1) if bad else kv_len, table, out={"out": torch.empty_like(q)})
+        assert attn.get_error() == (lib.SV_ERR_DATA if bad else lib.SV_OK)
+        attn.attend(pool, q, cu, kv_len, table, out={"out": out}, stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, outs[0]) for out in outs) and torch.isfinite(outs[0]).all()
+    assert attn.get_error() == lib.SV_OK
