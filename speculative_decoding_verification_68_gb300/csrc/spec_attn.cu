@@ -363,7 +363,7 @@ static AttnParams attn_params(const spec_attn_ctx* h, const Batch& B, const Rows
   A.q_heads = h->q_heads; A.kv_heads = h->kv_heads; A.group = h->q_heads / h->kv_heads;
   A.tile_tokens = BM / A.group;
   A.causal = causal != 0;
-  A.c = fmaxf(scale * LOG2E_F, 1.17549435e-38f);
+  A.c = fminf(fmaxf(scale * LOG2E_F, 1.17549435e-38f), 3.40282347e38f);   // above 0 and finite, as scale is
   A.out = (__nv_bfloat16*)out; A.lse = lse;
   A.ws = h->ws; A.counters = h->counters; A.odd = h->odd;
   return A;

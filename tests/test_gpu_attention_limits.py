@@ -84,3 +84,28 @@ def test_calls_on_a_stream_that_waits_for_no_other_right_after_init_and_get_erro
     torch.cuda.synchronize()
     assert all(torch.equal(out, outs[0]) for out in outs) and torch.isfinite(outs[0]).all()
     assert attn.get_error() == lib.SV_OK
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("scale", [1e-40, 1e-38, 2.9e38])
+def test_scales_at_the_ends_of_the_range(lib, scale, dtype):
+    """Queries of zero give every key the same weight, whatever the factor."""
+    n, d = 150, 64
+    attn = lib.SpecAttention(2, 1, d, 1)
+    pool = attn.alloc_pool(10, 16, dtype)
+    g = torch.Generator(device="cuda").manual_seed(41)
+    k, v = (torch.randn((n, 1, d), generator=g, device="cuda").bfloat16() for _ in range(2))
+    q = torch.zeros((n, 2, d), dtype=BF16, device="cuda")
+    table = torch.arange(10, dtype=torch.int32, device="cuda")[None]
+    attn.append(pool, k, v, ints(0, n), ints(n), table)
+    values = attn.read(pool, ints(0, n), ints(n), table, n_tokens=n)["v"].double()
+    seen = torch.arange(1, n + 1, device="cuda")[:, None].double()
+    mean, spread = values.cumsum(0) / seen[..., None], values.abs().cumsum(0) / seen[..., None]
+    calls = [attn.attend(pool, q, ints(0, n), ints(n), table, scale=scale, want_lse=True)]
+    if dtype == BF16:
+        calls.append(attn.prompt(q, k, v, ints(0, n), scale=scale, want_lse=True))
+    assert attn.get_error() == lib.SV_OK
+    for got in calls:
+        # rounding to bf16 (2^-8) of the weights, of the sum they are divided by, of the result
+        assert ((got["out"].double() - mean).abs() <= 2.0 ** -7 * mean.abs() + 2.0 ** -8 * spread).all()
+        assert ((got["lse"].double() - seen.log()).abs() <= 2.0 ** -16).all()
