@@ -25,7 +25,23 @@
  * vector is code * 2^(byte - 127).  The exponent is the least e >= -120 with
  * max|x| <= 448 * 2^e, so codes use the format's whole range and the scaling
  * itself rounds nothing; a vector that holds an infinity or NaN is stored as
- * NaN (byte 255) and reads back as NaN.
+ * NaN (byte 255) and reads back as NaN; so does any vector of byte 255,
+ * whatever its codes.
+ *
+ * Precision of the attention calls.  Sums, maxima and the products' accumulators
+ * are 32 bits wide; the output is rounded once, to bf16.  Inputs of the matrix
+ * products are 16 bits wide, so these are rounded before:
+ *   - the softmax weights: to bf16 over bf16 keys and values (relative 2^-8; the
+ *     sum they are divided by is corrected for the largest weight of every 64
+ *     keys), or to a sum of two bf16 (2^-16) for rows of up to 1152 keys, 128
+ *     where two row tiles share a CTA; to f16 over an e4m3 pool (2^-11, and
+ *     2^-25 of the row's largest contribution);
+ *   - over an e4m3 pool query rows to f16 (2^-11, and 2^-25 of the row's largest
+ *     element).  Codes and scales are used as they are, but vectors of scale
+ *     2^-112 or less may count as zero.
+ * A weight below 2^-126 of its row's largest is 0 (times an infinite value: NaN).
+ * Scores scale * q.k reach 2^25 in magnitude over an e4m3 pool and 2^30
+ * otherwise; past that weights may leave the range of their type.
  *
  * Conventions are those of spec_verify.h: device pointers, caller's buffers,
  * asynchronous on `cuda_stream`, status codes, argument errors found on the

@@ -36,7 +36,7 @@
 //   one tile, bf16    memory: 64 sequences of 8 tokens over 500-8000 cached, 64
 //                     query and 8 key-value heads of 128, 188 us, 6.1 TB/s
 //   one tile, e4m3    shared memory and instruction issue: 64 sequences of 16 over
-//                     1000-16000, 292 us, 3.5 TB/s and 865 TFLOP/s
+//                     1000-16000, 298 us, 3.5 TB/s and 847 TFLOP/s
 //   two tiles         a tile's softmax, about 1,600 cycles, where the other's
 //                     products take 1,100: 3 prompts of 4000-6450 tokens, 32 and 8
 //                     heads of 128, 687 us, 1,363 TFLOP/s
@@ -236,6 +236,8 @@ struct Segment {      // a run of blocks of one item
   long long start;    // unit of the item's first block
 };
 
+// The second part has 2^-16 of every weight on top (see the softmax), which the sum of weights does not: 2^-8 of
+// the output's own rounding.
 // Rounding the weights to bf16 costs little where many keys share the error.
 // An item of few blocks has its weights in two bf16 parts and takes the product
 // with the values twice: up to 1152 keys where copies bound (one tile: 1% of the
@@ -1168,9 +1170,11 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     // reference M covers s_ij + e, so a weight times a block value stays within
     // range whatever the vectors' sizes.  e of the values is kept within 2^64 of
     // the run's largest so that the weights do not vanish.  Where a vector is
-    // smaller than that (a token of another size that some rows may not even see)
+    // smaller than that (a token of another size, which some rows may not even see)
     // the codes stay as they are and the softmax applies each vector's own
-    // exponent: a cold path, a few hundred instructions a block.  Vectors of scale
+    // exponent, in the branch that raises the reference so that ordinary blocks pay
+    // next to nothing.  Such a block takes five times as long (64 sequences of 16
+    // over 1000-16000, all of them such: 1,560 instead of 297 us).  Vectors of scale
     // BYTE_ZERO and less, which zeros have, do not count for that.
     // Four warps convert the keys, four the values, a thread a vector.  Raw lines
     // are swizzled like the f16 ones, so that eight threads of eight keys reach
