@@ -35,7 +35,9 @@
  *     sum they are divided by is corrected for the largest weight of every 64
  *     keys), or to a sum of two bf16 (2^-16) for rows of up to 1152 keys, 128
  *     where two row tiles share a CTA; to f16 over an e4m3 pool (2^-11, and
- *     2^-25 of the row's largest contribution);
+ *     2^-25 of the row's largest contribution, or of its largest weight where
+ *     the vectors share a scale: a zero vector that takes nearly all the weight
+ *     leaves the others 2^-25 of their size);
  *   - over an e4m3 pool query rows to f16 (2^-11, and 2^-25 of the row's largest
  *     element).  Codes and scales are used as they are, but vectors of scale
  *     2^-112 or less may count as zero.
