@@ -28,21 +28,34 @@
  * NaN (byte 255) and reads back as NaN; so does any vector of byte 255,
  * whatever its codes.
  *
+ * Four bits.  SV_E2M1 pools hold codes of 4 bits (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives; bit 3 is the sign), k and v [num_pages, kv_heads, page_size,
+ * head_dim / 2] bytes with element 2i in the low half of byte i; k_block and
+ * v_block [num_pages, kv_heads, page_size, head_dim / 16], an e4m3 scale for
+ * every 16 elements; and k_scale and v_scale as above.  A value is code * scale *
+ * 2^(byte - 127).  The exponent e is the least one >= -120 with max|x| <= 2688 *
+ * 2^e; a block's scale is max|x_j| / 2^e / 6 rounded to e4m3; a code is
+ * x / 2^e / scale rounded to the nearest, ties to the even code, in 32 bits.  So
+ * the largest element of a block is off by 2^-4 of itself or less and the others
+ * by up to 0.18 of the largest, in blocks above 2^-13 of their vector's largest
+ * element; below, scales lose bits, and a block of less than 2^-18 is 0.  A
+ * vector with an infinity or NaN has NaN scales too.
+ *
  * Precision of the attention calls.  Sums, maxima and the products' accumulators
  * are 32 bits wide; the output is rounded once, to bf16.  Inputs of the matrix
  * products are 16 bits wide, so these are rounded before:
  *   - the softmax weights: to bf16 over bf16 keys and values (relative 2^-8; the
  *     sum they are divided by is corrected for the largest weight of every 64
  *     keys), or to a sum of two bf16 (2^-16) for rows of up to 1152 keys, 128
- *     where two row tiles share a CTA; to f16 over an e4m3 pool (2^-11, and
+ *     where two row tiles share a CTA; to f16 over a coded pool (e4m3 or e2m1; 2^-11, and
  *     2^-25 of the row's largest contribution, or of its largest weight where
  *     the vectors share a scale: a zero vector that takes nearly all the weight
  *     leaves the others 2^-25 of their size);
- *   - over an e4m3 pool query rows to f16 (2^-11, and 2^-25 of the row's largest
+ *   - over a coded pool query rows to f16 (2^-11, and 2^-25 of the row's largest
  *     element).  Codes and scales are used as they are, but vectors of scale
  *     2^-112 or less may count as zero.
  * A weight below 2^-126 of its row's largest is 0 (times an infinite value: NaN).
- * Scores scale * q.k reach 2^25 in magnitude over an e4m3 pool and 2^30
+ * Scores scale * q.k reach 2^25 in magnitude over a coded pool and 2^30
  * otherwise; past that weights may leave the range of their type.
  *
  * Conventions are those of spec_verify.h: device pointers, caller's buffers,
@@ -74,8 +87,8 @@ extern "C" {
 
 typedef struct spec_attn_ctx* spec_attn_t;
 
-/* Element type of a quantised pool (bf16 pools are SV_BF16). */
-enum { SV_E4M3 = 2 };
+/* Element types of a coded pool (bf16 pools are SV_BF16). */
+enum { SV_E4M3 = 2, SV_E2M1 = 3 };
 
 /* A pool of cache pages (see above). */
 typedef struct spec_attn_pool {
@@ -83,9 +96,11 @@ typedef struct spec_attn_pool {
   void* v;
   uint8_t* k_scale;   /* NULL for SV_BF16 */
   uint8_t* v_scale;
-  int32_t dtype;      /* SV_BF16 or SV_E4M3 */
+  int32_t dtype;      /* SV_BF16, SV_E4M3 or SV_E2M1 */
   int32_t num_pages;
   int32_t page_size;  /* 16, 32, 64 or 128 */
+  uint8_t* k_block;   /* SV_E2M1, 16-byte aligned; not read for the others */
+  uint8_t* v_block;
 } spec_attn_pool;
 
 /* The sequences of one call. */
@@ -108,6 +123,19 @@ typedef struct spec_attn_rows {
   int64_t head_stride;
 } spec_attn_rows;
 
+/* How positions turn vectors: the first rot_dim elements form rot_dim / 2 pairs
+ * (a, b), neighbours (2i, 2i+1) where interleaved is not 0, else halves
+ * (i, i + rot_dim / 2), and pair i at position p becomes
+ * (a c - b s, b c + a s), c = table[p, i] and s = table[p, rot_dim / 2 + i], in
+ * IEEE arithmetic of 32 bits, every product and sum rounded by itself. */
+typedef struct spec_attn_rope {
+  const float* table;         /* [max_positions, rot_dim], 16-byte aligned */
+  const int32_t* positions;   /* [n_tokens], or NULL: a token's place in the cache is its position */
+  int32_t max_positions;
+  int32_t rot_dim;            /* 16, 32, .. head_dim */
+  int32_t interleaved;
+} spec_attn_rope;
+
 /* Create a handle for q_heads query heads in groups of q_heads / kv_heads per
  * key-value head, head_dim 64 or 128, and batches of up to max_seqs
  * sequences.  Allocates the workspace of the split attention (fixed size,
@@ -116,14 +144,27 @@ typedef struct spec_attn_rows {
  * <= 65536.  Uses the current CUDA device. */
 int spec_attn_init(spec_attn_t* h, int q_heads, int kv_heads, int head_dim, int max_seqs);
 
-/* Write the new tokens' keys and values into the pool, quantising to e4m3
- * where the pool holds that.  One kernel launch. */
+/* Write the new tokens' keys and values into the pool, quantising to e4m3 or
+ * e2m1 where the pool holds that.  One kernel launch. */
 int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch,
                      const spec_attn_rows* k, const spec_attn_rows* v, void* cuda_stream);
 
+/* The same with the keys rotated on the way, and, where q and q_out are not NULL,
+ * the new tokens' queries from q into q_out; where k_out is not NULL it gets the
+ * rotated keys too (spec_attn_prompt takes those).  q_out and k_out are rounded
+ * once, to bf16; the pool gets the 32-bit keys, rounded or quantised once.  q_out
+ * may be q and k_out may be k, with the same strides; no other overlap.  rope's
+ * positions, where given, turn the vectors, and the cache's slots stay those of
+ * kv_len.  A position outside [0, max_positions) is SV_ERR_DATA: the pool skips
+ * the token, and its rows of q_out and k_out are NaN, as they are where its page
+ * is invalid; a token without a slot has rows of 0.  One kernel launch. */
+int spec_attn_append_rotated(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch, const spec_attn_rope* rope,
+                             const spec_attn_rows* q, const spec_attn_rows* k, const spec_attn_rows* v,
+                             const spec_attn_rows* q_out, const spec_attn_rows* k_out, void* cuda_stream);
+
 /* Copy the batch's tokens (positions kv_len[b] - n_b .. kv_len[b] - 1) out of
  * the pool into k_out and v_out, [n_tokens, kv_heads, head_dim] contiguous
- * bf16, 32-byte aligned (e4m3 values times their power of two, rounded to nearest even where
+ * bf16, 32-byte aligned (codes times their scale and power of two, rounded to nearest even where
  * bf16 is not exact: only below its normal range).  One kernel launch. */
 int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch,
                    void* k_out, void* v_out, void* cuda_stream);

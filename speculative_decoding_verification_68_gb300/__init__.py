@@ -10,7 +10,7 @@ memory and streams.
     out["tokens"], out["tau"], out["tv"]
 
 The paged key-value cache and the attention that precede it in a serving step
-are in ``attention.py`` (``SpecAttention``, ``KVPool``; ``include/spec_attn.h``).
+are in ``attention.py`` (``SpecAttention``, ``KVPool``, ``Rope``; ``include/spec_attn.h``).
 """
 from __future__ import annotations
 
@@ -291,11 +291,11 @@ class SpecVerifier:
 
 def __getattr__(name):
     # attention.py needs torch at import time; the verifier's names do not
-    if name in ("KVPool", "SpecAttention", "SV_E4M3"):
+    if name in ("KVPool", "Rope", "SpecAttention", "SV_E2M1", "SV_E4M3"):
         from . import attention
         return getattr(attention, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
-__all__ = ["SpecVerifier", "SpecVerifyError", "build", "check_batch", "check_outputs", "output_shapes", "KVPool", "SpecAttention", "SV_E4M3", "SV_FP32", "SV_BF16", "SV_FLAG_HOST_STAGING",
+__all__ = ["SpecVerifier", "SpecVerifyError", "build", "check_batch", "check_outputs", "output_shapes", "KVPool", "Rope", "SpecAttention", "SV_E2M1", "SV_E4M3", "SV_FP32", "SV_BF16", "SV_FLAG_HOST_STAGING",
            "SV_FLAG_NO_TMA", "SV_FLAG_KERNEL_TIMING", "SV_OK", "SV_ERR_DATA", "SV_ERR_ARG", "SV_ERR_TIMEOUT"]

@@ -11,7 +11,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 SOURCES = [os.path.join(PKG, "csrc", name) for name in ("spec_verify.cu", "spec_attn.cu")]
 HEADERS = [os.path.join(ROOT, "include", name) for name in ("spec_verify.h", "spec_attn.h")] + [
-    os.path.join(PKG, "csrc", name) for name in ("attn_common.cuh", "attn_plan.cuh", "attn_tile.cuh")]
+    os.path.join(PKG, "csrc", name) for name in ("attn_common.cuh", "attn_plan.cuh", "attn_rotate.cuh", "attn_tile.cuh")]
 LIB = os.path.join(PKG, "libspec_verify.so")
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC"]
@@ -93,6 +93,8 @@ def load() -> ctypes.CDLL:
     lib.spec_attn_init.argtypes = [p(vp), i, i, i, i]
     lib.spec_attn_append.restype = i
     lib.spec_attn_append.argtypes = [vp, vp, vp, vp, vp, vp]
+    lib.spec_attn_append_rotated.restype = i
+    lib.spec_attn_append_rotated.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
     lib.spec_attn_read.restype = i
     lib.spec_attn_read.argtypes = [vp, vp, vp, vp, vp, vp]
     lib.spec_attn_chunk.restype = i

@@ -10,7 +10,12 @@ positions are).  Per layer, a verification step of k drafts is
     out = attn.attend(pool, q, cu, kv_len, page_table)["out"]
 
 and, once SpecVerifier has given the accepted lengths, a sequence drops its
-rejected tokens by lowering its kv_len.
+rejected tokens by lowering its kv_len.  Where positions rotate queries and keys,
+
+    rope = Rope(table, interleaved=False)
+    q = attn.append_rotated(pool, k, v, cu, kv_len, page_table, rope, q=q)["q"]
+
+does both on the way into the cache.
 """
 from __future__ import annotations
 
@@ -20,19 +25,25 @@ import torch
 
 from . import _native
 
-SV_E4M3 = 2
+SV_E4M3, SV_E2M1 = 2, 3
+SCALE_BLOCK = 16            # elements of an e2m1 vector that share a scale
 PAGE_SIZES = (16, 32, 64, 128)
 
 
 class _CPool(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("num_pages", ctypes.c_int32),
-                ("page_size", ctypes.c_int32)]
+                ("page_size", ctypes.c_int32), ("k_block", ctypes.c_void_p), ("v_block", ctypes.c_void_p)]
 
 
 class _CBatch(ctypes.Structure):
     _fields_ = [("cu", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
                 ("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("max_kv", ctypes.c_int32)]
+
+
+class _CRope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("max_positions", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 class _CRows(ctypes.Structure):
@@ -96,14 +107,16 @@ def check_sequences(cu, device, max_seqs: int, kv_len=None, page_table=None, pag
 
 
 class KVPool:
-    """Cache pages: k and v [num_pages, kv_heads, page_size, head_dim], bf16, or
+    """Cache pages: k and v [num_pages, kv_heads, page_size, head_dim], bf16; or
     float8_e4m3fn with k_scale and v_scale [num_pages, kv_heads, page_size] uint8
-    (a vector is code * 2^(byte - 127))."""
+    (a vector is code * 2^(byte - 127)); or float4_e2m1fn_x2 [..., head_dim / 2]
+    with those and k_block and v_block [..., head_dim / 16] float8_e4m3fn (an
+    element is code * its block's scale * 2^(byte - 127))."""
 
-    def __init__(self, k, v, k_scale=None, v_scale=None):
+    def __init__(self, k, v, k_scale=None, v_scale=None, k_block=None, v_block=None):
         if k is None or k.dim() != 4:
             raise ValueError("k must be a [num_pages, kv_heads, page_size, head_dim] tensor")
-        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        if k.dtype not in (torch.bfloat16, torch.float8_e4m3fn, torch.float4_e2m1fn_x2):
             raise ValueError(f"unsupported cache dtype {k.dtype}")
         if k.shape[0] < 1 or k.shape[2] not in PAGE_SIZES:
             raise ValueError(f"page_size {k.shape[2]} with {k.shape[0]} pages: page_size must be one of {PAGE_SIZES}, "
@@ -112,18 +125,46 @@ class KVPool:
             _check(t, name, k.dtype, tuple(k.shape), k.device)
             if t.data_ptr() % 16:
                 raise ValueError(f"{name} must be 16-byte aligned")
-        self.quantised = k.dtype == torch.float8_e4m3fn
+        four = k.dtype == torch.float4_e2m1fn_x2
+        self.quantised = k.dtype != torch.bfloat16
+        self.head_dim = k.shape[3] * (2 if four else 1)
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if self.quantised:
                 _check(t, name, torch.uint8, tuple(k.shape[:3]), k.device)
             elif t is not None:
                 raise ValueError(f"{name}: a bf16 pool has no scales")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.num_pages, self.kv_heads, self.page_size, self.head_dim = k.shape
+        for t, name in ((k_block, "k_block"), (v_block, "v_block")):
+            if four:
+                _check(t, name, torch.float8_e4m3fn, (*k.shape[:3], self.head_dim // SCALE_BLOCK), k.device)
+                if t.data_ptr() % 16:
+                    raise ValueError(f"{name} must be 16-byte aligned")
+            elif t is not None:
+                raise ValueError(f"{name}: only a 4-bit pool has scales of blocks")
+        self.k, self.v, self.k_scale, self.v_scale, self.k_block, self.v_block = k, v, k_scale, v_scale, k_block, v_block
+        self.num_pages, self.kv_heads, self.page_size = k.shape[:3]
         self.device, self.dtype = k.device, k.dtype
         self._c = _CPool(k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if self.quantised else None,
-                         v_scale.data_ptr() if self.quantised else None, SV_E4M3 if self.quantised else 1,
-                         self.num_pages, self.page_size)
+                         v_scale.data_ptr() if self.quantised else None, SV_E2M1 if four else SV_E4M3 if self.quantised else 1,
+                         self.num_pages, self.page_size, k_block.data_ptr() if four else None, v_block.data_ptr() if four else None)
+        self._ref = ctypes.byref(self._c)
+
+
+class Rope:
+    """How positions turn queries and keys: table [max_positions, rot_dim] float32
+    holds the rot_dim / 2 cosines of a position, then its sines; the pairs that
+    turn are neighbours (interleaved) or element i and i + rot_dim / 2."""
+
+    def __init__(self, table, interleaved: bool = False):
+        if table is None or table.dim() != 2:
+            raise ValueError("table must be a [max_positions, rot_dim] tensor")
+        self.max_positions, self.rot_dim = table.shape
+        _check(table, "table", torch.float32, (self.max_positions, self.rot_dim), table.device)
+        if not 1 <= self.max_positions < 1 << 31 or self.rot_dim < 16 or self.rot_dim % 16:
+            raise ValueError(f"table: shape {tuple(table.shape)}, expected at least one position and a multiple of 16 columns")
+        if table.data_ptr() % 16:
+            raise ValueError("table must be 16-byte aligned")
+        self.table, self.interleaved, self.device = table, bool(interleaved), table.device
+        self._c = _CRope(table.data_ptr(), None, self.max_positions, self.rot_dim, int(self.interleaved))
         self._ref = ctypes.byref(self._c)
 
 
@@ -144,8 +185,9 @@ class SpecAttention:
         self._current = (lambda: raw(index)) if raw else (lambda: torch.cuda.current_stream(self.device).cuda_stream)
         # argument blocks of the calls, refilled by each (a handle is not thread-safe)
         self._batch_c, self._q_c, self._k_c, self._v_c = _CBatch(), _CRows(), _CRows(), _CRows()
-        self._batch_ref, self._q_ref, self._k_ref, self._v_ref = (
-            ctypes.byref(x) for x in (self._batch_c, self._q_c, self._k_c, self._v_c))
+        self._q_out_c, self._k_out_c = _CRows(), _CRows()
+        self._batch_ref, self._q_ref, self._k_ref, self._v_ref, self._q_out_ref, self._k_out_ref = (
+            ctypes.byref(x) for x in (self._batch_c, self._q_c, self._k_c, self._v_c, self._q_out_c, self._k_out_c))
 
     def close(self):
         if getattr(self, "_h", None):
@@ -168,13 +210,15 @@ class SpecAttention:
         return self._current() if stream is None else stream.cuda_stream
 
     def alloc_pool(self, num_pages: int, page_size: int = 64, dtype=torch.bfloat16) -> KVPool:
-        """An empty pool for this handle's heads."""
+        """An empty pool for this handle's heads: bfloat16, float8_e4m3fn or float4_e2m1fn_x2."""
         shape = (num_pages, self.kv_heads, page_size, self.head_dim)
-        k, v = (torch.zeros(shape, dtype=torch.uint8 if dtype == torch.float8_e4m3fn else dtype, device=self.device) for _ in range(2))
-        if dtype != torch.float8_e4m3fn:
-            return KVPool(k, v)
+        if dtype not in (torch.float8_e4m3fn, torch.float4_e2m1fn_x2):
+            return KVPool(*(torch.zeros(shape, dtype=dtype, device=self.device) for _ in range(2)))
+        four = dtype == torch.float4_e2m1fn_x2
+        codes = [torch.zeros((*shape[:3], shape[3] // 2 if four else shape[3]), dtype=torch.uint8, device=self.device).view(dtype) for _ in range(2)]
         scales = [torch.full(shape[:3], 127, dtype=torch.uint8, device=self.device) for _ in range(2)]
-        return KVPool(k.view(dtype), v.view(dtype), *scales)
+        blocks = [torch.zeros((*shape[:3], shape[3] // SCALE_BLOCK), dtype=torch.float8_e4m3fn, device=self.device) for _ in range(2)] if four else ()
+        return KVPool(*codes, *scales, *blocks)
 
     # The checks below test everything in one expression and leave it to the
     # functions above, which say what is wrong, to raise.
@@ -248,6 +292,49 @@ class SpecAttention:
         if rc:
             self._status(rc, "spec_attn_append")
 
+    def append_rotated(self, pool: KVPool, k, v, cu, kv_len, page_table, rope: Rope, q=None, positions=None, want_k: bool = False,
+                       out: dict | None = None, stream=None) -> dict:
+        """spec_attn_append_rotated: as append, with the keys rotated by their
+        positions on the way.  With q [n_tokens, q_heads, head_dim] the queries are
+        rotated too, into "q" of the result, and with want_k the rotated keys are
+        returned as "k" (for prompt).  positions: int32 [n_tokens], in place of the
+        tokens' places in the cache.  out may hold "q" and "k", which may be q and k
+        themselves (and no other tensor that overlaps them)."""
+        n = self._rows(self._k_c, k, "k", self.kv_heads)
+        self._rows(self._v_c, v, "v", self.kv_heads, n)
+        batch = self._batch(pool, n, cu, kv_len, page_table)
+        if rope.device != self.device:
+            raise ValueError(f"rope is on {rope.device}, expected {self.device}")
+        if rope.rot_dim > self.head_dim:
+            raise ValueError(f"rope turns {rope.rot_dim} elements of {self.head_dim}")
+        if positions is not None:
+            _check(positions, "positions", torch.int32, (n,), self.device)
+        rope._c.positions = None if positions is None else positions.data_ptr()
+        if q is not None:
+            self._rows(self._q_c, q, "q", self.q_heads, n)
+        if out is None:
+            out = {}
+            if q is not None:
+                out["q"] = torch.empty((n, self.q_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+            if want_k:
+                out["k"] = torch.empty((n, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+        elif (q is None) != (out.get("q") is None):
+            raise ValueError("q and output q go together")
+        elif want_k and out.get("k") is None:
+            raise ValueError("output k is required")
+        q_out, k_out = out.get("q"), out.get("k")
+        for name, t, src, c, heads in (("q", q_out, q, self._q_out_c, self.q_heads), ("k", k_out, k, self._k_out_c, self.kv_heads)):
+            if t is not None:
+                self._rows(c, t, f"output {name}", heads, n)
+                if n > 1 and abs(c.token_stride) < self.head_dim or heads > 1 and abs(c.head_stride) < self.head_dim:
+                    raise ValueError(f"output {name}: strides {tuple(t.stride())} let its rows overlap")
+        rc = self._lib.spec_attn_append_rotated(
+            self._h, pool._ref, batch, rope._ref, None if q is None else self._q_ref, self._k_ref, self._v_ref,
+            None if q_out is None else self._q_out_ref, None if k_out is None else self._k_out_ref, self._stream(stream))
+        if rc:
+            self._status(rc, "spec_attn_append_rotated")
+        return out
+
     def read(self, pool: KVPool, cu, kv_len, page_table, n_tokens: int, out: dict | None = None, stream=None) -> dict:
         """spec_attn_read: positions kv_len[b] - n_b .. kv_len[b] - 1 of every sequence
         as bf16 tensors "k" and "v" [n_tokens, kv_heads, head_dim]; n_tokens is at
@@ -318,4 +405,4 @@ class SpecAttention:
         return self._lib.spec_attn_get_error(self._h)
 
 
-__all__ = ["KVPool", "SpecAttention", "SV_E4M3", "check_rows", "check_sequences"]
+__all__ = ["KVPool", "Rope", "SpecAttention", "SV_E2M1", "SV_E4M3", "check_rows", "check_sequences"]

@@ -30,6 +30,8 @@ struct Pool {
   void* v;
   uint8_t* ks;
   uint8_t* vs;
+  uint8_t* kb;                     // e2m1: a scale for every 16 codes
+  uint8_t* vb;
 };
 struct Rows {
   const __nv_bfloat16* ptr;
@@ -66,6 +68,21 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
 __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint16_t c) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(c));
+  return r;
+}
+// eight e2m1 codes, the first in the lowest bits, to f16 values times f (both of a pair alike)
+__device__ __forceinline__ void e2m1_to_f16(uint32_t c, uint32_t f, uint32_t* y) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]) : "r"(c));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(y[i]) : "r"(f));
+}
+// eight floats to e2m1 codes (nearest even, saturating), the first in the lowest bits
+__device__ __forceinline__ uint32_t pack_e2m1(const float* x) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {

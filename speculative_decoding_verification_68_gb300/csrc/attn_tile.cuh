@@ -53,7 +53,9 @@
 
 namespace {
 
-enum { KIND_BF16 = 0, KIND_E4M3 = 1, KIND_PACKED = 2 };
+enum { KIND_BF16 = 0, KIND_E4M3 = 1, KIND_PACKED = 2, KIND_E2M1 = 3 };
+// Kinds whose codes become f16 in shared memory
+__host__ __device__ constexpr bool is_coded(int kind) { return kind == KIND_E4M3 || kind == KIND_E2M1; }
 
 constexpr int HALF_BYTES = BN * 128;  // 64 of the D columns of a block: 128 rows of one swizzled 128-byte line
 constexpr float LAZY = 8.0f;        // log2 of how far scores may pass the reference: f16 weights hold 2^15
@@ -72,7 +74,8 @@ constexpr float WIDE = 1.2676506e30f;   // 2^100, in place of the exponent of a 
 struct AttnParams {
   Batch B;
   Rows Q;
-  const uint8_t *ks, *vs;           // scale bytes (e4m3)
+  const uint8_t *ks, *vs;           // scale bytes (coded caches)
+  const uint8_t *kb, *vb;           // block scales (e2m1)
   int q_heads, kv_heads, group;
   int tile_tokens;                  // floor(128 / group)
   int causal;
@@ -243,7 +246,7 @@ struct Segment {      // a run of blocks of one item
 // with the values twice: up to 1152 keys where copies bound (one tile: 1% of the
 // time over the range, 2% up to 2048), up to 128 where the products do (a block of
 // two tiles takes 2.5 instead of 1.6 us).
-template <int KIND, int MT> __device__ __forceinline__ bool two_parts(const Segment& g) { return KIND != KIND_E4M3 && g.nblk <= (MT == 1 ? 9 : 1); }
+template <int KIND, int MT> __device__ __forceinline__ bool two_parts(const Segment& g) { return !is_coded(KIND) && g.nblk <= (MT == 1 ? 9 : 1); }
 
 // Walks one CTA's run of units.  Every role walks on its own.
 struct Walker {
@@ -283,14 +286,14 @@ struct Walker {
 // Causal rows see a prefix of the keys, so what such values do to a row follows
 // from three keys per column: the first with NaN, +inf and -inf.  Only blocks
 // that some rows see in part need this; elsewhere the products carry it.
-template <int D, bool FP8, typename Piece>
+template <int D, bool CODED, typename Piece>
 __device__ __forceinline__ void note_odd(int* odd, int* flag, Piece piece, int half, int key) {
 #pragma unroll 1
   for (int i = 0; i < D / 16; ++i) {
     uint16_t* const v = (uint16_t*)piece(i);
 #pragma unroll 1
     for (int e = 0; e < 8; ++e) {
-      const uint32_t w = v[e], inf = FP8 ? 0x7c00u : 0x7f80u;
+      const uint32_t w = v[e], inf = CODED ? 0x7c00u : 0x7f80u;
       if ((w & inf) != inf) continue;
       v[e] = 0;
       const int kind = (w & 0x7fffu) != inf ? 0 : w >> 15 ? 2 : 1;
@@ -315,10 +318,26 @@ __device__ __forceinline__ int scale_bytes(const AttnParams& A, const Segment& g
 __device__ __forceinline__ int value_exponent(int byte) { return min(max(byte - EXP_BIAS, EV_MIN), EV_MAX); }
 // A sum of weights times 2^x, x <= 0.  That of an e4m3 cache may be as large as 2^126 (see EV_MIN), so that the
 // product is a normal number where 2^x alone is not: two steps.
-template <bool FP8> __device__ __forceinline__ float scaled(float l, float x) {
-  if (!FP8) return ex2(x) * l;
+template <bool CODED> __device__ __forceinline__ float scaled(float l, float x) {
+  if (!CODED) return ex2(x) * l;
   const float h = ex2(0.5f * x);
   return h * l * h;
+}
+// The e4m3 scales of an e2m1 vector: one for every 16 codes
+template <int D> struct Scales {
+  uint32_t w[D / 64];
+  __device__ __forceinline__ uint16_t pair(int i) const { return (uint16_t)(w[i / 2] >> (16 * (i % 2))); }
+};
+template <int D> __device__ __forceinline__ Scales<D> ldg_scales(const uint8_t* p) {
+  Scales<D> r;
+  if constexpr (D == 128) {
+    const uint2 x = __ldg((const uint2*)p);
+    r.w[0] = x.x;
+    r.w[1] = x.y;
+  } else {
+    r.w[0] = __ldg((const uint32_t*)p);
+  }
+  return r;
 }
 // What a row that sees keys 0 .. lim-1 has in a column (0: nothing)
 template <int D> __device__ __forceinline__ float odd_value(const int* odd, int col, int lim) {
@@ -329,26 +348,27 @@ template <int D> __device__ __forceinline__ float odd_value(const int* odd, int 
 // -------------------------------------------------------------------- kernel
 template <int D, int KIND, int MT>
 struct Cfg {
-  static constexpr bool FP8 = KIND == KIND_E4M3;
+  static constexpr bool CODED = is_coded(KIND), E2M1 = KIND == KIND_E2M1;
   static constexpr int HALVES = D / 64;
   static constexpr int BUF = HALVES * HALF_BYTES;             // a block of keys or values in 16 bits
   static constexpr int QBYTES = MT * BUF;
-  static constexpr int RAW = BN * D;                          // a block of codes
-  static constexpr int NRAW = FP8 ? (D == 128 ? 4 : 8) : 0;
+  static constexpr int LINE = E2M1 ? D / 2 : D;               // bytes of a vector's codes
+  static constexpr int RAW = BN * LINE;                       // a block of codes
+  static constexpr int NRAW = !CODED ? 0 : D == 128 && !E2M1 ? 4 : 8;
   static constexpr int SMALL = 3072;                          // barriers and bookkeeping, behind the buffers
-  static constexpr int NBUF = FP8 ? (D == 128 ? 4 : 6) : (SMEM_LIMIT - SMALL - QBYTES) / BUF;
+  static constexpr int NBUF = CODED ? (D == 128 ? 4 : 6) : (SMEM_LIMIT - SMALL - QBYTES) / BUF;
   static constexpr int NK = (NBUF + 1) / 2, NV = NBUF / 2;
   static constexpr int SMEM = QBYTES + NBUF * BUF + NRAW * RAW + SMALL;
   static constexpr int Q_WARP0 = 2, Q_WARPS = 2;
   static constexpr int SOFT_WARP0 = 4, SOFT_WARPS = 8;        // per tile
   static constexpr int CONV_WARP0 = SOFT_WARP0 + SOFT_WARPS * MT;
-  static constexpr int CONV_WARPS = FP8 ? 8 : 0;
+  static constexpr int CONV_WARPS = CODED ? 8 : 0;
   static constexpr int WARPS = CONV_WARP0 + CONV_WARPS;
   static constexpr int THREADS = WARPS * 32;
   // Registers: five warpgroups start with 96 each; the first one, which copies and issues, or for e4m3 the
   // converting ones give up what the softmax needs to hold half a row of scores (64 sequences of 16 tokens over
   // 1000-16000 e4m3: 327 us with 96 for all, 297 with 120 and 72, 299 with 112 and 80).
-  static constexpr int REGS_SOFT = MT == 2 ? 104 : FP8 ? 120 : 0, REGS_WORK = FP8 ? 96 : 64, REGS_CONV = 72;
+  static constexpr int REGS_SOFT = MT == 2 ? 104 : CODED ? 120 : 0, REGS_WORK = CODED ? 96 : 64, REGS_CONV = 72;
   static_assert(REGS_SOFT == 0 || 128 * REGS_WORK + SOFT_WARPS * MT * 32 * REGS_SOFT + CONV_WARPS * 32 * REGS_CONV <= THREADS * 96, "register split");
   static constexpr int INFO = 8;                              // ring of block references (more than NK + 1)
 };
@@ -382,7 +402,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   static_assert(sizeof(Segment) <= 64, "ring of runs");
   float* const swap = (float*)(small + 1024);             // [tile][half][row]: between the two threads of a row
   float* const q_scale = (float*)(small + 2048);          // [2][row]: powers of two taken out of query rows (e4m3)
-  static_assert(!C::FP8 || MT == 1, "the second tile's part of swap lies over q_scale");
+  static_assert(!C::CODED || MT == 1, "the second tile's part of swap lies over q_scale");
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int tile_rows = MT * A.tile_tokens;
@@ -390,11 +410,11 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 
   // ---- set-up: barriers, tensor memory, and this CTA's run of units
   if (tid == 0) {
-    for (int i = 0; i < NK; ++i) { bar_init(k_full + 8 * i, C::FP8 ? 4 : 1); bar_init(k_empty + 8 * i, 1); }
-    for (int i = 0; i < NV; ++i) { bar_init(v_full + 8 * i, C::FP8 ? 4 : 1); bar_init(v_empty + 8 * i, 1); }
+    for (int i = 0; i < NK; ++i) { bar_init(k_full + 8 * i, C::CODED ? 4 : 1); bar_init(k_empty + 8 * i, 1); }
+    for (int i = 0; i < NV; ++i) { bar_init(v_full + 8 * i, C::CODED ? 4 : 1); bar_init(v_empty + 8 * i, 1); }
     for (int i = 0; i < C::NRAW; ++i) { bar_init(raw_full + 8 * i, 1); bar_init(raw_empty + 8 * i, 4); }
     for (int i = 0; i < 2; ++i) { bar_init(s_full + 8 * i, 1); bar_init(p_full + 8 * i, C::SOFT_WARPS); bar_init(o_done + 8 * i, 1); }
-    bar_init(q_full, C::FP8 ? C::Q_WARPS : 1);
+    bar_init(q_full, C::CODED ? C::Q_WARPS : 1);
     bar_init(q_empty, 1);
     bar_init(drain, 1);
     for (int i = 0; i < 4; ++i) odd_flag[i] = 0;
@@ -506,7 +526,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   const bool busy = W.any();
   // tensor memory: scores (and weights over them) at 0 and 128, outputs at 256 and 384
   const uint32_t S_COL = tmem, O_COL = tmem + 256;
-  constexpr bool BF = !C::FP8;
+  constexpr bool BF = !C::CODED;
   constexpr uint32_t ID_QK = instr_desc(BF, BN, false), ID_PV = instr_desc(BF, D, true);
   Segment g;
 
@@ -534,12 +554,12 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
           const CUtensorMap* const map = kv ? &map_v : &map_k;
-          if constexpr (C::FP8) {
+          if constexpr (C::CODED) {
             const unsigned n = nk++, s = n % C::NRAW;
             if (!(ok = bar_wait(raw_empty + 8 * s, ((n / C::NRAW) & 1) ^ 1, flags))) break;
             if (lane == 0) bar_expect(raw_full + 8 * s, C::RAW);
             __syncwarp();
-            if (lane < ppb) tma_2d(raw_at + s * C::RAW + lane * ps * D, map, 0, cur, raw_full + 8 * s);
+            if (lane < ppb) tma_2d(raw_at + s * C::RAW + lane * ps * C::LINE, map, 0, cur, raw_full + 8 * s);
           } else {
             const unsigned n = kv ? nv++ : nk++, ring = kv ? NV : NK, s = n % ring;
             const uint32_t full = (kv ? v_full : k_full) + 8 * s, empty = (kv ? v_empty : k_empty) + 8 * s;
@@ -559,11 +579,11 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       }
     }
     if (!ok) {                                             // let the copies in flight land
-      const int rings = C::FP8 ? 1 : 2;
+      const int rings = C::CODED ? 1 : 2;
       for (int kv = 0; kv < rings; ++kv) {
-        const unsigned n = kv ? nv : nk, ring = C::FP8 ? C::NRAW : kv ? NV : NK;
+        const unsigned n = kv ? nv : nk, ring = C::CODED ? C::NRAW : kv ? NV : NK;
         for (unsigned i = n > ring ? n - ring : 0; i + 1 < n; ++i) {
-          const uint32_t full = (C::FP8 ? raw_full : kv ? v_full : k_full) + 8 * (i % ring);
+          const uint32_t full = (C::CODED ? raw_full : kv ? v_full : k_full) + 8 * (i % ring);
           for (int it = 0; it < 4096 && !bar_try(full, (i / ring) & 1); ++it) {}
         }
       }
@@ -663,7 +683,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       // The rows of the next run, as soon as the scores of this one are all done.
       unsigned segs = 0;
       bool ok = true;
-      if constexpr (!C::FP8) {
+      if constexpr (!C::CODED) {
         const int used = A.tile_tokens * A.group;          // rows of a tile: floor(128 / group) tokens, the same box every time
         if (warp == C::Q_WARP0) {
           for (int i = lane; i < MT * C::HALVES * (BM - used) * 8; i += 32) {   // the rest never changes
@@ -789,18 +809,18 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               return (uint4*)(line + (ch / 8) * HALF_BYTES + (((ch % 8) ^ (r & 7)) << 4));
             };
             if (key >= g.kv) {
-              if (!C::FP8)
+              if (!C::CODED)
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) *piece(i) = make_uint4(0, 0, 0, 0);
             } else {
-              constexpr uint32_t EXP = C::FP8 ? 0x7c007c00u : 0x7f807f80u;
+              constexpr uint32_t EXP = C::CODED ? 0x7c007c00u : 0x7f807f80u;
               uint32_t found = 0;
 #pragma unroll
               for (int i = 0; i < D / 16; ++i) {
                 const uint4 w = *piece(i);
                 found |= __vcmpeq2(w.x & EXP, EXP) | __vcmpeq2(w.y & EXP, EXP) | __vcmpeq2(w.z & EXP, EXP) | __vcmpeq2(w.w & EXP, EXP);
               }
-              if (found) note_odd<D, C::FP8>(A.odd + (blockIdx.x * 4 + slot) * 3 * D, odd_flag + slot, piece, half, key);
+              if (found) note_odd<D, C::CODED>(A.odd + (blockIdx.x * 4 + slot) * 3 * D, odd_flag + slot, piece, half, key);
             }
           }
           fence_async();
@@ -814,7 +834,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         tm_ld32(s_at, x);
         tm_ld32(s_at + 32, x + 32);
         float cb = c, ev = 0.0f;
-        if constexpr (C::FP8) {
+        if constexpr (C::CODED) {
           const float2 t = info[n % C::INFO];
           if (j == j0) c *= q_scale[(segs & 1) * BM + r];
           cb = fmaxf(c * t.x, 1.17549435e-38f);              // a masked score's -inf times 0 would be NaN
@@ -839,7 +859,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         if (group_or(pair, 64, j == j0 || top > M + LAZY || !ok)) {
           // Set or raise the reference, the same for both threads of the row.
           float l_wide = 0.0f, m_wide = -INFINITY;         // sum of weights of a wide block, its reference
-          if (C::FP8 && ev == WIDE) {
+          if (C::CODED && ev == WIDE) {
             // The block's vectors are too far apart for one scale (no score is so low that top misses WIDE):
             // s_ij + e_j, with each vector's own exponents, in place of the scores; the sum is without e_j.
             const float x_all = info[n % C::INFO].x;       // keys' factor if positive, else their own and maybe -256 - the values' exponent
@@ -886,7 +906,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               tc_after();
             }
             const float f = up == -INFINITY ? 1.0f : ex2(M - up);
-            if (C::FP8 && f == 0.0f && l > 0.0f) l = scaled<true>(l, M - up);
+            if (C::CODED && f == 0.0f && l > 0.0f) l = scaled<true>(l, M - up);
             else l *= f;
             off *= f;
 #pragma unroll 1
@@ -899,7 +919,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             }
           }
           M = up;
-          if (C::FP8 && ev == WIDE) {
+          if (C::CODED && ev == WIDE) {
             l += scaled<true>(l_wide, M == -INFINITY ? 0.0f : m_wide - M);
             ev = 0.0f;
           }
@@ -921,13 +941,13 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             a = ex2(a);
             b = ex2(b);
             acc[i & 1] = add2(acc[i & 1], pk(a, b));
-            w[i] = C::FP8 ? pack_f16(a, b) : pack_bf16(a, b);
-            if (!C::FP8) {
+            w[i] = C::CODED ? pack_f16(a, b) : pack_bf16(a, b);
+            if (!C::CODED) {
               x[32 * h + 2 * i] = __float_as_uint(a);
               x[32 * h + 2 * i + 1] = __float_as_uint(b);
             }
           }
-          if (!C::FP8 && split) {
+          if (!C::CODED && split) {
             // the first part rounded towards 0, the second with 2^-16 of the weight on top: it is positive
             // where the weight is, and an infinite value stays one
 #pragma unroll
@@ -946,8 +966,8 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         upk(acc[0], s0, s1);
         upk(acc[1], s2, s3);
         const float add = (s0 + s1) + (s2 + s3);
-        l += C::FP8 ? add * ex2(-info[n % C::INFO].y) : add;   // 0 where it has been added already
-        if (!C::FP8 && !split) {
+        l += C::CODED ? add * ex2(-info[n % C::INFO].y) : add;   // 0 where it has been added already
+        if (!C::CODED && !split) {
           // what rounding to bf16 did to the largest of these weights (see the run's result)
           const float p = ex2(fmaf(best, cb, neg));
           off += __bfloat162float(__float2bfloat16(p)) - p;
@@ -1058,7 +1078,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
                           d0 = __ldcg(p + 2 * BM + r), d1 = __ldcg(q + 2 * BM + r);
               const float4 *const po = (const float4*)(p + 3 * BM) + half * (DH / 4) * BM + r, *const qo = (const float4*)(q + 3 * BM) + half * (DH / 4) * BM + r;
               const float m_top = fmaxf(m0, m1), ref = m_top == -INFINITY ? 0.0f : m_top;
-              const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref), sum = scaled<C::FP8>(l0, m0 - ref) + scaled<C::FP8>(l1, m1 - ref);
+              const float f0 = ex2(m0 - ref), f1 = ex2(m1 - ref), sum = scaled<C::CODED>(l0, m0 - ref) + scaled<C::CODED>(l1, m1 - ref);
               const float inv = sum == 0.0f ? 0.0f : 1.0f / (sum + f0 * d0 + f1 * d1), w0 = f0 * inv, w1 = f1 * inv;
               const int rt = r / A.group;
               const size_t to = (size_t)(g.row0 + tile * A.tile_tokens + rt) * A.q_heads + g.head * A.group + r - rt * A.group;
@@ -1096,7 +1116,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
             for (int x = c0; x <= c1; ++x) {
               float* const p = part(x, x == c0);
               const float x2 = __ldcg(p + ts) - ref;
-              sum += scaled<C::FP8>(__ldcg(p + BM + ts), x2);
+              sum += scaled<C::CODED>(__ldcg(p + BM + ts), x2);
               fix += ex2(x2) * __ldcg(p + 2 * BM + ts);
             }
             const float inv = nan ? quiet_nan() : sum == 0.0f ? 0.0f : 1.0f / (sum + fix);
@@ -1160,7 +1180,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       if (!g.more) break;
     } while (true);
     }
-  } else if constexpr (C::FP8) {
+  } else if constexpr (C::CODED) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONV));
     if (busy) {
     // ---------------------------------------------- e4m3 codes to f16 blocks
@@ -1185,7 +1205,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     const uint32_t full0 = kv ? v_full : k_full, empty0 = kv ? v_empty : k_empty;
     const unsigned ring = kv ? NV : NK;
     uint8_t* const out0 = gbase + ((kv ? v_at : k_at) - base) + key * 128;
-    const uint8_t* const raw0 = gbase + (raw_at - base) + key * D;
+    const uint8_t* const raw0 = gbase + (raw_at - base) + key * C::LINE;
     unsigned n = 0;
     bool ok = true, stop = false;
     while (!stop && W.next(A, tile_rows, g)) {
@@ -1201,20 +1221,31 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const size_t at = ((size_t)(page * A.kv_heads + g.head) << A.B.page_shift) + ((j * BN + key) & ((1 << A.B.page_shift) - 1));
         return make_int2(kv ? 0 : __ldg(A.ks + at), __ldg(A.vs + at));
       };
+      // the e4m3 scales of this thread's vector, one for every 16 codes
+      auto load_scales = [&](int j, int page) {
+        Scales<D> r = {};
+        if (!C::E2M1 || (unsigned)page >= (unsigned)A.B.num_pages) return r;
+        const size_t at = ((size_t)(page * A.kv_heads + g.head) << A.B.page_shift) + ((j * BN + key) & ((1 << A.B.page_shift) - 1));
+        return ldg_scales<D>((kv ? A.vb : A.kb) + at * (D / 16));
+      };
       // largest byte of a warp's vectors, and in the upper half 255 - the smallest that counts
       auto extremes = [&](int byte) {
         const int most = __reduce_max_sync(FULL, byte == BYTE_NAN ? 0 : byte);
         return most | __reduce_max_sync(FULL, byte == BYTE_NAN || byte <= BYTE_ZERO ? 0 : 255 - byte) << 16;
       };
-      int2 nxt = load_bytes(g.j0, page_of(g.j0));
-      int page = page_of(g.j0 + 1);
+      int page = page_of(g.j0);
+      int2 nxt = load_bytes(g.j0, page);
+      Scales<D> nxt_scales = load_scales(g.j0, page);
+      page = page_of(g.j0 + 1);
       for (int j = g.j0; j < g.j1; ++j, ++n) {
         const int2 cur = nxt;
+        const Scales<D> scales = nxt_scales;
         const int ka = kv ? 0 : extremes(cur.x), va = extremes(cur.y);
         int2* const wm = wmax + (n & 1) * 4;
         if (lane == 0) wm[warp & 3] = make_int2(ka, va);
         if ((stop = group_or(bar_id, BN, !ok))) break;     // all four warps leave, or none
         nxt = load_bytes(j + 1, page);
+        nxt_scales = load_scales(j + 1, page);
         page = page_of(j + 2);
         const unsigned kx = __vmaxu2(__vmaxu2(wm[0].x, wm[1].x), __vmaxu2(wm[2].x, wm[3].x));
         const unsigned vx = __vmaxu2(__vmaxu2(wm[0].y, wm[1].y), __vmaxu2(wm[2].y, wm[3].y));
@@ -1232,27 +1263,45 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const uint8_t* const src = raw0 + rs * C::RAW;
         uint8_t* const dst = out0 + bs * C::BUF;
         if (ok) {
-#pragma unroll 1
-          for (int h = 0; h < D / 64; ++h) {               // 64 codes: one line of the f16 block
-            uint4 xs[4];
+          if constexpr (C::E2M1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int ch = 4 * h + i;
-              xs[i] = *(const uint4*)(src + ((D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4));
-              if (!valid) xs[i] = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < D / 32; ++c) {             // 32 codes: half a line of the f16 block
+              const uint4 x = *(const uint4*)(src + ((D == 128 ? c ^ ((key >> 1) & 3) : c ^ ((key >> 2) & 1)) << 4));
+              uint32_t fs, y[16];                          // the scales of what is not valid are 0
+              asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(fs) : "r"(e4m3_to_f16x2(scales.pair(c))), "r"(f));
+              const uint32_t f0 = __byte_perm(fs, fs, 0x1010), f8 = __byte_perm(fs, fs, 0x3232);
+              e2m1_to_f16(x.x, f0, y);
+              e2m1_to_f16(x.y, f0, y + 4);
+              e2m1_to_f16(x.z, f8, y + 8);
+              e2m1_to_f16(x.w, f8, y + 12);
+              uint8_t* const line = dst + (c / 2) * HALF_BYTES;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *(uint4*)(line + (((4 * (c % 2) + i) ^ (key & 7)) << 4)) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
             }
+          } else {
+#pragma unroll 1
+            for (int h = 0; h < D / 64; ++h) {             // 64 codes: one line of the f16 block
+              uint4 xs[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t w[4] = {xs[i].x, xs[i].y, xs[i].z, xs[i].w};
-              uint32_t y[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint32_t hcode = e4m3_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(hcode), "r"(f));
+              for (int i = 0; i < 4; ++i) {
+                const int ch = 4 * h + i;
+                xs[i] = *(const uint4*)(src + ((D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4));
+                if (!valid) xs[i] = make_uint4(0, 0, 0, 0);
               }
-              uint8_t* const line = dst + h * HALF_BYTES;
-              *(uint4*)(line + (((2 * i) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-              *(uint4*)(line + (((2 * i + 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t w[4] = {xs[i].x, xs[i].y, xs[i].z, xs[i].w};
+                uint32_t y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const uint32_t hcode = e4m3_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+                  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(hcode), "r"(f));
+                }
+                uint8_t* const line = dst + h * HALF_BYTES;
+                *(uint4*)(line + (((2 * i) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+                *(uint4*)(line + (((2 * i + 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+              }
             }
           }
         }

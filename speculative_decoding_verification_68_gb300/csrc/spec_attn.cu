@@ -9,53 +9,12 @@
 #include <string.h>
 
 #include "attn_common.cuh"
+#include "attn_rotate.cuh"
 #include "attn_tile.cuh"
 #include "spec_attn.h"
 
 namespace {
 
-// ------------------------------------------------------- where a token lives
-// A warp works on one token at a time, all its heads: the search of its
-// sequence and page is paid once for 2 * heads vectors, whose 16-byte pieces
-// the lanes then hold, several in flight each.
-
-// The sequence that holds packed token t, or -1: 32 probes a step.  cu need not
-// be trusted: the search stays in range whatever it holds, and the result is
-// checked.
-__device__ __forceinline__ int find_seq(const Batch& B, int t, int lane) {
-  int lo = 0, hi = B.n_seqs;                      // largest b with cu[b] <= t
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) >> 5, probe = lo + lane * step;
-    const int below = __popc(__ballot_sync(FULL, probe < hi && __ldg(B.cu + min(probe, hi)) <= t));
-    lo += max(0, below - 1) * step;
-    hi = min(hi, lo + step);
-    lo = min(lo, hi - 1);
-  }
-  const int a = __ldg(B.cu + lo), e = __ldg(B.cu + lo + 1);
-  return (a >= 0 && a <= t && t < e && e <= B.n_tokens) ? lo : -1;
-}
-// Page of token t, and its slot there.  NO_ROW: in no sequence, as the rows that pad a batch are (a wrong cu
-// is reported by flag_invalid_seqs); INVALID: in one whose length or page is not valid, which is reported;
-// NO_SLOT: before the first position.
-enum { NO_SLOT = -1, INVALID = -2, NO_ROW = -3 };
-__device__ __forceinline__ int find_page(const Batch& B, int t, int lane, int& slot) {
-  const int b = find_seq(B, t, lane);
-  int page = NO_ROW;
-  if (b >= 0) {
-    const int len = __ldg(B.kv_len + b), pos = len - __ldg(B.cu + b + 1) + t;
-    if (!len_valid(B, len)) {
-      page = INVALID;
-    } else if (pos < 0) {
-      page = NO_SLOT;
-    } else {
-      page = __ldg(B.table + (size_t)b * B.max_pages + (pos >> B.page_shift));
-      if ((unsigned)page >= (unsigned)B.num_pages) page = INVALID;
-      slot = pos & ((1 << B.page_shift) - 1);
-    }
-  }
-  if (page == INVALID && lane == 0) B.flags[0] = 1;
-  return page;
-}
 // Pieces of a lane in flight, and warps of a block.  36K tokens appended to e4m3 pools take 40.1 us with 2
 // pieces, 47.3 with 4, 40.9 with 1 (8 tokens of 256 sequences 4.8, 5.0, 5.0); 39.1 us with 4 warps a block, 40.8
 // with 8, 42.2 with 16.  More loads in flight spread the stores over more pages at once.
@@ -77,8 +36,8 @@ __global__ void __launch_bounds__(128) sa_append_kernel(Batch B, Pool P, Rows K,
   const int pieces = 2 * heads * LV;              // keys, then values
   const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (t < B.n_tokens) {
-    int slot = 0;
-    const int page = find_page(B, t, lane, slot);
+    int slot = 0, pos;
+    const int page = find_page(B, t, lane, slot, pos);
     if (page < 0) return;
     const __nv_bfloat16 *const k = K.ptr + t * K.st + piece * E, *const v = V.ptr + t * V.st + piece * E;
     const long long vec0 = (((long long)page * heads) << B.page_shift) + slot;
@@ -136,16 +95,17 @@ __global__ void __launch_bounds__(128) sa_append_kernel(Batch B, Pool P, Rows K,
 // Bound by memory: 42,403 tokens of 8 heads of 128 from e4m3 take 45.4 us,
 // 5.75 TB/s.  A lane's 16 codes leave as one 32-byte store: as two of 16 bytes,
 // which fill half a sector each, the same call took 60 us.
-template <int D, bool FP8>
+template <int D, int POOL>
 __global__ void __launch_bounds__(128) sa_read_kernel(Batch B, Pool P, __nv_bfloat16* ko, __nv_bfloat16* vo, int heads) {
-  constexpr int E = piece_of<FP8>, LV = D / E;
+  constexpr bool FP8 = POOL == POOL_E4M3;
+  constexpr int E = piece_of<POOL != POOL_BF16>, LV = D / E;
   flag_invalid_seqs(B);
   const int lane = threadIdx.x & 31, piece = lane % LV;
   const int pieces = 2 * heads * LV;              // keys, then values
   const int t = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (t < B.n_tokens) {
-    int slot = 0;
-    const int page = find_page(B, t, lane, slot);
+    int slot = 0, pos;
+    const int page = find_page(B, t, lane, slot, pos);
     if (page == NO_ROW) return;
     __nv_bfloat16 *const kt = ko + (size_t)t * heads * D, *const vt = vo + (size_t)t * heads * D;
     if (page < 0) {
@@ -163,8 +123,13 @@ __global__ void __launch_bounds__(128) sa_read_kernel(Batch B, Pool P, __nv_bflo
         const bool is_v = vi >= heads;
         const long long vec = vec0 + ((long long)(is_v ? vi - heads : vi) << B.page_shift);
         if (vi >= 2 * heads) continue;
-        x[u] = ldg_stream((const char*)(is_v ? P.v : P.k) + (vec * D + piece * E) * (FP8 ? 1 : 2));
-        if constexpr (FP8) {
+        if constexpr (POOL == POOL_E2M1) {                 // 8 bytes and their scale
+          const uint2 c = __ldg((const uint2*)((const char*)(is_v ? P.v : P.k) + vec * (D / 2)) + piece);
+          x[u] = make_uint4(c.x, c.y, __ldg((is_v ? P.vb : P.kb) + vec * (D / 16) + piece), 0);
+        } else {
+          x[u] = ldg_stream((const char*)(is_v ? P.v : P.k) + (vec * D + piece * E) * (FP8 ? 1 : 2));
+        }
+        if constexpr (POOL != POOL_BF16) {
           const int byte = __ldg((is_v ? P.vs : P.ks) + vec);
           f[u] = byte == 0 ? __int_as_float(1 << 22) : scale_of(byte);   // 2^-127 is subnormal
         }
@@ -174,14 +139,19 @@ __global__ void __launch_bounds__(128) sa_read_kernel(Batch B, Pool P, __nv_bflo
         const int vi = (c0 + 32 * u) / LV;
         if (vi >= 2 * heads) continue;
         uint4* const dst = (uint4*)((vi < heads ? kt + vi * D : vt + (vi - heads) * D) + piece * E);
-        if constexpr (!FP8) {
+        if constexpr (POOL == POOL_BF16) {
           *dst = x[u];
         } else {
           const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-          uint32_t r[8];
+          uint32_t r[8], h[8];
+          if constexpr (POOL == POOL_E2M1) {               // a code times its scale is exact in f16
+            const uint32_t s = e4m3_to_f16x2((uint16_t)(x[u].z | x[u].z << 8));
+            e2m1_to_f16(x[u].x, s, h);
+            e2m1_to_f16(x[u].y, s, h + 4);
+          }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float2 z = f16x2_to_f32(e4m3_to_f16x2((uint16_t)(w[j >> 1] >> (16 * (j & 1)))));
+            const float2 z = f16x2_to_f32(FP8 ? e4m3_to_f16x2((uint16_t)(w[j >> 1] >> (16 * (j & 1)))) : h[j]);
             r[j] = pack_bf16(z.x * f[u], z.y * f[u]);
           }
           st_32(dst, r);
@@ -224,8 +194,9 @@ static bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 static int check_pool(const spec_attn_ctx* h, const spec_attn_pool* p) {
   if (!p || !p->k || !p->v || p->num_pages < 1 || !aligned16(p->k) || !aligned16(p->v)) return SV_ERR_ARG;
-  if (p->dtype != SV_BF16 && p->dtype != SV_E4M3) return SV_ERR_DTYPE;
-  if (p->dtype == SV_E4M3 && (!p->k_scale || !p->v_scale)) return SV_ERR_ARG;
+  if (p->dtype != SV_BF16 && p->dtype != SV_E4M3 && p->dtype != SV_E2M1) return SV_ERR_DTYPE;
+  if (p->dtype != SV_BF16 && (!p->k_scale || !p->v_scale)) return SV_ERR_ARG;
+  if (p->dtype == SV_E2M1 && (!p->k_block || !p->v_block || !aligned16(p->k_block) || !aligned16(p->v_block))) return SV_ERR_ARG;
   if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) return SV_ERR_SIZE;
   if ((long long)p->num_pages * h->kv_heads * p->page_size >= (1ll << 31)) return SV_ERR_SIZE;
   return SV_OK;
@@ -255,9 +226,39 @@ static Batch batch_of(const spec_attn_ctx* h, const spec_attn_batch* b, const sp
   r.flags = h->d_flags;
   return r;
 }
-static Pool pool_of(const spec_attn_pool* p) { return Pool{p->k, p->v, p->k_scale, p->v_scale}; }
+static Pool pool_of(const spec_attn_pool* p) {
+  const bool blocks = p->dtype == SV_E2M1;
+  return Pool{p->k, p->v, p->k_scale, p->v_scale, blocks ? p->k_block : nullptr, blocks ? p->v_block : nullptr};
+}
 static Rows rows_of(const spec_attn_rows* r) { return Rows{(const __nv_bfloat16*)r->ptr, r->token_stride, r->head_stride}; }
+static RowsOut out_rows_of(const spec_attn_rows* r) { return RowsOut{(__nv_bfloat16*)r->ptr, r->token_stride, r->head_stride}; }
 static int launched() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
+
+// Vectors of a token for a warp: all of them where there are tokens enough to fill the GPU, else fewer, a step of
+// loads at least.
+constexpr int WARPS_PER_SM = 16;
+template <int D, int POOL>
+static int launch_rotate(const spec_attn_ctx* h, const Batch& B, const Pool& P, const Turn& T, const Rows& Q, const Rows& K, const Rows& V,
+                         const RowsOut& QO, const RowsOut& KO, cudaStream_t s) {
+  const int step = 256 / D * UT;
+  const int q_heads = QO.ptr ? h->q_heads : 0, all = q_heads + 2 * h->kv_heads, steps = (all + step - 1) / step;
+  const long long want = ((long long)h->n_sm * WARPS_PER_SM + B.n_tokens - 1) / B.n_tokens;
+  const int per = (steps + (int)(want < steps ? want : steps) - 1) / (int)(want < steps ? want : steps) * step, splits = (all + per - 1) / per;
+  const long long warps = (long long)B.n_tokens * splits;
+  if (warps > 0x7fffffffll) return SV_ERR_SIZE;
+  sa_rotate_kernel<D, POOL><<<(unsigned)((warps + 3) / 4), 128, 0, s>>>(B, P, T, Q, K, V, QO, KO, q_heads, h->kv_heads, splits, per);
+  return launched();
+}
+static int rotate(const spec_attn_ctx* h, int dtype, const Batch& B, const Pool& P, const Turn& T, const Rows& Q, const Rows& K, const Rows& V,
+                  const RowsOut& QO, const RowsOut& KO, cudaStream_t s) {
+  if (h->D == 128)
+    return dtype == SV_E2M1   ? launch_rotate<128, POOL_E2M1>(h, B, P, T, Q, K, V, QO, KO, s)
+           : dtype == SV_E4M3 ? launch_rotate<128, POOL_E4M3>(h, B, P, T, Q, K, V, QO, KO, s)
+                              : launch_rotate<128, POOL_BF16>(h, B, P, T, Q, K, V, QO, KO, s);
+  return dtype == SV_E2M1   ? launch_rotate<64, POOL_E2M1>(h, B, P, T, Q, K, V, QO, KO, s)
+         : dtype == SV_E4M3 ? launch_rotate<64, POOL_E4M3>(h, B, P, T, Q, K, V, QO, KO, s)
+                            : launch_rotate<64, POOL_BF16>(h, B, P, T, Q, K, V, QO, KO, s);
+}
 
 extern "C" int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch,
                                 const spec_attn_rows* k, const spec_attn_rows* v, void* cuda_stream) {
@@ -268,6 +269,10 @@ extern "C" int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const
   const cudaStream_t s = (cudaStream_t)cuda_stream;
   const Batch B = batch_of(h, batch, pool);
   const Pool P = pool_of(pool);
+  if (pool->dtype == SV_E2M1) {
+    const RowsOut none = {nullptr, 0, 0};
+    return rotate(h, pool->dtype, B, P, Turn{}, rows_of(k), rows_of(k), rows_of(v), none, none, s);
+  }
   const int grid = (B.n_tokens + 3) / 4;           // four warps a block, a token each
   if (h->D == 128) {
     if (pool->dtype == SV_E4M3) sa_append_kernel<128, true><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
@@ -277,6 +282,22 @@ extern "C" int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const
     else sa_append_kernel<64, false><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
   }
   return launched();
+}
+
+extern "C" int spec_attn_append_rotated(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch, const spec_attn_rope* rope,
+                                        const spec_attn_rows* q, const spec_attn_rows* k, const spec_attn_rows* v,
+                                        const spec_attn_rows* q_out, const spec_attn_rows* k_out, void* cuda_stream) {
+  int rc;
+  if ((rc = check_device(h)) || (rc = check_pool(h, pool)) || (rc = check_batch(h, batch))) return rc;
+  if (!rope || !rope->table || !aligned16(rope->table) || rope->max_positions < 1 || !q != !q_out) return SV_ERR_ARG;
+  if (rope->rot_dim < 16 || rope->rot_dim > h->D || rope->rot_dim % 16) return SV_ERR_SIZE;
+  if (batch->n_seqs == 0 || batch->n_tokens == 0) return SV_OK;
+  if ((rc = check_rows(k)) || (rc = check_rows(v)) || (q && ((rc = check_rows(q)) || (rc = check_rows(q_out)))) || (k_out && (rc = check_rows(k_out))))
+    return rc;
+  const Turn T = {rope->table, rope->positions, rope->max_positions, rope->rot_dim, rope->interleaved != 0};
+  const RowsOut none = {nullptr, 0, 0};
+  return rotate(h, pool->dtype, batch_of(h, batch, pool), pool_of(pool), T, q ? rows_of(q) : rows_of(k), rows_of(k), rows_of(v),
+                q ? out_rows_of(q_out) : none, k_out ? out_rows_of(k_out) : none, (cudaStream_t)cuda_stream);
 }
 
 extern "C" int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch,
@@ -291,11 +312,13 @@ extern "C" int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const s
   const int grid = (B.n_tokens + 3) / 4;           // four warps a block, a token each
   __nv_bfloat16 *ko = (__nv_bfloat16*)k_out, *vo = (__nv_bfloat16*)v_out;
   if (h->D == 128) {
-    if (pool->dtype == SV_E4M3) sa_read_kernel<128, true><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
-    else sa_read_kernel<128, false><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
+    if (pool->dtype == SV_E2M1) sa_read_kernel<128, POOL_E2M1><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
+    else if (pool->dtype == SV_E4M3) sa_read_kernel<128, POOL_E4M3><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
+    else sa_read_kernel<128, POOL_BF16><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
   } else {
-    if (pool->dtype == SV_E4M3) sa_read_kernel<64, true><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
-    else sa_read_kernel<64, false><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
+    if (pool->dtype == SV_E2M1) sa_read_kernel<64, POOL_E2M1><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
+    else if (pool->dtype == SV_E4M3) sa_read_kernel<64, POOL_E4M3><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
+    else sa_read_kernel<64, POOL_BF16><<<grid, 128, 0, s>>>(B, P, ko, vo, h->kv_heads);
   }
   return launched();
 }
@@ -321,15 +344,17 @@ static EncodeTiled encode_tiled() {
   }();
   return f;
 }
-// Pool pages as rows of D elements, one page and head a box (64 columns of it for 16-bit elements, which swizzled lines hold)
+// Pool pages as rows of D elements, one page and head a box (64 columns of it for 16-bit elements, which swizzled
+// lines hold); codes go as bytes, in lines of 128, 64 or 32 that are swizzled by their length
 static bool map_pool(CUtensorMap* m, const spec_attn_ctx* h, const spec_attn_pool* p, void* base) {
-  const bool e4m3 = p->dtype == SV_E4M3;
-  const cuuint64_t dims[2] = {(cuuint64_t)h->D, (cuuint64_t)p->num_pages * h->kv_heads * p->page_size};
-  const cuuint64_t strides[1] = {(cuuint64_t)h->D * (e4m3 ? 1 : 2)};
-  const cuuint32_t box[2] = {(cuuint32_t)(e4m3 ? h->D : 64), (cuuint32_t)p->page_size}, step[2] = {1, 1};
-  return encode_tiled()(m, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, step,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, e4m3 && h->D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const bool coded = p->dtype != SV_BF16;
+  const cuuint64_t line = p->dtype == SV_E2M1 ? h->D / 2 : h->D;                      // elements of a row
+  const cuuint64_t dims[2] = {line, (cuuint64_t)p->num_pages * h->kv_heads * p->page_size};
+  const cuuint64_t strides[1] = {line * (coded ? 1 : 2)};
+  const cuuint32_t box[2] = {(cuuint32_t)(coded ? line : 64), (cuuint32_t)p->page_size}, step[2] = {1, 1};
+  const CUtensorMapSwizzle swizzle = !coded || line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : line == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
+  return encode_tiled()(m, coded ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, step,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // Packed rows [token, head, D]; a box of `tokens` tokens of `box_heads` heads and 64 columns
 static bool map_rows(CUtensorMap* m, int D, int heads, const Rows& r, int n_tokens, int box_heads, int tokens) {
@@ -349,7 +374,7 @@ static bool allow_smem() {
 }
 template <int D>
 static bool allow_smem_all() {
-  return allow_smem<D, KIND_BF16, 1>() && allow_smem<D, KIND_BF16, 2>() && allow_smem<D, KIND_E4M3, 1>() && allow_smem<D, KIND_PACKED, 1>() && allow_smem<D, KIND_PACKED, 2>();
+  return allow_smem<D, KIND_BF16, 1>() && allow_smem<D, KIND_BF16, 2>() && allow_smem<D, KIND_E4M3, 1>() && allow_smem<D, KIND_E2M1, 1>() && allow_smem<D, KIND_PACKED, 1>() && allow_smem<D, KIND_PACKED, 2>();
 }
 template <int D, int KIND, int MT>
 static int launch_attention(const spec_attn_ctx* h, const AttnParams& A, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t s) {
@@ -359,7 +384,7 @@ static int launch_attention(const spec_attn_ctx* h, const AttnParams& A, const C
 static AttnParams attn_params(const spec_attn_ctx* h, const Batch& B, const Rows& Q, int causal, float scale, void* out, float* lse) {
   AttnParams A;
   A.B = B; A.Q = Q;
-  A.ks = A.vs = nullptr;
+  A.ks = A.vs = A.kb = A.vb = nullptr;
   A.q_heads = h->q_heads; A.kv_heads = h->kv_heads; A.group = h->q_heads / h->kv_heads;
   A.tile_tokens = BM / A.group;
   A.causal = causal != 0;
@@ -431,8 +456,12 @@ extern "C" int spec_attn_chunk(spec_attn_t h, const spec_attn_pool* pool, const 
   CUtensorMap mq, mk, mv;
   if (!map_queries(&mq, h, A)) return SV_ERR_ARG;
   if (!map_pool(&mk, h, pool, pool->k) || !map_pool(&mv, h, pool, pool->v)) return SV_ERR_CUDA;
-  if (pool->dtype == SV_E4M3) {
+  if (pool->dtype != SV_BF16) {
     A.ks = pool->k_scale; A.vs = pool->v_scale;
+    if (pool->dtype == SV_E2M1) {
+      A.kb = pool->k_block; A.vb = pool->v_block;
+      return h->D == 128 ? launch_attention<128, KIND_E2M1, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E2M1, 1>(h, A, mq, mk, mv, s);
+    }
     return h->D == 128 ? launch_attention<128, KIND_E4M3, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E4M3, 1>(h, A, mq, mk, mv, s);
   }
   // The table's width is a poor bound where it has room for the longest sequence of all: a chunk of 113 tokens over
