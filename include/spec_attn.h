@@ -32,7 +32,7 @@
  * their negatives; bit 3 is the sign), k and v [num_pages, kv_heads, page_size,
  * head_dim / 2] bytes with element 2i in the low half of byte i; k_block and
  * v_block [num_pages, kv_heads, page_size, head_dim / 16], an e4m3 scale for
- * every 16 elements; and k_scale and v_scale as above.  A value is code * scale *
+ * every 16 elements; and k_scale and v_scale as above, all 16-byte aligned.  A value is code * scale *
  * 2^(byte - 127).  The exponent e is the least one >= -120 with max|x| <= 2688 *
  * 2^e; a block's scale is max|x_j| / 2^e / 6 rounded to e4m3; a code is
  * x / 2^e / scale rounded to the nearest, ties to the even code, in 32 bits.  So

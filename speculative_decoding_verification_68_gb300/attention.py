@@ -131,6 +131,8 @@ class KVPool:
         for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
             if self.quantised:
                 _check(t, name, torch.uint8, tuple(k.shape[:3]), k.device)
+                if four and t.data_ptr() % 16:
+                    raise ValueError(f"{name} must be 16-byte aligned")
             elif t is not None:
                 raise ValueError(f"{name}: a bf16 pool has no scales")
         for t, name in ((k_block, "k_block"), (v_block, "v_block")):

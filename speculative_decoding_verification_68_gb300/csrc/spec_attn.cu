@@ -196,7 +196,8 @@ static int check_pool(const spec_attn_ctx* h, const spec_attn_pool* p) {
   if (!p || !p->k || !p->v || p->num_pages < 1 || !aligned16(p->k) || !aligned16(p->v)) return SV_ERR_ARG;
   if (p->dtype != SV_BF16 && p->dtype != SV_E4M3 && p->dtype != SV_E2M1) return SV_ERR_DTYPE;
   if (p->dtype != SV_BF16 && (!p->k_scale || !p->v_scale)) return SV_ERR_ARG;
-  if (p->dtype == SV_E2M1 && (!p->k_block || !p->v_block || !aligned16(p->k_block) || !aligned16(p->v_block))) return SV_ERR_ARG;
+  if (p->dtype == SV_E2M1 && (!p->k_block || !p->v_block || !aligned16(p->k_block) ||
+                              !aligned16(p->v_block) || !aligned16(p->k_scale) || !aligned16(p->v_scale))) return SV_ERR_ARG;
   if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128) return SV_ERR_SIZE;
   if ((long long)p->num_pages * h->kv_heads * p->page_size >= (1ll << 31)) return SV_ERR_SIZE;
   return SV_OK;
