@@ -9,9 +9,9 @@ import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SOURCES = [os.path.join(PKG, "csrc", name) for name in ("spec_verify.cu", "spec_attn.cu")]
+SOURCES = [os.path.join(PKG, "csrc", name) for name in ("spec_verify.cu", "spec_attn.cu", "spec_attn_few.cu")]
 HEADERS = [os.path.join(ROOT, "include", name) for name in ("spec_verify.h", "spec_attn.h")] + [
-    os.path.join(PKG, "csrc", name) for name in ("attn_common.cuh", "attn_plan.cuh", "attn_rotate.cuh", "attn_tile.cuh")]
+    os.path.join(PKG, "csrc", name) for name in ("attn_common.cuh", "attn_few.cuh", "attn_plan.cuh", "attn_rotate.cuh", "attn_tile.cuh")]
 LIB = os.path.join(PKG, "libspec_verify.so")
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC"]

@@ -6,16 +6,8 @@
 
 #include "attn_plan.cuh"
 
-namespace {
-
-constexpr unsigned FULL = 0xffffffffu;
-constexpr float LOG2E_F = 1.44269504088896341f;
-constexpr float LN2_F = 0.69314718055994531f;
-constexpr int EXP_MIN = -120;      // least exponent of a cached vector's scale
-constexpr int EXP_BIAS = 127;
-constexpr int BYTE_NAN = 255;      // scale byte of a vector that holds an infinity or NaN
-
 // ---------------------------------------------------------------- parameters
+namespace sv_attn {   // the same types in every translation unit
 struct Batch {                     // spec_attn_batch, plus what follows from the handle
   const int32_t* cu;
   const int32_t* kv_len;           // null: packed prompts (a sequence holds its new tokens only)
@@ -37,6 +29,19 @@ struct Rows {
   const __nv_bfloat16* ptr;
   long long st, sh;                // token and head strides, elements
 };
+
+}  // namespace sv_attn
+
+namespace {
+
+using namespace sv_attn;
+
+constexpr unsigned FULL = 0xffffffffu;
+constexpr float LOG2E_F = 1.44269504088896341f;
+constexpr float LN2_F = 0.69314718055994531f;
+constexpr int EXP_MIN = -120;      // least exponent of a cached vector's scale
+constexpr int EXP_BIAS = 127;
+constexpr int BYTE_NAN = 255;      // scale byte of a vector that holds an infinity or NaN
 
 // ------------------------------------------------------------------- helpers
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }

@@ -51,6 +51,26 @@
 #include "attn_common.cuh"
 #include "attn_plan.cuh"
 
+namespace sv_attn {
+
+struct AttnParams {
+  Batch B;
+  Rows Q;
+  const uint8_t *ks, *vs;           // scale bytes (coded caches)
+  const uint8_t *kb, *vb;           // block scales (e2m1)
+  int q_heads, kv_heads, group;
+  int tile_tokens;                  // floor(128 / group)
+  int causal;
+  float c;                          // scale * log2(e)
+  __nv_bfloat16* out;
+  float* lse;
+  float* ws;                        // partials: [cta][2][MT] of PART floats
+  int* counters;                    // [cta][MT], zero between calls
+  int* odd;                         // [cta][4][3][D] first keys with values that are not finite (see note_odd), else ODD_NONE
+};
+
+}  // namespace sv_attn
+
 namespace {
 
 enum { KIND_BF16 = 0, KIND_E4M3 = 1, KIND_PACKED = 2, KIND_E2M1 = 3 };
@@ -70,22 +90,6 @@ constexpr int EV_MIN = -97, EV_MAX = 126;
 constexpr int BYTE_ZERO = 15;       // vectors of this scale (below 2^-103) and less count as zero beside others
 constexpr int SPREAD = 14;          // exponents apart that a block's vectors may be to share one scale
 constexpr float WIDE = 1.2676506e30f;   // 2^100, in place of the exponent of a block's values: vectors have their own
-
-struct AttnParams {
-  Batch B;
-  Rows Q;
-  const uint8_t *ks, *vs;           // scale bytes (coded caches)
-  const uint8_t *kb, *vb;           // block scales (e2m1)
-  int q_heads, kv_heads, group;
-  int tile_tokens;                  // floor(128 / group)
-  int causal;
-  float c;                          // scale * log2(e)
-  __nv_bfloat16* out;
-  float* lse;
-  float* ws;                        // partials: [cta][2][MT] of PART floats
-  int* counters;                    // [cta][MT], zero between calls
-  int* odd;                         // [cta][4][3][D] first keys with values that are not finite (see note_odd), else ODD_NONE
-};
 
 // Floats of one partial: M, l and its correction per row, then O as [D / 4][128] float4
 template <int D> __host__ __device__ constexpr int part_floats() { return 3 * BM + BM * D; }
@@ -282,6 +286,109 @@ struct Walker {
   }
 };
 
+// This CTA's run of units (all NT threads; red64 holds 22 sums and places, found 10 places from 1 on).
+// Also reports sequences that are not valid.
+template <int NT>
+__device__ __forceinline__ Walker plan_run(const AttnParams& A, int tile_rows, long long* red64, int* work, long long& units, long long& ctas) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int* const flags = A.B.flags;
+  long long mine = 0;
+  for (int b = tid; b < A.B.n_seqs; b += NT) {
+    const Seq s = load_seq(A.B, b, tile_rows);
+    if (s.bad && blockIdx.x == 0) flags[0] = 1;
+    mine += tiles_before(s, s.tiles, tile_rows, A.causal) * A.kv_heads;
+  }
+  long long sum = mine;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
+  if (lane == 0) red64[warp] = sum;
+  __syncthreads();
+  units = 0;
+  for (int w = 0; w < (NT / 32); ++w) units += red64[w];
+  ctas = min((long long)gridDim.x, max(1ll, units / MIN_RUN));
+  Walker W;
+  W.at = W.u1 = 0;                                        // an empty run
+  W.b = W.head = W.t = 0;
+  if (blockIdx.x < ctas && units > 0) {
+    // the items that hold the run's two cuts; the last cut of all is the end
+    const long long cut[2] = {cut_at(units, ctas, blockIdx.x), cut_at(units, ctas, blockIdx.x + 1)};
+    long long before = 0;
+    for (int b0 = 0; b0 < A.B.n_seqs && before <= cut[1]; b0 += NT) {   // their sequences
+      const int b = b0 + tid;
+      if (A.B.n_seqs > NT) {
+        mine = 0;
+        if (b < A.B.n_seqs) {
+          const Seq s = load_seq(A.B, b, tile_rows);
+          mine = tiles_before(s, s.tiles, tile_rows, A.causal) * A.kv_heads;
+        }
+      }
+      long long scan = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(FULL, scan, o);
+        if (lane >= o) scan += x;
+      }
+      __syncthreads();
+      if (lane == 31) red64[warp] = scan;
+      __syncthreads();
+      long long chunk = 0, below = before;
+      for (int w = 0; w < (NT / 32); ++w) {
+        const long long x = red64[w];
+        if (w < warp) below += x;
+        chunk += x;
+      }
+      const long long end = below + scan, begin = end - mine;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (begin <= cut[e] && cut[e] < end) {
+          const Spot at = locate(cut[e] - begin, mine / A.kv_heads);
+          int* const found = work + 1 + 5 * e;            // sequence, head, tile, unit within the item
+          found[0] = b;
+          found[1] = at.head;
+          red64[20 + e] = at.unit;
+        }
+      before += chunk;                                    // uniform
+    }
+    __syncthreads();
+    // their tiles: half of the threads look for each
+    const int mine_e = tid >= NT / 2;
+    if (cut[mine_e] < units) {
+      int* const found = work + 1 + 5 * mine_e;
+      const Seq s = load_seq(A.B, found[0], tile_rows);
+      const long long r = red64[20 + mine_e];
+      for (int t = tid - mine_e * (NT / 2); t < s.tiles; t += NT / 2) {
+        const long long lo = tiles_before(s, t, tile_rows, A.causal);
+        if (lo <= r && r < lo + SETUP + tile_blocks(s, t, tile_rows, A.causal)) {
+          found[2] = t;
+          found[3] = (int)(r - lo);
+        }
+      }
+    }
+    __syncthreads();
+    long long to[2], from = 0;
+#pragma unroll
+    for (int e = 1; e >= 0; --e) {
+      const int* const found = work + 1 + 5 * e;
+      to[e] = cut[e];
+      if (cut[e] == units) continue;
+      W.b = found[0]; W.head = found[1]; W.t = found[2];
+      W.s = load_seq(A.B, W.b, tile_rows);
+      const int in = found[3], size = SETUP + tile_blocks(W.s, W.t, tile_rows, A.causal);
+      from = cut[e] - in;
+      to[e] = moved_cut(cut[e], in, size);
+    }
+    W.u0 = to[0];
+    W.u1 = to[1];
+    W.at = from;
+    if (W.u0 < W.u1 && W.u0 > from && to[0] != cut[0]) {  // moved to the end of that item
+      W.at = W.u0;
+      W.advance(A, tile_rows);
+    }
+    if (W.u0 >= W.u1) W.at = W.u1;
+  }
+  return W;
+}
+
 // --------------------------------------------- values that are not finite
 // Causal rows see a prefix of the keys, so what such values do to a row follows
 // from three keys per column: the first with NaN, +inf and -inf.  Only blocks
@@ -424,101 +531,8 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(work)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  long long* const red64 = (long long*)red;
-  long long mine = 0;
-  for (int b = tid; b < A.B.n_seqs; b += NT) {
-    const Seq s = load_seq(A.B, b, tile_rows);
-    if (s.bad && blockIdx.x == 0) flags[0] = 1;
-    mine += tiles_before(s, s.tiles, tile_rows, A.causal) * A.kv_heads;
-  }
-  long long sum = mine;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(FULL, sum, o);
-  if (lane == 0) red64[warp] = sum;
-  __syncthreads();
-  long long units = 0;
-  for (int w = 0; w < C::WARPS; ++w) units += red64[w];
-  const long long ctas = min((long long)gridDim.x, max(1ll, units / MIN_RUN));
-  Walker W;
-  W.at = W.u1 = 0;                                        // an empty run
-  W.b = W.head = W.t = 0;
-  if (blockIdx.x < ctas && units > 0) {
-    // the items that hold the run's two cuts; the last cut of all is the end
-    const long long cut[2] = {cut_at(units, ctas, blockIdx.x), cut_at(units, ctas, blockIdx.x + 1)};
-    long long before = 0;
-    for (int b0 = 0; b0 < A.B.n_seqs && before <= cut[1]; b0 += NT) {   // their sequences
-      const int b = b0 + tid;
-      if (A.B.n_seqs > NT) {
-        mine = 0;
-        if (b < A.B.n_seqs) {
-          const Seq s = load_seq(A.B, b, tile_rows);
-          mine = tiles_before(s, s.tiles, tile_rows, A.causal) * A.kv_heads;
-        }
-      }
-      long long scan = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(FULL, scan, o);
-        if (lane >= o) scan += x;
-      }
-      __syncthreads();
-      if (lane == 31) red64[warp] = scan;
-      __syncthreads();
-      long long chunk = 0, below = before;
-      for (int w = 0; w < C::WARPS; ++w) {
-        const long long x = red64[w];
-        if (w < warp) below += x;
-        chunk += x;
-      }
-      const long long end = below + scan, begin = end - mine;
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-        if (begin <= cut[e] && cut[e] < end) {
-          const Spot at = locate(cut[e] - begin, mine / A.kv_heads);
-          int* const found = work + 1 + 5 * e;            // sequence, head, tile, unit within the item
-          found[0] = b;
-          found[1] = at.head;
-          red64[20 + e] = at.unit;
-        }
-      before += chunk;                                    // uniform
-    }
-    __syncthreads();
-    // their tiles: half of the threads look for each
-    const int mine_e = tid >= NT / 2;
-    if (cut[mine_e] < units) {
-      int* const found = work + 1 + 5 * mine_e;
-      const Seq s = load_seq(A.B, found[0], tile_rows);
-      const long long r = red64[20 + mine_e];
-      for (int t = tid - mine_e * (NT / 2); t < s.tiles; t += NT / 2) {
-        const long long lo = tiles_before(s, t, tile_rows, A.causal);
-        if (lo <= r && r < lo + SETUP + tile_blocks(s, t, tile_rows, A.causal)) {
-          found[2] = t;
-          found[3] = (int)(r - lo);
-        }
-      }
-    }
-    __syncthreads();
-    long long to[2], from = 0;
-#pragma unroll
-    for (int e = 1; e >= 0; --e) {
-      const int* const found = work + 1 + 5 * e;
-      to[e] = cut[e];
-      if (cut[e] == units) continue;
-      W.b = found[0]; W.head = found[1]; W.t = found[2];
-      W.s = load_seq(A.B, W.b, tile_rows);
-      const int in = found[3], size = SETUP + tile_blocks(W.s, W.t, tile_rows, A.causal);
-      from = cut[e] - in;
-      to[e] = moved_cut(cut[e], in, size);
-    }
-    W.u0 = to[0];
-    W.u1 = to[1];
-    W.at = from;
-    if (W.u0 < W.u1 && W.u0 > from && to[0] != cut[0]) {  // moved to the end of that item
-      W.at = W.u0;
-      W.advance(A, tile_rows);
-    }
-    if (W.u0 >= W.u1) W.at = W.u1;
-  }
+  long long units, ctas;
+  Walker W = plan_run<NT>(A, tile_rows, (long long*)red, work, units, ctas);
   tc_before();
   __syncthreads();
   tc_after();

@@ -13,6 +13,11 @@
 #include "attn_tile.cuh"
 #include "spec_attn.h"
 
+namespace sv_attn {   // spec_attn_few.cu
+bool few_init(int D);
+int few_launch(const AttnParams& A, const Pool& P, int D, int rows, int n_sm, cudaStream_t s);
+}  // namespace sv_attn
+
 namespace {
 
 // Pieces of a lane in flight, and warps of a block.  36K tokens appended to e4m3 pools take 40.1 us with 2
@@ -408,6 +413,13 @@ static bool two_tiles(const spec_attn_ctx* h, const AttnParams& A, long long key
   return rows > BM && units >= (long long)TWO_TILE_UNITS * h->n_sm;
 }
 
+// Rows of a tile of the kernel for few rows, 0: not for this call.  The mean number of rows of a sequence and head
+// decides, and a tile holds a group at least.
+static int few_rows(const AttnParams& A) {
+  const long long rows = ((long long)A.B.n_tokens * A.group + A.B.n_seqs - 1) / A.B.n_seqs;
+  return A.group > 16 || rows > 16 ? 0 : rows <= 8 && A.group <= 8 ? 8 : 16;
+}
+
 extern "C" int spec_attn_init(spec_attn_t* out, int q_heads, int kv_heads, int head_dim, int max_seqs) {
   if (!out) return SV_ERR_ARG;
   *out = nullptr;
@@ -422,7 +434,7 @@ extern "C" int spec_attn_init(spec_attn_t* out, int q_heads, int kv_heads, int h
     free_ctx(h);
     return SV_ERR_CUDA;
   }
-  if (!encode_tiled() || !(head_dim == 128 ? allow_smem_all<128>() : allow_smem_all<64>())) {
+  if (!encode_tiled() || !few_init(head_dim) || !(head_dim == 128 ? allow_smem_all<128>() : allow_smem_all<64>())) {
     cudaGetLastError();
     free_ctx(h);
     return SV_ERR_CUDA;
@@ -461,6 +473,8 @@ extern "C" int spec_attn_chunk(spec_attn_t h, const spec_attn_pool* pool, const 
     A.ks = pool->k_scale; A.vs = pool->v_scale;
     if (pool->dtype == SV_E2M1) {
       A.kb = pool->k_block; A.vb = pool->v_block;
+      const int few = few_rows(A);
+      if (few) return few_launch(A, pool_of(pool), h->D, few, h->n_sm, s);
       return h->D == 128 ? launch_attention<128, KIND_E2M1, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E2M1, 1>(h, A, mq, mk, mv, s);
     }
     return h->D == 128 ? launch_attention<128, KIND_E4M3, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E4M3, 1>(h, A, mq, mk, mv, s);
