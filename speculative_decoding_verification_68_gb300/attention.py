@@ -309,33 +309,49 @@ class SpecAttention:
             raise ValueError(f"rope is on {rope.device}, expected {self.device}")
         if rope.rot_dim > self.head_dim:
             raise ValueError(f"rope turns {rope.rot_dim} elements of {self.head_dim}")
-        if positions is not None:
+        if positions is None:
+            rope._c.positions = None
+        else:
             _check(positions, "positions", torch.int32, (n,), self.device)
-        rope._c.positions = None if positions is None else positions.data_ptr()
+            rope._c.positions = positions.data_ptr()
+        q_ref = q_out = k_out = None
         if q is not None:
             self._rows(self._q_c, q, "q", self.q_heads, n)
+            q_ref = self._q_ref
         if out is None:
             out = {}
             if q is not None:
-                out["q"] = torch.empty((n, self.q_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
+                out["q"] = self._new_rows(self._q_out_c, n, self.q_heads)
+                q_out = self._q_out_ref
             if want_k:
-                out["k"] = torch.empty((n, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
-        elif (q is None) != (out.get("q") is None):
-            raise ValueError("q and output q go together")
-        elif want_k and out.get("k") is None:
-            raise ValueError("output k is required")
-        q_out, k_out = out.get("q"), out.get("k")
-        for name, t, src, c, heads in (("q", q_out, q, self._q_out_c, self.q_heads), ("k", k_out, k, self._k_out_c, self.kv_heads)):
-            if t is not None:
-                self._rows(c, t, f"output {name}", heads, n)
-                if n > 1 and abs(c.token_stride) < self.head_dim or heads > 1 and abs(c.head_stride) < self.head_dim:
-                    raise ValueError(f"output {name}: strides {tuple(t.stride())} let its rows overlap")
-        rc = self._lib.spec_attn_append_rotated(
-            self._h, pool._ref, batch, rope._ref, None if q is None else self._q_ref, self._k_ref, self._v_ref,
-            None if q_out is None else self._q_out_ref, None if k_out is None else self._k_out_ref, self._stream(stream))
+                out["k"] = self._new_rows(self._k_out_c, n, self.kv_heads)
+                k_out = self._k_out_ref
+        else:
+            if (q is None) != (out.get("q") is None):
+                raise ValueError("q and output q go together")
+            if q is not None:
+                q_out = self._out_rows(self._q_out_c, self._q_out_ref, out["q"], "output q", self.q_heads, n)
+            if out.get("k") is not None:
+                k_out = self._out_rows(self._k_out_c, self._k_out_ref, out["k"], "output k", self.kv_heads, n)
+            elif want_k:
+                raise ValueError("output k is required")
+        rc = self._lib.spec_attn_append_rotated(self._h, pool._ref, batch, rope._ref, q_ref, self._k_ref, self._v_ref, q_out, k_out,
+                                                self._stream(stream))
         if rc:
             self._status(rc, "spec_attn_append_rotated")
         return out
+
+    def _new_rows(self, c, n, heads):
+        d = self.head_dim
+        t = torch.empty((n, heads, d), dtype=torch.bfloat16, device=self.device)
+        c.ptr, c.token_stride, c.head_stride = t.data_ptr(), heads * d, d
+        return t
+
+    def _out_rows(self, c, ref, t, name, heads, n):
+        self._rows(c, t, name, heads, n)
+        if n > 1 and abs(c.token_stride) < self.head_dim or heads > 1 and abs(c.head_stride) < self.head_dim:
+            raise ValueError(f"{name}: strides {tuple(t.stride())} let its rows overlap")
+        return ref
 
     def read(self, pool: KVPool, cu, kv_len, page_table, n_tokens: int, out: dict | None = None, stream=None) -> dict:
         """spec_attn_read: positions kv_len[b] - n_b .. kv_len[b] - 1 of every sequence

@@ -61,7 +61,7 @@ struct Few {
   static constexpr int QBYTES = R * D * 2;
   static constexpr int CJ = D / 32;                        // words of codes of a key that a thread takes
   static constexpr int MT = D / 16;                        // 16-column tiles of the output
-  static constexpr int CM = MT < 32768 / (CONSUMERS * NTILES * 512) ? MT : 32768 / (CONSUMERS * NTILES * 512);   // of them merged at a time
+  static constexpr int CM = NTILES == 1 ? 4 : 2;           // of them merged at a time
   static_assert(MT % CM == 0 && CM > 0, "merge passes");
   static constexpr int MERGE = CONSUMERS * CM * NTILES * 512;
   static constexpr int SMALL = 2048;                       // barriers and bookkeeping
@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
       const int sc_at = (sl < 2 * SC ? C::KB_AT : C::VB_AT) + sl % (2 * SC) * 16;
       const uint8_t* const ex_src = lane & 2 ? A.vs : A.ks;
       const int ex_at = (lane & 2 ? C::VS_AT : C::KS_AT) + (lane & 1) * 16;
+      const uint8_t *const kc_lane = kc + lane * 16, *const vc_lane = vc + lane * 16;
       unsigned done = 0;                                   // slices of the lane's consuming warp in earlier runs
       bool ok = true;
       Segment g;
@@ -174,20 +175,21 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
             nxt = pages(chunk + 1);
           }
           const int page0 = __shfl_sync(FULL, cur, e & 31), page1 = __shfl_sync(FULL, cur, (e + 1) & 31);
-          const long long v0 = (((long long)page0 * A.kv_heads + g.head) << shift) + (pos & (ps - 1));
-          const long long v1 = ps == 16 ? ((long long)page1 * A.kv_heads + g.head) << shift : v0 + 16;
+          // vectors of a pool are counted in 31 bits
+          const unsigned v0 = ((unsigned)(page0 * A.kv_heads + g.head) << shift) + (pos & (ps - 1));
+          const unsigned v1 = ps == 16 ? (unsigned)(page1 * A.kv_heads + g.head) << shift : v0 + 16;
           if (!(ok = bar_wait(empty + 8 * s, ((n / C::DEPTH) & 1) ^ 1, flags))) break;
-          const uint32_t dst = base + C::RING_AT + s * C::STAGE;
+          const uint32_t dst = base + C::RING_AT + s * C::STAGE, to = dst + lane * 16;
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int h = 0; h < 2; ++h) {
+            const uint8_t *const k = kc_lane + (size_t)(h ? v1 : v0) * C::LINE, *const v = vc_lane + (size_t)(h ? v1 : v0) * C::LINE;
 #pragma unroll
             for (int x = 0; x < C::LINE / 32; ++x) {
-              const long long from = (h ? v1 : v0) * C::LINE + x * 512 + lane * 16;
-              const int to = (h * (C::LINE / 32) + x) * 512 + lane * 16;
-              async16(dst + C::K_AT + to, kc + from);
-              async16(dst + C::V_AT + to, vc + from);
+              async16(to + C::K_AT + (h * (C::LINE / 32) + x) * 512, k + x * 512);
+              async16(to + C::V_AT + (h * (C::LINE / 32) + x) * 512, v + x * 512);
             }
-          if (lane < 4 * SC) async16(dst + sc_at, sc_src + (sl_half ? v1 : v0) * SC);
+          }
+          if (lane < 4 * SC) async16(dst + sc_at, sc_src + (size_t)(sl_half ? v1 : v0) * SC);
           if (lane < 4) async16(dst + ex_at, ex_src + (lane & 1 ? v1 : v0));
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full + 8 * s) : "memory");
           w += 3;
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
         ok = bar_wait(q_full + 8 * buf, (segs >> 1) & 1, flags);
         if (group_or(BAR_ALL, CT, !ok)) break;             // all of them leave, or none
         const Segment& g = runs[segs & 3];
-        const int count = slices(g), kv = g.kv;
+        const int count = slices(g), kv = g.kv, pos0 = g.j0 * BN, lim0 = g.lim0;
         const int all_see = A.causal ? min(g.lim0, kv) : kv;       // keys that every row sees
         bool small_q = true;                               // factors of scores stay far from the ends of their range
         float cq[NTILES][2], M[NTILES][2], N[NTILES][2], l[NTILES][2], o[MT][NTILES][4];
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
           if (ok) ok = bar_wait(full + 8 * s, (n / C::DEPTH) & 1, flags);
           if (!ok) break;
           uint8_t* const st = mem + C::RING_AT + s * C::STAGE;
-          const int pos = g.j0 * BN + i * C::SLICE;
+          const int pos = pos0 + i * C::SLICE;
           const bool edge = pos + C::SLICE > all_see;
           // ---- what is rare is put right in the slice itself, a lane a key: slots past the end, which may hold
           // anything, become 0; keys of NaN get scales of NaN; and where some rows do not see all keys, values of
@@ -361,17 +363,21 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
           bool raise = false;
 #pragma unroll
           for (int nt = 0; nt < NTILES; ++nt) {
+            if (plain) {
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
+              for (int m = 0; m < 2; ++m)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const float f = cq[nt][c & 1] * kx[m][c >> 1];
-                S[m][nt][c] *= plain ? f : positive(f);
-              }
+                for (int c = 0; c < 4; ++c) S[m][nt][c] *= cq[nt][c & 1] * kx[m][c >> 1];
+            } else {
+#pragma unroll
+              for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) S[m][nt][c] *= positive(cq[nt][c & 1] * kx[m][c >> 1]);
+            }
             if (edge) {
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
-                const int row = nt * 8 + 2 * t4 + c, lim = (A.causal ? min(kv, g.lim0 + row / A.group) : kv) - pos - gq;
+                const int row = nt * 8 + 2 * t4 + c, lim = (A.causal ? min(kv, lim0 + row / A.group) : kv) - pos - gq;
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll

@@ -78,7 +78,7 @@ struct Turn {
   const float* table;              // [max_positions, rot]: cosines, then sines
   const int32_t* positions;        // of the tokens; null: their places in the cache
   int max_positions;
-  int rot;                         // 0: no rotation
+  int rot;
   int interleaved;
 };
 struct RowsOut {
@@ -97,21 +97,63 @@ __device__ __forceinline__ uint4 ld_once(const void* p) {   // not through the r
   return v;
 }
 
-constexpr int UT = 4;              // 16-byte pieces of a lane in flight
+constexpr int UT = 2;              // 16-byte pieces that a lane loads at a time, while it works on as many before
+
+// 1 / s of a scale of 4 significant bits, correctly rounded (the tests take every scale)
+__device__ __forceinline__ float reciprocal(float s) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  return s > 0.0f ? __fmaf_rn(__fmaf_rn(-r, s, 1.0f), r, r) : 0.0f;
+}
+// x / s correctly rounded, r = fl(1 / s) (see above); two at once
+__device__ __forceinline__ u64 quotient(u64 x, u64 s_neg, u64 r) {
+  const u64 q = mul2f(x, r);
+  return fma2(fma2(q, s_neg, x), r, q);
+}
+
+struct Four {
+  uint8_t byte, scale;             // of the vector, of the block
+};
+// Quantises n elements y of a block of an e2m1 vector: to y / 2^e / scale.  top and block are the bits of the largest
+// magnitude of the vector and of the block.
+__device__ __forceinline__ Four four_scale(uint32_t top, uint32_t block, float* y, const int n) {
+  const bool bad = top >= 0x7f800000u;            // an infinity or NaN
+  int e = least_exponent(top, 11, 0x280000u);
+  Four f;
+  f.byte = (uint8_t)(bad ? BYTE_NAN : e + EXP_BIAS);
+  float most = __uint_as_float(block);
+  if (e < -64) {                                  // tiny vectors: away from the end of the exponents' range, exactly
+    e += 64;
+    most *= 18446744073709551616.0f;
+#pragma unroll
+    for (int i = 0; i < n; ++i) y[i] *= 18446744073709551616.0f;
+  }
+  // everything in units of 2^e: powers of two round nothing
+  const float unit = __uint_as_float((uint32_t)(EXP_BIAS + e) << 23), inv = __uint_as_float((uint32_t)(EXP_BIAS - e) << 23);
+  float sixth, ignored;
+  upk(quotient(pk(most * inv, 0.0f), pk(-6.0f, -6.0f), pk(1.0f / 6.0f, 0.0f)), sixth, ignored);
+  f.scale = bad ? 0x7f : (uint8_t)pack_e4m3(sixth, 0.0f, 0.0f, 0.0f);
+  const float s = f16x2_to_f32(e4m3_to_f16x2(f.scale)).x, r = reciprocal(s) * inv, sn = -s * unit;
+  const u64 r2 = pk(r, r), s2 = pk(sn, sn);
+#pragma unroll
+  for (int i = 0; i < n; i += 2) upk(quotient(pk(y[i], y[i + 1]), s2, r2), y[i], y[i + 1]);
+  return f;
+}
 
 template <int D, int POOL>
-__global__ void __launch_bounds__(128) sa_rotate_kernel(Batch B, Pool P, Turn T, Rows Q, Rows K, Rows V, RowsOut QO, RowsOut KO, int q_heads,
+__global__ void __launch_bounds__(128, POOL == POOL_E2M1 ? 8 : 7) sa_rotate_kernel(Batch B, Pool P, Turn T, Rows Q, Rows K, Rows V, RowsOut QO, RowsOut KO, int q_heads,
                                                         int heads, int splits, int per) {
+  constexpr int U = UT;
   constexpr int LV = D / 8, VS = 32 / LV;         // lanes of a vector, vectors a step
   flag_invalid_seqs(B);
   const int lane = threadIdx.x & 31, piece = lane % LV, sub = lane / LV;
   const int unit = blockIdx.x * 4 + (threadIdx.x >> 5);
   const int t = unit / splits, v0 = (unit - t * splits) * per, v1 = min(v0 + per, q_heads + 2 * heads);
   if (t >= B.n_tokens) return;
-  uint4 x[UT];
-  auto load = [&](int v) {
+  uint4 x[U];
+  auto load = [&](int v, uint4* x) {
 #pragma unroll
-    for (int u = 0; u < UT; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int vi = v + u * VS + sub;
       const __nv_bfloat16* src = Q.ptr + t * Q.st + vi * Q.sh;
       if (vi >= q_heads) src = K.ptr + t * K.st + (vi - q_heads) * K.sh;
@@ -119,15 +161,13 @@ __global__ void __launch_bounds__(128) sa_rotate_kernel(Batch B, Pool P, Turn T,
       x[u] = vi < v1 ? ld_once(src + piece * 8) : make_uint4(0, 0, 0, 0);
     }
   };
-  load(v0);
+  load(v0, x);
   int slot = 0, pos = 0, page = find_page(B, t, lane, slot, pos);
   if (page == NO_ROW) return;
-  if (T.rot > 0) {
-    if (T.positions) pos = __ldg(T.positions + t);
-    if (page >= 0 && (unsigned)pos >= (unsigned)T.max_positions) {
-      page = INVALID;
-      if (lane == 0) B.flags[0] = 1;
-    }
+  if (T.positions) pos = __ldg(T.positions + t);
+  if (page >= 0 && (unsigned)pos >= (unsigned)T.max_positions) {
+    page = INVALID;
+    if (lane == 0) B.flags[0] = 1;
   }
   if (page < 0) {                                 // nothing for the cache; its rows are 0 or NaN
     const uint32_t f = page == INVALID ? 0x7fc07fc0u : 0;
@@ -165,8 +205,10 @@ __global__ void __launch_bounds__(128) sa_rotate_kernel(Batch B, Pool P, Turn T,
   }
   const long long vec0 = (((long long)page * heads) << B.page_shift) + slot;
   for (int v = v0;;) {
+    uint4 next[U];
+    if (v + VS * U < v1) load(v + VS * U, next);
 #pragma unroll
-    for (int u = 0; u < UT; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int vi = v + u * VS + sub, kh = vi - q_heads;
       if (v + u * VS >= v1) break;                // uniform
       const bool in = vi < v1, is_v = kh >= heads, turned = turns && !is_v;
@@ -178,7 +220,7 @@ __global__ void __launch_bounds__(128) sa_rotate_kernel(Batch B, Pool P, Turn T,
         y[2 * i + 1] = bf_hi(w[i]);
         o[i] = w[i];
       }
-      if (T.rot > 0 && v + u * VS < q_heads + heads) {        // uniform: some vector of the step is a query or a key
+      if (v + u * VS < q_heads + heads) {        // uniform: some vector of the step is a query or a key
         if (!T.interleaved)
 #pragma unroll
           for (int i = 0; i < 4; ++i) o[i] = __shfl_sync(FULL, w[i], from);
@@ -201,42 +243,45 @@ __global__ void __launch_bounds__(128) sa_rotate_kernel(Batch B, Pool P, Turn T,
       if constexpr (POOL == POOL_BF16) {
         if (in && kh >= 0) *(uint4*)(dst + (vec * D + piece * 8) * 2) = make_uint4(w[0], w[1], w[2], w[3]);
       } else {
-        uint32_t top = 0;                         // magnitudes as bit patterns order like the values
+        uint32_t top = 0;                         // magnitudes as bit patterns order like the values, NaN above all
+        if (v + u * VS < q_heads + heads) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(y[e]) & 0x7fffffffu);
+          for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[i]) & 0x7fffffffu);
+        } else {                                  // bf16 as they came: two at once
+          const uint32_t m = 0x7fff7fffu, z = __vmaxu2(__vmaxu2(w[0] & m, w[1] & m), __vmaxu2(w[2] & m, w[3] & m));
+          top = max(z << 16, z & 0xffff0000u);
+        }
         top = max(top, __shfl_xor_sync(FULL, top, 1));
         const uint32_t block = top;
 #pragma unroll
         for (int s = LV / 2; s > 1; s >>= 1) top = max(top, __shfl_xor_sync(FULL, top, s));
         const bool bad = top >= 0x7f800000u;      // an infinity or NaN
-        const int e = POOL == POOL_E4M3 ? least_exponent(top, 8, 0x600000u) : least_exponent(top, 11, 0x280000u);
-        const float inv = __uint_as_float((uint32_t)(EXP_BIAS - e) << 23);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] *= inv;
+        uint8_t byte;
         if constexpr (POOL == POOL_E4M3) {
+          const int e = least_exponent(top, 8, 0x600000u);
+          byte = (uint8_t)(bad ? BYTE_NAN : e + EXP_BIAS);
+          const float inv = __uint_as_float((uint32_t)(EXP_BIAS - e) << 23);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] *= inv;
           uint2 c = make_uint2(pack_e4m3(y[0], y[1], y[2], y[3]), pack_e4m3(y[4], y[5], y[6], y[7]));
           if (bad) c = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
           if (in && kh >= 0) *(uint2*)(dst + vec * D + piece * 8) = c;
         } else {
-          const uint16_t sc = bad ? 0x7f : (uint16_t)(pack_e4m3(__fdiv_rn(__uint_as_float(block) * inv, 6.0f), 0.0f, 0.0f, 0.0f) & 0xff);
-          const float s = f16x2_to_f32(e4m3_to_f16x2(sc)).x, r = s > 0.0f ? __frcp_rn(s) : 0.0f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float q = y[i] * r;
-            y[i] = __fmaf_rn(__fmaf_rn(-q, s, y[i]), r, q);
-          }
+          const Four f = four_scale(top, block, y, 8);
+          byte = f.byte;
           const uint32_t c = bad ? 0 : pack_e2m1(y);
           if (in && kh >= 0) {
             *(uint32_t*)(dst + vec * (D / 2) + piece * 4) = c;
-            if (!(piece & 1)) (is_v ? P.vb : P.kb)[vec * (D / 16) + piece / 2] = (uint8_t)sc;
+            if (!(piece & 1)) (is_v ? P.vb : P.kb)[vec * (D / 16) + piece / 2] = f.scale;
           }
         }
-        if (in && kh >= 0 && piece == 0) (is_v ? P.vs : P.ks)[vec] = (uint8_t)(bad ? BYTE_NAN : e + EXP_BIAS);
+        if (in && kh >= 0 && piece == 0) (is_v ? P.vs : P.ks)[vec] = byte;
       }
     }
-    v += VS * UT;
+    v += VS * U;
     if (v >= v1) return;
-    load(v);
+#pragma unroll
+    for (int u = 0; u < U; ++u) x[u] = next[u];
   }
 }
 

@@ -194,10 +194,6 @@ __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t* r) {
 }
 __device__ __forceinline__ float ex2(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
 __device__ __forceinline__ float max3(float a, float b, float c) { float y; asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c)); return y; }
-typedef unsigned long long u64;
-__device__ __forceinline__ u64 pk(float lo, float hi) { u64 r; asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi)); return r; }
-__device__ __forceinline__ void upk(u64 v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) { u64 d; asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c)); return d; }
 __device__ __forceinline__ u64 add2(u64 a, u64 b) { u64 d; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b)); return d; }
 __device__ __forceinline__ void group_sync(int id, int n) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ bool group_or(int id, int n, bool v) {
@@ -1278,7 +1274,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         uint8_t* const dst = out0 + bs * C::BUF;
         if (ok) {
           if constexpr (C::E2M1) {
-#pragma unroll
+#pragma unroll 2
             for (int c = 0; c < D / 32; ++c) {             // 32 codes: half a line of the f16 block
               const uint4 x = *(const uint4*)(src + ((D == 128 ? c ^ ((key >> 1) & 3) : c ^ ((key >> 2) & 1)) << 4));
               uint32_t fs, y[16];                          // the scales of what is not valid are 0

@@ -33,9 +33,9 @@ template <bool FP8> constexpr int piece_of = FP8 ? 16 : 8;
 // memory, 2 D bytes read and D + 1 (e4m3) or 2 D written per vector: 35,894
 // tokens of 8 heads of 128 to e4m3 take 39.1 us, 5.65 TB/s; a few tokens 2.7 us,
 // a launch and the chain of search, page, vector and store.
-template <int D, bool FP8>
+template <int D, int POOL>
 __global__ void __launch_bounds__(128) sa_append_kernel(Batch B, Pool P, Rows K, Rows V, int heads) {
-  constexpr int E = piece_of<FP8>, LV = D / E, NL = E / 8;
+  constexpr int E = piece_of<POOL != POOL_BF16>, LV = D / E, NL = E / 8;
   flag_invalid_seqs(B);
   const int lane = threadIdx.x & 31, piece = lane % LV;
   const int pieces = 2 * heads * LV;              // keys, then values
@@ -61,8 +61,31 @@ __global__ void __launch_bounds__(128) sa_append_kernel(Batch B, Pool P, Rows K,
         const bool in = vi < 2 * heads, is_v = vi >= heads;
         const long long vec = vec0 + ((long long)(is_v ? vi - heads : vi) << B.page_shift);
         char* const dst = (char*)(is_v ? P.v : P.k);
-        if constexpr (!FP8) {
+        if constexpr (POOL == POOL_BF16) {
           if (in) *(uint4*)(dst + (vec * D + piece * E) * 2) = x[u][0];
+        } else if constexpr (POOL == POOL_E2M1) {          // a lane's 16 elements share a scale
+          uint32_t w[8], z = 0;
+          float y[16];
+#pragma unroll
+          for (int i = 0; i < NL; ++i) {
+            w[4 * i] = x[u][i].x; w[4 * i + 1] = x[u][i].y; w[4 * i + 2] = x[u][i].z; w[4 * i + 3] = x[u][i].w;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            z = __vmaxu2(z, w[i] & 0x7fff7fffu);           // magnitudes as bit patterns order like the values
+            y[2 * i] = bf_lo(w[i]);
+            y[2 * i + 1] = bf_hi(w[i]);
+          }
+          const uint32_t block = max(z << 16, z & 0xffff0000u);
+          uint32_t top = block;
+#pragma unroll
+          for (int o = LV / 2; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(FULL, top, o));
+          const Four f = four_scale(top, block, y, 16);
+          if (in) {
+            *(uint2*)(dst + vec * (D / 2) + piece * 8) = f.byte == BYTE_NAN ? make_uint2(0, 0) : make_uint2(pack_e2m1(y), pack_e2m1(y + 8));
+            (is_v ? P.vb : P.kb)[vec * (D / 16) + piece] = f.scale;
+            if (piece == 0) (is_v ? P.vs : P.ks)[vec] = f.byte;
+          }
         } else {
           // magnitudes as bf16 bit patterns order like the values, infinities and NaN above all
           uint32_t top = 0, c[4];
@@ -255,15 +278,12 @@ static int launch_rotate(const spec_attn_ctx* h, const Batch& B, const Pool& P, 
   sa_rotate_kernel<D, POOL><<<(unsigned)((warps + 3) / 4), 128, 0, s>>>(B, P, T, Q, K, V, QO, KO, q_heads, h->kv_heads, splits, per);
   return launched();
 }
-static int rotate(const spec_attn_ctx* h, int dtype, const Batch& B, const Pool& P, const Turn& T, const Rows& Q, const Rows& K, const Rows& V,
-                  const RowsOut& QO, const RowsOut& KO, cudaStream_t s) {
-  if (h->D == 128)
-    return dtype == SV_E2M1   ? launch_rotate<128, POOL_E2M1>(h, B, P, T, Q, K, V, QO, KO, s)
-           : dtype == SV_E4M3 ? launch_rotate<128, POOL_E4M3>(h, B, P, T, Q, K, V, QO, KO, s)
-                              : launch_rotate<128, POOL_BF16>(h, B, P, T, Q, K, V, QO, KO, s);
-  return dtype == SV_E2M1   ? launch_rotate<64, POOL_E2M1>(h, B, P, T, Q, K, V, QO, KO, s)
-         : dtype == SV_E4M3 ? launch_rotate<64, POOL_E4M3>(h, B, P, T, Q, K, V, QO, KO, s)
-                            : launch_rotate<64, POOL_BF16>(h, B, P, T, Q, K, V, QO, KO, s);
+template <int D>
+static int launch_turned(const spec_attn_ctx* h, int dtype, const Batch& B, const Pool& P, const Turn& T, const Rows& Q, const Rows& K, const Rows& V,
+                         const RowsOut& QO, const RowsOut& KO, cudaStream_t s) {
+  return dtype == SV_E2M1   ? launch_rotate<D, POOL_E2M1>(h, B, P, T, Q, K, V, QO, KO, s)
+         : dtype == SV_E4M3 ? launch_rotate<D, POOL_E4M3>(h, B, P, T, Q, K, V, QO, KO, s)
+                            : launch_rotate<D, POOL_BF16>(h, B, P, T, Q, K, V, QO, KO, s);
 }
 
 extern "C" int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch,
@@ -275,17 +295,15 @@ extern "C" int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const
   const cudaStream_t s = (cudaStream_t)cuda_stream;
   const Batch B = batch_of(h, batch, pool);
   const Pool P = pool_of(pool);
-  if (pool->dtype == SV_E2M1) {
-    const RowsOut none = {nullptr, 0, 0};
-    return rotate(h, pool->dtype, B, P, Turn{}, rows_of(k), rows_of(k), rows_of(v), none, none, s);
-  }
   const int grid = (B.n_tokens + 3) / 4;           // four warps a block, a token each
   if (h->D == 128) {
-    if (pool->dtype == SV_E4M3) sa_append_kernel<128, true><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
-    else sa_append_kernel<128, false><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
+    if (pool->dtype == SV_E2M1) sa_append_kernel<128, POOL_E2M1><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
+    else if (pool->dtype == SV_E4M3) sa_append_kernel<128, POOL_E4M3><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
+    else sa_append_kernel<128, POOL_BF16><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
   } else {
-    if (pool->dtype == SV_E4M3) sa_append_kernel<64, true><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
-    else sa_append_kernel<64, false><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
+    if (pool->dtype == SV_E2M1) sa_append_kernel<64, POOL_E2M1><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
+    else if (pool->dtype == SV_E4M3) sa_append_kernel<64, POOL_E4M3><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
+    else sa_append_kernel<64, POOL_BF16><<<grid, 128, 0, s>>>(B, P, rows_of(k), rows_of(v), h->kv_heads);
   }
   return launched();
 }
@@ -302,8 +320,10 @@ extern "C" int spec_attn_append_rotated(spec_attn_t h, const spec_attn_pool* poo
     return rc;
   const Turn T = {rope->table, rope->positions, rope->max_positions, rope->rot_dim, rope->interleaved != 0};
   const RowsOut none = {nullptr, 0, 0};
-  return rotate(h, pool->dtype, batch_of(h, batch, pool), pool_of(pool), T, q ? rows_of(q) : rows_of(k), rows_of(k), rows_of(v),
-                q ? out_rows_of(q_out) : none, k_out ? out_rows_of(k_out) : none, (cudaStream_t)cuda_stream);
+  const Rows Q = q ? rows_of(q) : rows_of(k);
+  const RowsOut QO = q ? out_rows_of(q_out) : none, KO = k_out ? out_rows_of(k_out) : none;
+  return (h->D == 128 ? launch_turned<128> : launch_turned<64>)(h, pool->dtype, batch_of(h, batch, pool), pool_of(pool), T, Q, rows_of(k), rows_of(v),
+                                                                QO, KO, (cudaStream_t)cuda_stream);
 }
 
 extern "C" int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_batch* batch,
