@@ -90,9 +90,6 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
   return y;
 }
-__device__ __forceinline__ void async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // A reference before there is a score: -infinity would make NaN of differences.  Scores stay above -2^30, and 2 to the
 // difference of a score that is not seen, or of two of these, is 0 and 1.
 constexpr float NOTHING = -1e30f;

@@ -147,6 +147,9 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* m, int x
   asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                ::"r"(dst), "l"(m), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
 }
+__device__ __forceinline__ void async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 #define R8(r, o) "=r"((r)[o]), "=r"((r)[o + 1]), "=r"((r)[o + 2]), "=r"((r)[o + 3]), "=r"((r)[o + 4]), "=r"((r)[o + 5]), "=r"((r)[o + 6]), "=r"((r)[o + 7])
 #define I8(r, o) "r"((r)[o]), "r"((r)[o + 1]), "r"((r)[o + 2]), "r"((r)[o + 3]), "r"((r)[o + 4]), "r"((r)[o + 5]), "r"((r)[o + 6]), "r"((r)[o + 7])
 __device__ __forceinline__ void prefetch_3d(const CUtensorMap* m, int x, int y, int z) {
@@ -426,22 +429,6 @@ template <bool CODED> __device__ __forceinline__ float scaled(float l, float x) 
   const float h = ex2(0.5f * x);
   return h * l * h;
 }
-// The e4m3 scales of an e2m1 vector: one for every 16 codes
-template <int D> struct Scales {
-  uint32_t w[D / 64];
-  __device__ __forceinline__ uint16_t pair(int i) const { return (uint16_t)(w[i / 2] >> (16 * (i % 2))); }
-};
-template <int D> __device__ __forceinline__ Scales<D> ldg_scales(const uint8_t* p) {
-  Scales<D> r;
-  if constexpr (D == 128) {
-    const uint2 x = __ldg((const uint2*)p);
-    r.w[0] = x.x;
-    r.w[1] = x.y;
-  } else {
-    r.w[0] = __ldg((const uint32_t*)p);
-  }
-  return r;
-}
 // What a row that sees keys 0 .. lim-1 has in a column (0: nothing)
 template <int D> __device__ __forceinline__ float odd_value(const int* odd, int col, int lim) {
   const bool nan = __ldcg(odd + col) < lim, pos = __ldcg(odd + D + col) < lim, neg = __ldcg(odd + 2 * D + col) < lim;
@@ -457,11 +444,14 @@ struct Cfg {
   static constexpr int QBYTES = MT * BUF;
   static constexpr int LINE = E2M1 ? D / 2 : D;               // bytes of a vector's codes
   static constexpr int RAW = BN * LINE;                       // a block of codes
-  static constexpr int NRAW = !CODED ? 0 : D == 128 && !E2M1 ? 4 : 8;
-  static constexpr int SMALL = 3072;                          // barriers and bookkeeping, behind the buffers
+  static constexpr int NRAW = !CODED ? 0 : D == 128 ? (E2M1 ? 6 : 4) : 8;
+  static constexpr int SCALES = BN * (D / 16);                // e2m1: the scales of a block of codes, and behind them
+  static constexpr int SIDE = E2M1 ? SCALES + BN : 0;         // its vectors' exponents
+  static constexpr int SMALL = E2M1 ? 3328 : 3072;            // barriers and bookkeeping, behind the buffers
   static constexpr int NBUF = CODED ? (D == 128 ? 4 : 6) : (SMEM_LIMIT - SMALL - QBYTES) / BUF;
   static constexpr int NK = (NBUF + 1) / 2, NV = NBUF / 2;
-  static constexpr int SMEM = QBYTES + NBUF * BUF + NRAW * RAW + SMALL;
+  static constexpr int SMEM = QBYTES + NBUF * BUF + NRAW * (RAW + SIDE) + SMALL;
+  static_assert(SMEM <= SMEM_LIMIT, "shared memory");
   static constexpr int Q_WARP0 = 2, Q_WARPS = 2;
   static constexpr int SOFT_WARP0 = 4, SOFT_WARPS = 8;        // per tile
   static constexpr int CONV_WARP0 = SOFT_WARP0 + SOFT_WARPS * MT;
@@ -473,7 +463,7 @@ struct Cfg {
   // 1000-16000 e4m3: 327 us with 96 for all, 297 with 120 and 72, 299 with 112 and 80).
   static constexpr int REGS_SOFT = MT == 2 ? 104 : CODED ? 120 : 0, REGS_WORK = CODED ? 96 : 64, REGS_CONV = 72;
   static_assert(REGS_SOFT == 0 || 128 * REGS_WORK + SOFT_WARPS * MT * 32 * REGS_SOFT + CONV_WARPS * 32 * REGS_CONV <= THREADS * 96, "register split");
-  static constexpr int INFO = 8;                              // ring of block references (more than NK + 1)
+  static constexpr int INFO = E2M1 ? 16 : 8;                  // ring of block references (more than NK + 1, and NRAW / 2 ahead)
 };
 // named barriers: pairs of softmax warps of a quarter of a tile's rows, tiles, converting warps
 enum { BAR_PAIR = 1, BAR_TILE = 9, BAR_CONV = 11 };      // the last: one for keys, one for values
@@ -487,7 +477,8 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   extern __shared__ __align__(1024) uint8_t gbase[];
   const uint32_t base = saddr(gbase);
   const uint32_t q_at = base, k_at = q_at + C::QBYTES, v_at = k_at + NK * C::BUF, raw_at = v_at + NV * C::BUF;
-  uint8_t* const small = gbase + (raw_at - base) + C::NRAW * C::RAW;
+  uint8_t* const side0 = gbase + (raw_at - base) + C::NRAW * C::RAW;
+  uint8_t* const small = side0 + C::NRAW * C::SIDE;
   const uint32_t bars = saddr(small);
   // barriers, 8 bytes each
   const uint32_t k_full = bars, k_empty = k_full + 8 * NK, v_full = k_empty + 8 * NK, v_empty = v_full + 8 * NV,
@@ -499,8 +490,9 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   static_assert(8 * (2 * NK + 2 * NV + 2 * C::NRAW + 9) <= 320, "barrier area");
   int* const work = (int*)(small + 320);                  // tensor-memory base, plan, merge flags [16]
   int* const odd_flag = (int*)(small + 640);              // whether a run has values that are not finite in such a block [4]
-  float2* const info = (float2*)(small + 384);            // block references of an e4m3 cache [INFO]
-  int* const red = (int*)(small + 448);                   // planning (20 sums and 2 places of 8 bytes), then the converters' maxima
+  float2* const info = (float2*)(small + 384);            // block references of a coded cache [INFO]
+  int* const red = (int*)(small + 448);                   // planning (20 sums and 2 places of 8 bytes), then the converters' maxima (e4m3)
+  int4* const refs = (int4*)(small + 3072);               // e2m1: exponents of keys and values, whether vectors have their own [INFO]
   Segment* const runs = (Segment*)(small + 768);          // runs as the query warps announce them [4]
   static_assert(sizeof(Segment) <= 64, "ring of runs");
   float* const swap = (float*)(small + 1024);             // [tile][half][row]: between the two threads of a row
@@ -515,9 +507,9 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   if (tid == 0) {
     for (int i = 0; i < NK; ++i) { bar_init(k_full + 8 * i, C::CODED ? 4 : 1); bar_init(k_empty + 8 * i, 1); }
     for (int i = 0; i < NV; ++i) { bar_init(v_full + 8 * i, C::CODED ? 4 : 1); bar_init(v_empty + 8 * i, 1); }
-    for (int i = 0; i < C::NRAW; ++i) { bar_init(raw_full + 8 * i, 1); bar_init(raw_empty + 8 * i, 4); }
+    for (int i = 0; i < C::NRAW; ++i) { bar_init(raw_full + 8 * i, C::E2M1 ? 34 : 1); bar_init(raw_empty + 8 * i, 4); }
     for (int i = 0; i < 2; ++i) { bar_init(s_full + 8 * i, 1); bar_init(p_full + 8 * i, C::SOFT_WARPS); bar_init(o_done + 8 * i, 1); }
-    bar_init(q_full, C::CODED ? C::Q_WARPS : 1);
+    bar_init(q_full, C::E2M1 ? C::CONV_WARPS : C::CODED ? C::Q_WARPS : 1);
     bar_init(q_empty, 1);
     bar_init(drain, 1);
     for (int i = 0; i < 4; ++i) odd_flag[i] = 0;
@@ -719,6 +711,90 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               for (int it = 0; it < 4096 && !bar_try(q_full, (segs - 1) & 1); ++it) {}
           }
           __syncwarp();
+        }
+      } else if constexpr (C::E2M1) {
+        // ---------------------------------------------- scales (e2m1)
+        // One warp, ahead of the conversion: every block's scales and exponents to shared memory, and the exponents
+        // that its keys and values share.  A lane has 4 keys and their values.  Also asks for the run's query rows.
+        if (warp == C::Q_WARP0) {
+          constexpr int NSC = D / 16, VP = 16 / NSC;       // scales of a vector, vectors of a 16-byte piece
+          unsigned n = 0;
+          while (ok && W.next(A, tile_rows, g)) {
+            const __nv_bfloat16* const rows = A.Q.ptr + g.row0 * A.Q.st + g.head * A.group * A.Q.sh;
+            const int n_tok = min(A.tile_tokens, g.ntok);
+            for (int r = lane; r < n_tok * A.group; r += 32) {
+              const char* const line = (const char*)(rows + r / A.group * A.Q.st + r % A.group * A.Q.sh);
+#pragma unroll
+              for (int o = 0; o < 2 * D; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + o));
+            }
+            const int32_t* const tab = A.B.table + (size_t)g.b * A.B.max_pages;
+            const int mask = (1 << A.B.page_shift) - 1;
+            auto page_of = [&](int j) {                    // of this lane's keys of block j; -1: none
+              const int p = j * BN + 4 * lane;
+              const int page = p < g.kv ? __ldg(tab + (p >> A.B.page_shift)) : -1;
+              return (unsigned)page < (unsigned)A.B.num_pages ? page : -1;
+            };
+            auto vectors = [&](int page) { return (unsigned)(page * A.kv_heads + g.head) << A.B.page_shift; };
+            auto load_bytes = [&](int j, int page) {       // the exponents of this lane's keys and values, 0 where there is none
+              uint2 r = make_uint2(0, 0);
+              if (page >= 0) {
+                const int p = j * BN + 4 * lane, left = g.kv - p;
+                const unsigned at = vectors(page) + (p & mask), keep = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1;
+                r = make_uint2(__ldg((const unsigned*)(A.ks + at)) & keep, __ldg((const unsigned*)(A.vs + at)) & keep);
+              }
+              return r;
+            };
+            // largest byte of 4, and in the upper half 255 - the smallest that counts
+            auto extremes = [&](unsigned w) {
+              int most = 0, least = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int byte = (w >> (8 * i)) & 255;
+                most = max(most, byte == BYTE_NAN ? 0 : byte);
+                least = max(least, byte == BYTE_NAN || byte <= BYTE_ZERO ? 0 : 255 - byte);
+              }
+              return make_int2(__reduce_max_sync(FULL, most), __reduce_max_sync(FULL, least));
+            };
+            int run = EV_MIN, page = page_of(g.j0), page1 = page_of(g.j0 + 1);
+            uint2 bytes = load_bytes(g.j0, page);
+            for (int j = g.j0; j < g.j1; ++j, ++n) {
+              const uint2 cur = bytes;
+              const int cur_page = page;
+              bytes = load_bytes(j + 1, page1);
+              page = page1;
+              page1 = page_of(j + 2);
+              const unsigned slot[2] = {2 * n % C::NRAW, (2 * n + 1) % C::NRAW};
+              for (int kv = 0; kv < 2 && ok; ++kv) ok = bar_wait(raw_empty + 8 * slot[kv], (((2 * n + kv) / C::NRAW) & 1) ^ 1, flags);
+              if (!ok) break;
+#pragma unroll
+              for (int x = 0; x < C::SCALES / 512; ++x) {
+                const int piece = x * 32 + lane, key = piece * VP, owner = __shfl_sync(FULL, cur_page, key / 4);
+                if (owner >= 0) {
+                  const size_t at = (size_t)(vectors(owner) + ((j * BN + key) & mask)) * NSC;
+                  async16(saddr(side0 + slot[0] * C::SIDE) + piece * 16, A.kb + at);
+                  async16(saddr(side0 + slot[1] * C::SIDE) + piece * 16, A.vb + at);
+                }
+              }
+              *(unsigned*)(side0 + slot[0] * C::SIDE + C::SCALES + 4 * lane) = cur.x;
+              *(unsigned*)(side0 + slot[1] * C::SIDE + C::SCALES + 4 * lane) = cur.y;
+              const int2 kx = extremes(cur.x), vx = extremes(cur.y);
+              const int ek = max(kx.x - EXP_BIAS, EXP_MIN);
+              const int ev = min(max(vx.x - EXP_BIAS, max(run - 64, EV_MIN)), EV_MAX);
+              run = max(run, ev);
+              const bool wide_k = ek - (255 - kx.y - EXP_BIAS) > SPREAD, wide_v = ev - (255 - vx.y - EXP_BIAS) > SPREAD;
+              if (lane == 0) {
+                refs[n % C::INFO] = make_int4(ek, ev, wide_k, wide_v);
+                info[n % C::INFO] = make_float2(!wide_k ? __int_as_float((ek + EXP_BIAS) << 23) : wide_v ? -1.0f : -256.0f - ev, wide_k || wide_v ? WIDE : (float)ev);
+              }
+              __syncwarp();
+#pragma unroll
+              for (int kv = 0; kv < 2; ++kv) {
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(raw_full + 8 * slot[kv]) : "memory");
+                if (lane == 0) bar_arrive(raw_full + 8 * slot[kv]);
+              }
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
         }
       } else {
         // as f16, normalised by a power of two: 16 bytes a thread, the threads of a row together
@@ -1190,6 +1266,103 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
       if (!g.more) break;
     } while (true);
     }
+  } else if constexpr (C::E2M1) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONV));
+    if (busy) {
+    // ---------------------------------------------- e2m1 codes to f16 blocks
+    // As below, a code times its scale in the place of a code (2 significant bits times 4: exact too); the scales'
+    // warp has found what the block's vectors share.  These warps also lay out the query rows of a run, as soon as
+    // the scores of the run before are done, two threads a row: with nothing else to do then, all eight take 1 us
+    // where two warps of their own took 8.
+    const int key = tid & 127, kv = (warp - C::CONV_WARP0) >> 2;
+    const uint32_t full0 = kv ? v_full : k_full, empty0 = kv ? v_empty : k_empty;
+    const unsigned ring = kv ? NV : NK;
+    uint8_t* const out0 = gbase + ((kv ? v_at : k_at) - base) + key * 128;
+    const uint8_t* const raw0 = gbase + (raw_at - base) + key * C::LINE;
+    unsigned n = 0, segs = 0;
+    bool ok = true;
+    while (ok && W.next(A, tile_rows, g)) {
+      {
+        constexpr int NQ = D / 16;                         // 16-byte pieces of half a row
+        const int t = tid - C::CONV_WARP0 * 32, r = t >> 1, part = t & 1, tok = r / A.group;
+        const __nv_bfloat16* const row = A.Q.ptr + (g.row0 + tok) * A.Q.st + (g.head * A.group + r - tok * A.group) * A.Q.sh + part * (D / 2);
+        if (!(ok = bar_wait(q_empty, (segs & 1) ^ 1, flags))) break;
+        if (t == 0) runs[segs & 3] = g;                    // the softmax is at most two runs behind
+        uint4 x[NQ];
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) x[i] = tok < min(A.tile_tokens, g.ntok) ? __ldg((const uint4*)row + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu), __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+        top = max(top & 0xffff, top >> 16);
+        top = max(top, __shfl_xor_sync(FULL, top, 1));
+        // largest magnitude in [1, 2): f16 holds it exactly, and what is 2^-14 of it or more
+        const int e = top >= 0x7f80u ? 0 : min(max((int)(top >> 7), 7), 247) - EXP_BIAS;
+        const float f = __int_as_float((EXP_BIAS - e) << 23);
+        const u64 f2 = pk(f, f);
+        if (part == 0) q_scale[(segs & 1) * BM + r] = __int_as_float((EXP_BIAS + e) << 23);
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) {
+          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            float a, b;
+            upk(mul2f(pk(bf_lo(w[y]), bf_hi(w[y])), f2), a, b);
+            w[y] = pack_f16(a, b);
+          }
+          const int ch = part * NQ + i;
+          *(uint4*)(gbase + (ch / 8) * HALF_BYTES + r * 128 + (((ch % 8) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) bar_arrive(q_full);
+        ++segs;
+      }
+      for (int j = g.j0; j < g.j1; ++j, ++n) {
+        const unsigned raw = 2 * n + kv, rs = raw % C::NRAW, bs = n % ring;
+        if (!(ok = bar_wait(raw_full + 8 * rs, (raw / C::NRAW) & 1, flags))) break;
+        const uint8_t* const side = side0 + rs * C::SIDE;
+        const bool valid = key < g.kv - j * BN;            // slots past the end may hold anything
+        const int4 ref = refs[n % C::INFO];
+        const int by = side[C::SCALES + key];
+        int d = by - EXP_BIAS - (kv ? ref.y : ref.x);      // <= 0 (1 above EV_MAX)
+        if (kv ? ref.w : ref.z) d = kv ? by - EXP_BIAS - value_exponent(by) : 0;
+        const uint32_t f1 = by == BYTE_NAN ? 0x7e00u : (uint32_t)max(15 + d, 0) << 10, f = f1 | (f1 << 16);   // NaN whatever the codes
+        uint32_t scales[D / 64];
+        if constexpr (D == 128) {
+          const uint2 w = *(const uint2*)(side + key * 8);
+          scales[0] = valid ? w.x : 0;
+          scales[1] = valid ? w.y : 0;
+        } else {
+          scales[0] = valid ? *(const uint32_t*)(side + key * 4) : 0;
+        }
+        if (!(ok = bar_wait(empty0 + 8 * bs, ((n / ring) & 1) ^ 1, flags))) break;
+        const uint8_t* const src = raw0 + rs * C::RAW;
+        uint8_t* const dst = out0 + bs * C::BUF;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {                 // 32 codes: half a line of the f16 block
+          const uint4 w = *(const uint4*)(src + ((D == 128 ? c ^ ((key >> 1) & 3) : c ^ ((key >> 2) & 1)) << 4));
+          uint32_t fs;
+          asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(fs) : "r"(e4m3_to_f16x2((uint16_t)(scales[c / 2] >> (16 * (c % 2))))), "r"(f));
+          const uint32_t f0 = __byte_perm(fs, fs, 0x1010), f8 = __byte_perm(fs, fs, 0x3232), words[4] = {w.x, w.y, w.z, w.w};
+          uint8_t* const line = dst + (c / 2) * HALF_BYTES;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t y[4];
+            e2m1_to_f16(words[i], i < 2 ? f0 : f8, y);
+            *(uint4*)(line + (((4 * (c % 2) + i) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(raw_empty + 8 * rs);
+          bar_arrive(full0 + 8 * bs);
+        }
+      }
+    }
+    }
   } else if constexpr (C::CODED) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_CONV));
     if (busy) {
@@ -1231,31 +1404,20 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const size_t at = ((size_t)(page * A.kv_heads + g.head) << A.B.page_shift) + ((j * BN + key) & ((1 << A.B.page_shift) - 1));
         return make_int2(kv ? 0 : __ldg(A.ks + at), __ldg(A.vs + at));
       };
-      // the e4m3 scales of this thread's vector, one for every 16 codes
-      auto load_scales = [&](int j, int page) {
-        Scales<D> r = {};
-        if (!C::E2M1 || (unsigned)page >= (unsigned)A.B.num_pages) return r;
-        const size_t at = ((size_t)(page * A.kv_heads + g.head) << A.B.page_shift) + ((j * BN + key) & ((1 << A.B.page_shift) - 1));
-        return ldg_scales<D>((kv ? A.vb : A.kb) + at * (D / 16));
-      };
       // largest byte of a warp's vectors, and in the upper half 255 - the smallest that counts
       auto extremes = [&](int byte) {
         const int most = __reduce_max_sync(FULL, byte == BYTE_NAN ? 0 : byte);
         return most | __reduce_max_sync(FULL, byte == BYTE_NAN || byte <= BYTE_ZERO ? 0 : 255 - byte) << 16;
       };
-      int page = page_of(g.j0);
-      int2 nxt = load_bytes(g.j0, page);
-      Scales<D> nxt_scales = load_scales(g.j0, page);
-      page = page_of(g.j0 + 1);
+      int2 nxt = load_bytes(g.j0, page_of(g.j0));
+      int page = page_of(g.j0 + 1);
       for (int j = g.j0; j < g.j1; ++j, ++n) {
         const int2 cur = nxt;
-        const Scales<D> scales = nxt_scales;
         const int ka = kv ? 0 : extremes(cur.x), va = extremes(cur.y);
         int2* const wm = wmax + (n & 1) * 4;
         if (lane == 0) wm[warp & 3] = make_int2(ka, va);
         if ((stop = group_or(bar_id, BN, !ok))) break;     // all four warps leave, or none
         nxt = load_bytes(j + 1, page);
-        nxt_scales = load_scales(j + 1, page);
         page = page_of(j + 2);
         const unsigned kx = __vmaxu2(__vmaxu2(wm[0].x, wm[1].x), __vmaxu2(wm[2].x, wm[3].x));
         const unsigned vx = __vmaxu2(__vmaxu2(wm[0].y, wm[1].y), __vmaxu2(wm[2].y, wm[3].y));
@@ -1273,45 +1435,27 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         const uint8_t* const src = raw0 + rs * C::RAW;
         uint8_t* const dst = out0 + bs * C::BUF;
         if (ok) {
-          if constexpr (C::E2M1) {
-#pragma unroll 2
-            for (int c = 0; c < D / 32; ++c) {             // 32 codes: half a line of the f16 block
-              const uint4 x = *(const uint4*)(src + ((D == 128 ? c ^ ((key >> 1) & 3) : c ^ ((key >> 2) & 1)) << 4));
-              uint32_t fs, y[16];                          // the scales of what is not valid are 0
-              asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(fs) : "r"(e4m3_to_f16x2(scales.pair(c))), "r"(f));
-              const uint32_t f0 = __byte_perm(fs, fs, 0x1010), f8 = __byte_perm(fs, fs, 0x3232);
-              e2m1_to_f16(x.x, f0, y);
-              e2m1_to_f16(x.y, f0, y + 4);
-              e2m1_to_f16(x.z, f8, y + 8);
-              e2m1_to_f16(x.w, f8, y + 12);
-              uint8_t* const line = dst + (c / 2) * HALF_BYTES;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *(uint4*)(line + (((4 * (c % 2) + i) ^ (key & 7)) << 4)) = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-            }
-          } else {
 #pragma unroll 1
-            for (int h = 0; h < D / 64; ++h) {             // 64 codes: one line of the f16 block
-              uint4 xs[4];
+          for (int h = 0; h < D / 64; ++h) {             // 64 codes: one line of the f16 block
+            uint4 xs[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int ch = 4 * h + i;
-                xs[i] = *(const uint4*)(src + ((D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4));
-                if (!valid) xs[i] = make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 4; ++i) {
+              const int ch = 4 * h + i;
+              xs[i] = *(const uint4*)(src + ((D == 128 ? ch ^ (key & 7) : ch ^ ((key >> 1) & 3)) << 4));
+              if (!valid) xs[i] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t w[4] = {xs[i].x, xs[i].y, xs[i].z, xs[i].w};
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const uint32_t hcode = e4m3_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+                asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(hcode), "r"(f));
               }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t w[4] = {xs[i].x, xs[i].y, xs[i].z, xs[i].w};
-                uint32_t y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const uint32_t hcode = e4m3_to_f16x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
-                  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y[e]) : "r"(hcode), "r"(f));
-                }
-                uint8_t* const line = dst + h * HALF_BYTES;
-                *(uint4*)(line + (((2 * i) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-                *(uint4*)(line + (((2 * i + 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-              }
+              uint8_t* const line = dst + h * HALF_BYTES;
+              *(uint4*)(line + (((2 * i) ^ (key & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+              *(uint4*)(line + (((2 * i + 1) ^ (key & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
             }
           }
         }
