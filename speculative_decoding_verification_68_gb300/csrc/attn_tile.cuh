@@ -492,7 +492,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   int* const odd_flag = (int*)(small + 640);              // whether a run has values that are not finite in such a block [4]
   float2* const info = (float2*)(small + 384);            // block references of a coded cache [INFO]
   int* const red = (int*)(small + 448);                   // planning (20 sums and 2 places of 8 bytes), then the converters' maxima (e4m3)
-  int4* const refs = (int4*)(small + 3072);               // e2m1: exponents of keys and values, whether vectors have their own [INFO]
+  int2* const refs = (int2*)(small + 3072);               // e2m1: exponents of blocks, whether vectors have their own: of keys [INFO], values [INFO]
   Segment* const runs = (Segment*)(small + 768);          // runs as the query warps announce them [4]
   static_assert(sizeof(Segment) <= 64, "ring of runs");
   float* const swap = (float*)(small + 1024);             // [tile][half][row]: between the two threads of a row
@@ -534,7 +534,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 
   if (warp < C::SOFT_WARP0) {
     if constexpr (C::REGS_SOFT > 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_WORK));
-    if (busy && warp == 0) {
+    if (busy && warp == 0 && !C::E2M1) {
     // ---------------------------------------------------------------- copies
     const int ps = 1 << A.B.page_shift, ppb = BN >> A.B.page_shift;
     const int nowhere = A.B.num_pages * A.kv_heads * ps;   // a row past the pool: the copy fills zeros
@@ -713,13 +713,13 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
           __syncwarp();
         }
       } else if constexpr (C::E2M1) {
-        // ---------------------------------------------- scales (e2m1)
-        // One warp, ahead of the conversion: every block's scales and exponents to shared memory, and the exponents
-        // that its keys and values share.  A lane has 4 keys and their values.  Also asks for the run's query rows.
+        // ---------------------------------------- codes and scales (e2m1)
+        // One warp for the keys and one for the values, each with a ring of its own: the values of a block are wanted
+        // two blocks of time after its keys, and a common order would let the keys wait for the values' places.  A warp
+        // copies a block's codes, scales and exponents, and finds the exponent that its vectors share, a lane 4 of them;
+        // the keys' warp also the values', for the softmax.  The third warp asks for query rows ahead of time.
         if (warp == C::Q_WARP0) {
-          constexpr int NSC = D / 16, VP = 16 / NSC;       // scales of a vector, vectors of a 16-byte piece
-          unsigned n = 0;
-          while (ok && W.next(A, tile_rows, g)) {
+          while (W.next(A, tile_rows, g)) {
             const __nv_bfloat16* const rows = A.Q.ptr + g.row0 * A.Q.st + g.head * A.group * A.Q.sh;
             const int n_tok = min(A.tile_tokens, g.ntok);
             for (int r = lane; r < n_tok * A.group; r += 32) {
@@ -727,24 +727,39 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
 #pragma unroll
               for (int o = 0; o < 2 * D; o += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(line + o));
             }
+          }
+        } else {
+          constexpr int NSC = D / 16, VP = 16 / NSC, NR = C::NRAW / 2;   // scales of a vector, vectors of a 16-byte piece, blocks of the ring
+          const int kv = warp == 0 ? 0 : 1, ps = 1 << A.B.page_shift, ppb = BN >> A.B.page_shift, per_page = ps / 4;   // lanes of a page
+          const CUtensorMap* const map = kv ? &map_v : &map_k;
+          const uint8_t *const blocks = kv ? A.vb : A.kb, *const exps = kv ? A.vs : A.ks;
+          unsigned n = 0;
+          while (ok && W.next(A, tile_rows, g)) {
             const int32_t* const tab = A.B.table + (size_t)g.b * A.B.max_pages;
-            const int mask = (1 << A.B.page_shift) - 1;
-            auto page_of = [&](int j) {                    // of this lane's keys of block j; -1: none
-              const int p = j * BN + 4 * lane;
-              const int page = p < g.kv ? __ldg(tab + (p >> A.B.page_shift)) : -1;
+            // numbers of 32 pages, and of the next 32, a lane each; -1: none
+            const int used = (g.kv + ps - 1) >> A.B.page_shift, first = (g.j0 * BN) >> A.B.page_shift;
+            auto pages = [&](int c) {
+              const int x = first + 32 * c + lane;
+              return x < used ? __ldg(tab + x) : -1;
+            };
+            int chunk = 0, page0 = pages(0), page1 = pages(1);
+            auto page_of = [&](int j) {                    // of this lane's vectors of block j, of this 32 or the next
+              const int x = (j - g.j0) * ppb + lane / per_page;
+              const int page = __shfl_sync(FULL, x >> 5 == chunk ? page0 : page1, x & 31);
               return (unsigned)page < (unsigned)A.B.num_pages ? page : -1;
             };
             auto vectors = [&](int page) { return (unsigned)(page * A.kv_heads + g.head) << A.B.page_shift; };
-            auto load_bytes = [&](int j, int page) {       // the exponents of this lane's keys and values, 0 where there is none
-              uint2 r = make_uint2(0, 0);
-              if (page >= 0) {
-                const int p = j * BN + 4 * lane, left = g.kv - p;
-                const unsigned at = vectors(page) + (p & mask), keep = left >= 4 ? 0xffffffffu : (1u << (8 * left)) - 1;
-                r = make_uint2(__ldg((const unsigned*)(A.ks + at)) & keep, __ldg((const unsigned*)(A.vs + at)) & keep);
-              }
-              return r;
+            // exponents of this lane's vectors; `kept` clears those past the end when they are used, two blocks on
+            auto load_bytes = [&](const uint8_t* of, int j, int page) {
+              unsigned w = 0;
+              if (page >= 0) w = __ldg((const unsigned*)(of + vectors(page) + ((j * BN + 4 * lane) & (ps - 1))));
+              return w;
             };
-            // largest byte of 4, and in the upper half 255 - the smallest that counts
+            auto kept = [&](unsigned w, int j) {
+              const int left = g.kv - j * BN - 4 * lane;
+              return left >= 4 ? w : left <= 0 ? 0u : w & ((1u << (8 * left)) - 1);
+            };
+            // largest byte of a block's, and 255 - the smallest that counts
             auto extremes = [&](unsigned w) {
               int most = 0, least = 0;
 #pragma unroll
@@ -755,46 +770,59 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
               }
               return make_int2(__reduce_max_sync(FULL, most), __reduce_max_sync(FULL, least));
             };
-            int run = EV_MIN, page = page_of(g.j0), page1 = page_of(g.j0 + 1);
-            uint2 bytes = load_bytes(g.j0, page);
+            int run = EV_MIN, at0 = page_of(g.j0), at1 = page_of(g.j0 + 1);
+            unsigned bytes = load_bytes(exps, g.j0, at0), bytes1 = load_bytes(exps, g.j0 + 1, at1);
+            unsigned vbytes = kv ? 0 : load_bytes(A.vs, g.j0, at0), vbytes1 = kv ? 0 : load_bytes(A.vs, g.j0 + 1, at1);
             for (int j = g.j0; j < g.j1; ++j, ++n) {
-              const uint2 cur = bytes;
-              const int cur_page = page;
-              bytes = load_bytes(j + 1, page1);
-              page = page1;
-              page1 = page_of(j + 2);
-              const unsigned slot[2] = {2 * n % C::NRAW, (2 * n + 1) % C::NRAW};
-              for (int kv = 0; kv < 2 && ok; ++kv) ok = bar_wait(raw_empty + 8 * slot[kv], (((2 * n + kv) / C::NRAW) & 1) ^ 1, flags);
-              if (!ok) break;
+              const unsigned cur = kept(bytes, j), vcur = kv ? cur : kept(vbytes, j), slot = 2 * (n % NR) + kv;
+              const int cur_page = at0;
+              if (((j - g.j0) * ppb) >> 5 != chunk) {
+                ++chunk;
+                page0 = page1;
+                page1 = pages(chunk + 1);
+              }
+              bytes = bytes1;
+              vbytes = vbytes1;
+              at0 = at1;
+              at1 = page_of(j + 2);
+              bytes1 = load_bytes(exps, j + 2, at1);
+              if (!kv) vbytes1 = load_bytes(A.vs, j + 2, at1);
+              if (!(ok = bar_wait(raw_empty + 8 * slot, ((n / NR) & 1) ^ 1, flags))) break;
+              uint8_t* const side = side0 + slot * C::SIDE;
+              *(unsigned*)(side + C::SCALES + 4 * lane) = cur;
+              __syncwarp();
+              if (lane == 0) bar_expect(raw_full + 8 * slot, C::RAW);
+              __syncwarp();
+              const int mine = __shfl_sync(FULL, cur_page, lane * per_page & 31);
+              if (lane < ppb) tma_2d(raw_at + slot * C::RAW + lane * ps * C::LINE, map, 0, mine < 0 ? A.B.num_pages * A.kv_heads * ps : (int)vectors(mine), raw_full + 8 * slot);
 #pragma unroll
               for (int x = 0; x < C::SCALES / 512; ++x) {
                 const int piece = x * 32 + lane, key = piece * VP, owner = __shfl_sync(FULL, cur_page, key / 4);
-                if (owner >= 0) {
-                  const size_t at = (size_t)(vectors(owner) + ((j * BN + key) & mask)) * NSC;
-                  async16(saddr(side0 + slot[0] * C::SIDE) + piece * 16, A.kb + at);
-                  async16(saddr(side0 + slot[1] * C::SIDE) + piece * 16, A.vb + at);
-                }
+                if (owner >= 0) async16(saddr(side) + piece * 16, blocks + (size_t)(vectors(owner) + ((j * BN + key) & (ps - 1))) * NSC);
               }
-              *(unsigned*)(side0 + slot[0] * C::SIDE + C::SCALES + 4 * lane) = cur.x;
-              *(unsigned*)(side0 + slot[1] * C::SIDE + C::SCALES + 4 * lane) = cur.y;
-              const int2 kx = extremes(cur.x), vx = extremes(cur.y);
-              const int ek = max(kx.x - EXP_BIAS, EXP_MIN);
+              const int2 vx = extremes(vcur);
               const int ev = min(max(vx.x - EXP_BIAS, max(run - 64, EV_MIN)), EV_MAX);
               run = max(run, ev);
-              const bool wide_k = ek - (255 - kx.y - EXP_BIAS) > SPREAD, wide_v = ev - (255 - vx.y - EXP_BIAS) > SPREAD;
-              if (lane == 0) {
-                refs[n % C::INFO] = make_int4(ek, ev, wide_k, wide_v);
-                info[n % C::INFO] = make_float2(!wide_k ? __int_as_float((ek + EXP_BIAS) << 23) : wide_v ? -1.0f : -256.0f - ev, wide_k || wide_v ? WIDE : (float)ev);
+              const bool wide_v = ev - (255 - vx.y - EXP_BIAS) > SPREAD;
+              if (kv) {
+                if (lane == 0) refs[C::INFO + n % C::INFO] = make_int2(ev, wide_v);
+              } else {
+                const int2 kx = extremes(cur);
+                const int ek = max(kx.x - EXP_BIAS, EXP_MIN);
+                const bool wide_k = ek - (255 - kx.y - EXP_BIAS) > SPREAD;
+                if (lane == 0) {                           // for the softmax too, ahead of the keys and so of the block's scores
+                  refs[n % C::INFO] = make_int2(ek, wide_k);
+                  info[n % C::INFO] = make_float2(!wide_k ? __int_as_float((ek + EXP_BIAS) << 23) : wide_v ? -1.0f : -256.0f - ev, wide_k || wide_v ? WIDE : (float)ev);
+                }
               }
-              __syncwarp();
-#pragma unroll
-              for (int kv = 0; kv < 2; ++kv) {
-                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(raw_full + 8 * slot[kv]) : "memory");
-                if (lane == 0) bar_arrive(raw_full + 8 * slot[kv]);
-              }
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(raw_full + 8 * slot) : "memory");
+              if (lane == 0) bar_arrive(raw_full + 8 * slot);
             }
           }
           asm volatile("cp.async.wait_all;" ::: "memory");
+          if (!ok)                                         // let the copies in flight land
+            for (unsigned i = n > NR ? n - NR : 0; i < n; ++i)
+              for (int it = 0; it < 4096 && !bar_try(raw_full + 8 * (2 * (i % NR) + kv), (i / NR) & 1); ++it) {}
         }
       } else {
         // as f16, normalised by a power of two: 16 bytes a thread, the threads of a row together
@@ -1320,14 +1348,15 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         ++segs;
       }
       for (int j = g.j0; j < g.j1; ++j, ++n) {
-        const unsigned raw = 2 * n + kv, rs = raw % C::NRAW, bs = n % ring;
-        if (!(ok = bar_wait(raw_full + 8 * rs, (raw / C::NRAW) & 1, flags))) break;
+        constexpr unsigned NR = C::NRAW / 2;
+        const unsigned rs = 2 * (n % NR) + kv, bs = n % ring;
+        if (!(ok = bar_wait(raw_full + 8 * rs, (n / NR) & 1, flags))) break;
         const uint8_t* const side = side0 + rs * C::SIDE;
         const bool valid = key < g.kv - j * BN;            // slots past the end may hold anything
-        const int4 ref = refs[n % C::INFO];
+        const int2 ref = refs[kv * C::INFO + n % C::INFO];
         const int by = side[C::SCALES + key];
-        int d = by - EXP_BIAS - (kv ? ref.y : ref.x);      // <= 0 (1 above EV_MAX)
-        if (kv ? ref.w : ref.z) d = kv ? by - EXP_BIAS - value_exponent(by) : 0;
+        int d = by - EXP_BIAS - ref.x;                     // <= 0 (1 above EV_MAX)
+        if (ref.y) d = kv ? by - EXP_BIAS - value_exponent(by) : 0;
         const uint32_t f1 = by == BYTE_NAN ? 0x7e00u : (uint32_t)max(15 + d, 0) << 10, f = f1 | (f1 << 16);   // NaN whatever the codes
         uint32_t scales[D / 64];
         if constexpr (D == 128) {
@@ -1340,7 +1369,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         if (!(ok = bar_wait(empty0 + 8 * bs, ((n / ring) & 1) ^ 1, flags))) break;
         const uint8_t* const src = raw0 + rs * C::RAW;
         uint8_t* const dst = out0 + bs * C::BUF;
-#pragma unroll
+#pragma unroll 2
         for (int c = 0; c < D / 32; ++c) {                 // 32 codes: half a line of the f16 block
           const uint4 w = *(const uint4*)(src + ((D == 128 ? c ^ ((key >> 1) & 3) : c ^ ((key >> 2) & 1)) << 4));
           uint32_t fs;
