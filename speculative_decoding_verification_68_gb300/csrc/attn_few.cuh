@@ -26,11 +26,12 @@
 // product as one f16 factor.  So vectors may differ in size as they like.
 //
 // Work is cut into runs as in attn_tile.cuh (the same schedule, with up to 16
-// rows to a tile).  Warps: three copy slices, one lays out query rows as f16, and
-// the others, 16 or 12 for 8 or 16 rows, are as above.  A slice is 4,672 bytes at
-// D = 128.  Every consuming warp has a ring of its own, which the same copying
-// warp fills: barriers are waited on by parity, and a ring that several filled or
-// emptied, out of step, could be two rounds ahead of one of them.
+// rows to a tile).  One warp announces the runs and lays out query rows as f16, a
+// run ahead; the others, 15 or 11 for 8 or 16 rows, are as above.  Each copies its
+// own slices, two or more ahead, into places of its own, so that none waits for
+// another but at a run's end, where it has the next run's first slices on the way
+// already.  (Three copying warps for all, in turns: a warp waited for its slice for
+// 37% of the time, behind those that were late.)
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -45,12 +46,8 @@ namespace {
 template <int D, int NTILES>
 struct Few {
   static constexpr int R = 8 * NTILES;                     // rows
-  static constexpr int CONSUMERS = NTILES == 1 ? 16 : 12;
-  static constexpr int WARPS = CONSUMERS + 4, THREADS = WARPS * 32, CT = CONSUMERS * 32;
-  // Registers: 640 threads start with 96, 512 with 128; the first four warps keep 56
-  static constexpr int REGS = NTILES == 1 ? 104 : 152, REGS_COPY = 56;
-  static constexpr int REGS_LAUNCH = NTILES == 1 ? 96 : 128;
-  static_assert(128 * REGS_COPY + CT * REGS <= THREADS * REGS_LAUNCH, "register split");
+  static constexpr int CONSUMERS = NTILES == 1 ? 15 : 11;        // and one for queries: 4 or 3 warps to a quarter of the registers
+  static constexpr int WARPS = CONSUMERS + 1, THREADS = WARPS * 32, CT = CONSUMERS * 32;   // the last one: query rows
   static constexpr int SLICE = 32;                         // keys
   static constexpr int LINE = D / 2, NSC = D / 16;         // bytes of a vector's codes, its scales
   static constexpr int K_AT = 0, V_AT = SLICE * LINE, KB_AT = 2 * SLICE * LINE, VB_AT = KB_AT + SLICE * NSC, KS_AT = VB_AT + SLICE * NSC, VS_AT = KS_AT + SLICE;
@@ -64,7 +61,7 @@ struct Few {
   static constexpr int CM = NTILES == 1 ? 4 : 2;           // of them merged at a time
   static_assert(MT % CM == 0 && CM > 0, "merge passes");
   static constexpr int MERGE = CONSUMERS * CM * NTILES * 512;
-  static constexpr int SMALL = 2048;                       // barriers and bookkeeping
+  static constexpr int SMALL = 384;                        // barriers and bookkeeping
   static constexpr int OUT_AT = SMALL, OUT = R * D * 4;
   static constexpr int STAT_AT = OUT_AT + OUT, STAT = CONSUMERS * R * 16;      // (M, N, l, -) of every warp and row
   static constexpr int ROW_AT = STAT_AT + STAT, ROW = R * 16;                  // of the run
@@ -113,17 +110,16 @@ enum { BAR_ALL = 1 };              // the consuming warps
 template <int D, int NTILES>
 __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(const __grid_constant__ AttnParams A, const uint8_t* kc, const uint8_t* vc) {
   using C = Few<D, NTILES>;
-  constexpr int R = C::R, NS = C::NS, MT = C::MT, CT = C::CT;
+  constexpr int R = C::R, MT = C::MT, CT = C::CT;
   extern __shared__ __align__(1024) uint8_t mem[];
-  const uint32_t base = saddr(mem), full = base, empty = full + 8 * NS, q_full = empty + 8 * NS, q_empty = q_full + 16;
-  int* const work = (int*)(mem + 16 * NS + 32);           // plan [16]
-  Segment* const runs = (Segment*)(mem + 16 * NS + 96);   // as the query warp announces them [4]
-  static_assert(16 * NS + 96 + 4 * 64 <= C::SMALL && sizeof(Segment) <= 64 && NS % 2 == 0, "bookkeeping");
+  const uint32_t base = saddr(mem), q_full = base, q_empty = q_full + 16;
+  int* const work = (int*)(mem + 32);                     // plan [16]
+  Segment* const runs = (Segment*)(mem + 96);             // as the query warp announces them [4]
+  static_assert(96 + 4 * 64 <= C::SMALL && sizeof(Segment) <= 64, "bookkeeping");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* const flags = A.B.flags;
 
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) { bar_init(full + 8 * i, 32); bar_init(empty + 8 * i, 1); }
     for (int i = 0; i < 2; ++i) { bar_init(q_full + 8 * i, 1); bar_init(q_empty + 8 * i, 1); }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -135,70 +131,8 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
   // slices of a run of an item's blocks
   auto slices = [&](const Segment& g) { return max(0, (min(g.kv, g.j1 * BN) - g.j0 * BN + C::SLICE - 1) / C::SLICE); };
 
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_COPY));
-    if (busy && warp != 1) {
-      // -------------------------------------------------------------- copies
-      // For every third of the consuming warps each, 16 bytes a lane at a time.  A slice is two runs of 16 keys, in one page or in two
-      // of 16 slots.  Lanes hold 32 pages' numbers, and the next 32.
-      const int p = warp == 0 ? 0 : warp - 1;
-      constexpr int SC = C::NSC;                           // 16-byte pieces of 16 keys' scales
-      const int sl = lane & (4 * SC - 1), sl_half = sl / SC & 1;               // this lane's piece of the scales
-      const uint8_t* const sc_src = (sl < 2 * SC ? A.kb : A.vb) + (sl & (SC - 1)) * 16;
-      const int sc_at = (sl < 2 * SC ? C::KB_AT : C::VB_AT) + sl % (2 * SC) * 16;
-      const uint8_t* const ex_src = lane & 2 ? A.vs : A.ks;
-      const int ex_at = (lane & 2 ? C::VS_AT : C::KS_AT) + (lane & 1) * 16;
-      const uint8_t *const kc_lane = kc + lane * 16, *const vc_lane = vc + lane * 16;
-      unsigned done = 0;                                   // slices of the lane's consuming warp in earlier runs
-      bool ok = true;
-      Segment g;
-      while (ok && W.next(A, A.tile_tokens, g)) {
-        const int32_t* const tab = A.B.table + (size_t)g.b * A.B.max_pages;
-        const int used = (g.kv + ps - 1) >> shift, first = (g.j0 * BN) >> shift, count = slices(g);
-        auto pages = [&](int c) {                          // numbers of pages first + 32 c on, 0 where there is none:
-          const int x = first + 32 * c + lane;             // such a page's slots are not used, or their rows are NaN
-          const int page = x < used ? __ldg(tab + x) : 0;
-          return (unsigned)page < (unsigned)A.B.num_pages ? page : 0;
-        };
-        int chunk = 0, cur = pages(0), nxt = pages(1);
-        int w = p;
-        unsigned round = 0;
-        for (int i = p; i < count; i = (int)round * C::CONSUMERS + w) {        // slice i is warp w's
-          const unsigned n = __shfl_sync(FULL, done, w) + round, s = w * C::DEPTH + n % C::DEPTH;
-          const int pos = g.j0 * BN + i * C::SLICE, e = (pos >> shift) - first;
-          if (e >> 5 != chunk) {
-            ++chunk;
-            cur = nxt;
-            nxt = pages(chunk + 1);
-          }
-          const int page0 = __shfl_sync(FULL, cur, e & 31), page1 = __shfl_sync(FULL, cur, (e + 1) & 31);
-          // vectors of a pool are counted in 31 bits
-          const unsigned v0 = ((unsigned)(page0 * A.kv_heads + g.head) << shift) + (pos & (ps - 1));
-          const unsigned v1 = ps == 16 ? (unsigned)(page1 * A.kv_heads + g.head) << shift : v0 + 16;
-          if (!(ok = bar_wait(empty + 8 * s, ((n / C::DEPTH) & 1) ^ 1, flags))) break;
-          const uint32_t dst = base + C::RING_AT + s * C::STAGE, to = dst + lane * 16;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint8_t *const k = kc_lane + (size_t)(h ? v1 : v0) * C::LINE, *const v = vc_lane + (size_t)(h ? v1 : v0) * C::LINE;
-#pragma unroll
-            for (int x = 0; x < C::LINE / 32; ++x) {
-              async16(to + C::K_AT + (h * (C::LINE / 32) + x) * 512, k + x * 512);
-              async16(to + C::V_AT + (h * (C::LINE / 32) + x) * 512, v + x * 512);
-            }
-          }
-          if (lane < 4 * SC) async16(dst + sc_at, sc_src + (size_t)(sl_half ? v1 : v0) * SC);
-          if (lane < 4) async16(dst + ex_at, ex_src + (lane & 1 ? v1 : v0));
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(full + 8 * s) : "memory");
-          w += 3;
-          if (w >= C::CONSUMERS) {
-            w = p;
-            ++round;
-          }
-        }
-        done += max(0, count - lane + C::CONSUMERS - 1) / C::CONSUMERS;
-      }
-      asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (busy && warp == 1) {
+  if (warp == C::CONSUMERS) {
+    if (busy) {
       // ---------------------------------------------------------- query rows
       // As f16, normalised by a power of two, 8 elements a lane.  Element 8 ch + .. of row r goes where the product's
       // thread finds its D / 4 elements in 16-byte pieces, the pieces of a warp next to one another.
@@ -245,10 +179,9 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS));
     if (busy) {
       // ----------------------------------------------------- scores to outputs
-      const int w = warp - 4, ct = tid - 128, gq = lane >> 2, t4 = lane & 3;   // row group and place in it of operand fragments
+      const int w = warp, ct = tid, gq = lane >> 2, t4 = lane & 3;   // row group and place in it of operand fragments
       constexpr int DV = D / 8;                            // columns of a value that a thread takes
       float4* const stat = (float4*)(mem + C::STAT_AT);    // [warp][row]
       float4* const row_stat = (float4*)(mem + C::ROW_AT); // [row]
@@ -256,11 +189,66 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
       float* const res = (float*)(mem + C::OUT_AT);        // [row][D]
       unsigned n = 0, segs = 0;                            // slices of this warp, runs
       bool ok = true;
+      // ---- copies.  The cursor: the run it is in, its next slice there, what has been asked for and not used, and the
+      // page of the slice's first and second 16 keys (in lanes 0 and 1), loaded a slice ahead
+      unsigned at_run = 0, asked = 0, pending = 0;
+      int at = 0, at_count = 0, at_pos0 = 0, at_used = 0, at_head = 0, at_page = 0;
+      const int32_t* at_tab = nullptr;
+      constexpr int SC = C::NSC;                           // 16-byte pieces of 16 keys' scales
+      const int sl = lane & (4 * SC - 1), sl_half = sl / SC & 1;               // this lane's piece of the scales
+      const uint8_t *const kc_lane = kc + lane * 16, *const vc_lane = vc + lane * 16;
+      const uint8_t* const sc_src = (sl < 2 * SC ? A.kb : A.vb) + (sl & (SC - 1)) * 16;
+      const int sc_at = (sl < 2 * SC ? C::KB_AT : C::VB_AT) + sl % (2 * SC) * 16;
+      const uint8_t* const ex_src = lane & 2 ? A.vs : A.ks;
+      const int ex_at = (lane & 2 ? C::VS_AT : C::KS_AT) + (lane & 1) * 16;
+      const uint32_t ring = base + C::RING_AT + w * C::DEPTH * C::STAGE;
+      auto look_up = [&]() {                               // numbers of the pages of slice `at`; 0 where there is none: such a
+        const int x = ((at_pos0 + at * C::SLICE) >> shift) + (ps == 16 ? lane & 1 : 0);   // page's slots are not used, or their rows NaN
+        at_page = x < at_used && at < at_count ? __ldg(at_tab + x) : 0;
+      };
+      auto enter = [&](unsigned run) {                     // an announced run
+        const Segment& g = runs[run & 3];
+        at_run = run;
+        at = w;
+        at_count = slices(g);
+        at_pos0 = g.j0 * BN;
+        at_used = (g.kv + ps - 1) >> shift;
+        at_head = g.head;
+        at_tab = A.B.table + (size_t)g.b * A.B.max_pages;
+        look_up();
+      };
+      auto ask = [&]() {                                   // asks for slice `at`
+        const int page = (unsigned)at_page < (unsigned)A.B.num_pages ? at_page : 0, pos = at_pos0 + at * C::SLICE;
+        const int page0 = __shfl_sync(FULL, page, 0), page1 = __shfl_sync(FULL, page, 1);
+        at += C::CONSUMERS;
+        look_up();
+        // vectors of a pool are counted in 31 bits
+        const unsigned v0 = ((unsigned)(page0 * A.kv_heads + at_head) << shift) + (pos & (ps - 1));
+        const unsigned v1 = ps == 16 ? (unsigned)(page1 * A.kv_heads + at_head) << shift : v0 + 16;
+        const uint32_t dst = ring + asked % C::DEPTH * C::STAGE, to = dst + lane * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t *const k = kc_lane + (size_t)(h ? v1 : v0) * C::LINE, *const v = vc_lane + (size_t)(h ? v1 : v0) * C::LINE;
+#pragma unroll
+          for (int x = 0; x < C::LINE / 32; ++x) {
+            async16(to + C::K_AT + (h * (C::LINE / 32) + x) * 512, k + x * 512);
+            async16(to + C::V_AT + (h * (C::LINE / 32) + x) * 512, v + x * 512);
+          }
+        }
+        if (lane < 4 * SC) async16(dst + sc_at, sc_src + (size_t)(sl_half ? v1 : v0) * SC);
+        if (lane < 4) async16(dst + ex_at, ex_src + (lane & 1 ? v1 : v0));
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        ++asked;
+        ++pending;
+      };
       do {
         const unsigned buf = segs & 1;
         ok = bar_wait(q_full + 8 * buf, (segs >> 1) & 1, flags);
         if (group_or(BAR_ALL, CT, !ok)) break;             // all of them leave, or none
         const Segment& g = runs[segs & 3];
+        if (segs == 0 || at_run != segs) enter(segs);
+        while (pending < C::DEPTH && at < at_count) ask();
+        const bool more = g.more != 0;
         const int count = slices(g), kv = g.kv, pos0 = g.j0 * BN, lim0 = g.lim0;
         const int all_see = A.causal ? min(g.lim0, kv) : kv;       // keys that every row sees
         bool small_q = true;                               // factors of scores stay far from the ends of their range
@@ -278,10 +266,12 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
           }
         small_q = __all_sync(FULL, small_q);
         for (int i = w; i < count; i += C::CONSUMERS, ++n) {
-          const unsigned s = w * C::DEPTH + n % C::DEPTH;
-          if (ok) ok = bar_wait(full + 8 * s, (n / C::DEPTH) & 1, flags);
-          if (!ok) break;
-          uint8_t* const st = mem + C::RING_AT + s * C::STAGE;
+          if (pending == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");           // the oldest has to be there
+          else if (pending == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+          else if (pending == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+          else asm volatile("cp.async.wait_group 3;" ::: "memory");
+          __syncwarp();
+          uint8_t* const st = mem + C::RING_AT + (w * C::DEPTH + n % C::DEPTH) * C::STAGE;
           const int pos = pos0 + i * C::SLICE;
           const bool edge = pos + C::SLICE > all_see;
           // ---- what is rare is put right in the slice itself, a lane a key: slots past the end, which may hold
@@ -514,7 +504,9 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
             }
           }
           __syncwarp();
-          if (lane == 0) bar_arrive(empty + 8 * s);
+          --pending;
+          if (at_run == segs && at >= at_count && more && ok && (ok = bar_wait(q_full + 8 * (buf ^ 1), ((segs + 1) >> 1) & 1, flags))) enter(segs + 1);
+          if (at < at_count) ask();
         }
         // ---- the warps' results meet
         const int parts = min(count, C::CONSUMERS);
@@ -640,10 +632,10 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
           }
         }
         ++segs;
-        const bool more = g.more != 0;
         group_sync(BAR_ALL, CT);                           // results and statistics are used again
         if (!more) break;
       } while (true);
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
 }
