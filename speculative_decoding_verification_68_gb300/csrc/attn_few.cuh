@@ -58,7 +58,7 @@ struct Few {
   static constexpr int QBYTES = R * D * 2;
   static constexpr int CJ = D / 32;                        // words of codes of a key that a thread takes
   static constexpr int MT = D / 16;                        // 16-column tiles of the output
-  static constexpr int CM = NTILES == 1 ? 4 : 2;           // of them merged at a time
+  static constexpr int CM = NTILES == 1 ? MT : 4;         // of them merged at a time
   static_assert(MT % CM == 0 && CM > 0, "merge passes");
   static constexpr int MERGE = CONSUMERS * CM * NTILES * 512;
   static constexpr int SMALL = 384;                        // barriers and bookkeeping
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   long long units, ctas;
-  Walker W = plan_run<C::THREADS>(A, A.tile_tokens, (long long*)(mem + C::OUT_AT), work, units, ctas);
+  Walker W = plan_run<C::THREADS, true>(A, A.tile_tokens, (long long*)(mem + C::OUT_AT), work, units, ctas);
   __syncthreads();
   const bool busy = W.any();
   const int shift = A.B.page_shift, ps = 1 << shift;
@@ -560,12 +560,18 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
 #pragma unroll
                 for (int c = 0; c < 4; ++c) merge[w * PASS + (m * NTILES + nt) * 128 + c * 32 + lane] = o[m0 + m][nt][c];
           group_sync(BAR_ALL, CT);
-          for (int x = ct; x < PASS; x += CT) {
-            float sum = 0.0f;
-            for (int y = 0; y < parts; ++y) sum += merge[y * PASS + x];
-            const int ln = x & 31, c = (x >> 5) & 3, nt = (x >> 7) % NTILES, m = m0 + (x >> 7) / NTILES;
+          for (int x4 = ct; x4 < PASS / 4; x4 += CT) {
+            float4 sum = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int y = 0; y < parts; ++y) {
+              const float4 t = *(const float4*)(merge + y * PASS + 4 * x4);
+              sum.x += t.x; sum.y += t.y; sum.z += t.z; sum.w += t.w;
+            }
+            // four lanes of a row group: the same columns of rows two apart
+            const int x = 4 * x4, ln = x & 31, c = (x >> 5) & 3, nt = (x >> 7) % NTILES, m = m0 + (x >> 7) / NTILES;
             const int col = NTILES == 1 ? 4 * (m >> 1) + 2 * (c >> 1) + (m & 1) : 2 * m + (c >> 1);
-            res[(nt * 8 + 2 * (ln & 3) + (c & 1)) * D + DV * (ln >> 2) + col] = sum;
+            float* const to = res + (nt * 8 + (c & 1)) * D + DV * (ln >> 2) + col;
+            to[0] = sum.x; to[2 * D] = sum.y; to[4 * D] = sum.z; to[6 * D] = sum.w;
           }
         }
         group_sync(BAR_ALL, CT);

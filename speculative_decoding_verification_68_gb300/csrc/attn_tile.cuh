@@ -285,12 +285,114 @@ struct Walker {
   }
 };
 
+// The same by every warp for itself, of up to SHORT_SEQS sequences and 2^24 units: no barriers, and numbers of 32 bits,
+// whose divisions are short (%SHORT%).  False: not for this batch, in all warps.
+constexpr int SHORT_SEQS = 128;
+__device__ __forceinline__ bool plan_short(const AttnParams& A, int tile_rows, Walker& W, long long& units64, long long& ctas64) {
+  const int lane = threadIdx.x & 31;
+  if (A.B.n_seqs > SHORT_SEQS) return false;
+  constexpr int CH = SHORT_SEQS / 32;
+  Seq s[CH];
+  unsigned end[CH];                                       // units up to the end of the lane's sequence
+  bool fits = true;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    s[i] = Seq{0, 0, 0, 0, false};
+    if (32 * i + lane < A.B.n_seqs) s[i] = load_seq(A.B, 32 * i + lane, tile_rows);
+  }
+  unsigned units = 0;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    if (32 * i >= A.B.n_seqs) {                           // uniform
+      end[i] = units;
+      continue;
+    }
+    if (s[i].bad && blockIdx.x == 0) A.B.flags[0] = 1;
+    const long long mine = tiles_before(s[i], s[i].tiles, tile_rows, A.causal) * A.kv_heads;
+    fits &= mine < 1 << 17;                               // 128 of these are 2^24
+    unsigned scan = (unsigned)mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned x = __shfl_up_sync(FULL, scan, o);
+      if (lane >= o) scan += x;
+    }
+    end[i] = units + scan;
+    units += __shfl_sync(FULL, scan, 31);
+  }
+  if (!__all_sync(FULL, fits)) return false;
+  const unsigned runs = min(gridDim.x, max(1u, units / MIN_RUN));
+  units64 = units;
+  ctas64 = runs;
+  W.at = W.u1 = 0;                                        // an empty run
+  W.b = W.head = W.t = 0;
+  if (blockIdx.x >= runs || units == 0) return true;
+  const unsigned cut[2] = {units * blockIdx.x / runs, units * (blockIdx.x + 1) / runs};
+  long long to[2], from = 0;
+#pragma unroll
+  for (int e = 1; e >= 0; --e) {
+    to[e] = cut[e];
+    if (cut[e] == units) continue;
+    // the sequence: the first whose end lies past the cut
+    int b = -1;
+    Seq q = s[0];
+    unsigned begin = 0, size = 0;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const unsigned past = b < 0 ? __ballot_sync(FULL, end[i] > cut[e]) : 0;
+      if (past) {
+        const int l = __ffs(past) - 1;
+        b = 32 * i + l;
+        q.row0 = __shfl_sync(FULL, s[i].row0, l);
+        q.n = __shfl_sync(FULL, s[i].n, l);
+        q.kv = __shfl_sync(FULL, s[i].kv, l);
+        q.tiles = __shfl_sync(FULL, s[i].tiles, l);
+        q.bad = __shfl_sync(FULL, (int)s[i].bad, l);
+        const unsigned prev_chunk = i > 0 ? __shfl_sync(FULL, end[i > 0 ? i - 1 : 0], 31) : 0;
+        begin = l > 0 ? __shfl_sync(FULL, end[i], l > 0 ? l - 1 : 0) : prev_chunk;
+        size = __shfl_sync(FULL, end[i], l) - begin;
+      }
+    }
+    const unsigned per_head = size / A.kv_heads, head = (cut[e] - begin) / per_head, r = cut[e] - begin - head * per_head;
+    int t = 0, in = 0, units_of = 0;
+    for (int t0 = 0; t0 < q.tiles; t0 += 32) {            // its tile
+      const int x = t0 + lane;
+      const long long lo = x < q.tiles ? tiles_before(q, x, tile_rows, A.causal) : 0;
+      const int all = x < q.tiles ? SETUP + tile_blocks(q, x, tile_rows, A.causal) : 0;
+      const unsigned hit = __ballot_sync(FULL, x < q.tiles && lo <= r && r < lo + all);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        t = t0 + l;
+        in = (int)r - __shfl_sync(FULL, (int)lo, l);
+        units_of = __shfl_sync(FULL, all, l);
+        break;
+      }
+    }
+    W.b = b; W.head = (int)head; W.t = t;
+    W.s = q;
+    from = (long long)cut[e] - in;
+    to[e] = moved_cut(cut[e], in, units_of);
+  }
+  W.u0 = to[0];
+  W.u1 = to[1];
+  W.at = from;
+  if (W.u0 < W.u1 && W.u0 > from && to[0] != (long long)cut[0]) {   // moved to the end of that item
+    W.at = W.u0;
+    W.advance(A, tile_rows);
+  }
+  if (W.u0 >= W.u1) W.at = W.u1;
+  return true;
+}
+
 // This CTA's run of units (all NT threads; red64 holds 22 sums and places, found 10 places from 1 on).
 // Also reports sequences that are not valid.
-template <int NT>
+template <int NT, bool SHORT>
 __device__ __forceinline__ Walker plan_run(const AttnParams& A, int tile_rows, long long* red64, int* work, long long& units, long long& ctas) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int* const flags = A.B.flags;
+  if constexpr (SHORT) {
+    Walker W;
+    if (plan_short(A, tile_rows, W, units, ctas)) return W;
+  }
   long long mine = 0;
   for (int b = tid; b < A.B.n_seqs; b += NT) {
     const Seq s = load_seq(A.B, b, tile_rows);
@@ -520,7 +622,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   long long units, ctas;
-  Walker W = plan_run<NT>(A, tile_rows, (long long*)red, work, units, ctas);
+  Walker W = plan_run<NT, C::E2M1>(A, tile_rows, (long long*)red, work, units, ctas);
   tc_before();
   __syncthreads();
   tc_after();

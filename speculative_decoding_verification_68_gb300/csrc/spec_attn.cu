@@ -436,8 +436,8 @@ static bool two_tiles(const spec_attn_ctx* h, const AttnParams& A, long long key
 // Rows of a tile of the kernel for few rows, 0: not for this call.  The mean number of rows of a sequence and head
 // decides, and a tile holds a group at least.
 static int few_rows(const AttnParams& A) {
-  const long long rows = ((long long)A.B.n_tokens * A.group + A.B.n_seqs - 1) / A.B.n_seqs;
-  return A.group > 16 || rows > 16 ? 0 : rows <= 8 && A.group <= 8 ? 8 : 16;
+  const long long mean = ((long long)A.B.n_tokens * A.group + A.B.n_seqs - 1) / A.B.n_seqs, rows = mean > A.group ? mean : A.group;
+  return rows > 16 ? 0 : rows <= 8 ? 8 : 16;
 }
 
 extern "C" int spec_attn_init(spec_attn_t* out, int q_heads, int kv_heads, int head_dim, int max_seqs) {
