@@ -153,6 +153,7 @@ CASES = [  # new, old, hq, hkv, d, page
     ([1] * 150, list(range(0, 750, 5)), 8, 1, 64, 32),
     ([3] * 30, list(range(0, 1500, 50)), 16, 4, 128, 16),
     ([100], [1000], 4, 4, 128, 16),
+    ([3] * 140, list(range(0, 560, 4)), 16, 2, 64, 16),            # more sequences than a warp plans by itself
 ]
 
 
