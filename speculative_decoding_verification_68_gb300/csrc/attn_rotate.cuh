@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(128, POOL == POOL_E2M1 ? 8 : 7) sa_rotate_kern
     return;
   }
   // this lane's place in the rotation
-  float C[8], S[8];
+  u64 C2[4], S2[4];                               // two elements' each: rounded one by one, two at a time
   int from = lane;
   const bool turns = piece * 8 < T.rot;
   if (turns) {
@@ -187,19 +187,20 @@ __global__ void __launch_bounds__(128, POOL == POOL_E2M1 ? 8 : 7) sa_rotate_kern
     const int half = T.rot / 2;
     if (T.interleaved) {
       const float4 c = __ldg((const float4*)(row + piece * 4)), s = __ldg((const float4*)(row + half + piece * 4));
-      C[0] = C[1] = c.x; C[2] = C[3] = c.y; C[4] = C[5] = c.z; C[6] = C[7] = c.w;
-      S[1] = s.x; S[3] = s.y; S[5] = s.z; S[7] = s.w;
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) S[e] = -S[e + 1];
+      C2[0] = pk(c.x, c.x); C2[1] = pk(c.y, c.y); C2[2] = pk(c.z, c.z); C2[3] = pk(c.w, c.w);
+      S2[0] = pk(-s.x, s.x); S2[1] = pk(-s.y, s.y); S2[2] = pk(-s.z, s.z); S2[3] = pk(-s.w, s.w);
     } else {
       const bool first = piece * 8 < half;
       from = first ? lane + half / 8 : lane - half / 8;
       const float* const c = row + piece * 8 - (first ? 0 : half);
+      const float sign = first ? -1.0f : 1.0f;
 #pragma unroll
-      for (int e = 0; e < 8; e += 4) {
-        const float4 a = __ldg((const float4*)(c + e)), b = __ldg((const float4*)(c + half + e));
-        C[e] = a.x; C[e + 1] = a.y; C[e + 2] = a.z; C[e + 3] = a.w;
-        S[e] = first ? -b.x : b.x; S[e + 1] = first ? -b.y : b.y; S[e + 2] = first ? -b.z : b.z; S[e + 3] = first ? -b.w : b.w;
+      for (int e = 0; e < 2; ++e) {
+        const float4 a = __ldg((const float4*)c + e), b = __ldg((const float4*)(c + half) + e);
+        C2[2 * e] = pk(a.x, a.y);
+        C2[2 * e + 1] = pk(a.z, a.w);
+        S2[2 * e] = pk(sign * b.x, sign * b.y);
+        S2[2 * e + 1] = pk(sign * b.z, sign * b.w);
       }
     }
   }
@@ -229,8 +230,11 @@ __global__ void __launch_bounds__(128, POOL == POOL_E2M1 ? 8 : 7) sa_rotate_kern
           for (int i = 0; i < 4; ++i) {
             const float a = y[2 * i], b = y[2 * i + 1];
             const float pa = T.interleaved ? b : bf_lo(o[i]), pb = T.interleaved ? a : bf_hi(o[i]);
-            y[2 * i] = __fadd_rn(__fmul_rn(a, C[2 * i]), __fmul_rn(pa, S[2 * i]));
-            y[2 * i + 1] = __fadd_rn(__fmul_rn(b, C[2 * i + 1]), __fmul_rn(pb, S[2 * i + 1]));
+            float x0, x1, z0, z1;                 // sums one by one: a packed sum of packed products is fused
+            upk(mul2f(pk(a, b), C2[i]), x0, x1);
+            upk(mul2f(pk(pa, pb), S2[i]), z0, z1);
+            y[2 * i] = __fadd_rn(x0, z0);
+            y[2 * i + 1] = __fadd_rn(x1, z1);
             w[i] = pack_bf16(y[2 * i], y[2 * i + 1]);
           }
         }

@@ -1,5 +1,5 @@
 // The attention kernel: softmax(scale * q k^T) v on the tensor cores, over the
-// paged cache (bf16 or e4m3) or packed prompts.
+// paged cache (bf16, e4m3 or e2m1) or packed prompts.
 //
 // For a row i of scores s_ij = scale * log2(e) * q_i.k_j one pass over the keys
 // keeps a reference M_i (the running maximum), l_i = sum_j 2^(s_ij - M_i) and
@@ -26,7 +26,9 @@
 // (TMA), one issues the matrix products, two load the query rows of the next
 // run, and eight per tile do the softmax, two threads a row (a warp reaches
 // only the 32 tensor-memory lanes of its place in its warpgroup).  For an e4m3
-// cache eight more turn the codes into f16 (see below).
+// or e2m1 cache eight more turn the codes into f16 (see below); for e2m1 these
+// lay out the query rows too, two warps copy keys and values with their scales,
+// and one prefetches query rows.
 //
 // Tiles.  Two tiles of rows share a CTA's key blocks and take turns: the
 // products of one (about 1,100 cycles a block) run under the softmax of the
@@ -37,6 +39,10 @@
 //                     query and 8 key-value heads of 128, 188 us, 6.1 TB/s
 //   one tile, e4m3    shared memory and instruction issue: 64 sequences of 16 over
 //                     1000-16000, 298 us, 3.5 TB/s and 847 TFLOP/s
+//   one tile, e2m1    the softmax (about 1,800 cycles a block) and what shared memory
+//                     and issue slots the conversion takes beside it: the same over
+//                     4-bit caches, 278 us, 2.4 TB/s and 1,014 TFLOP/s.  Up to 16 rows
+//                     go to attn_few.cuh
 //   two tiles         a tile's softmax, about 1,600 cycles, where the other's
 //                     products take 1,100: 3 prompts of 4000-6450 tokens, 32 and 8
 //                     heads of 128, 687 us, 1,363 TFLOP/s
@@ -197,7 +203,6 @@ __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t* r) {
 }
 __device__ __forceinline__ float ex2(float x) { float y; asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x)); return y; }
 __device__ __forceinline__ float max3(float a, float b, float c) { float y; asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c)); return y; }
-__device__ __forceinline__ u64 add2(u64 a, u64 b) { u64 d; asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b)); return d; }
 __device__ __forceinline__ void group_sync(int id, int n) { asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ bool group_or(int id, int n, bool v) {
   uint32_t r;
@@ -286,7 +291,8 @@ struct Walker {
 };
 
 // The same by every warp for itself, of up to SHORT_SEQS sequences and 2^24 units: no barriers, and numbers of 32 bits,
-// whose divisions are short (%SHORT%).  False: not for this batch, in all warps.
+// whose divisions are short (64 sequences of 16 tokens over 4-bit caches: 287 -> 278 us, of 8 tokens 149 -> 143).  False:
+// not for this batch, in all warps.  The other caches' kernels keep the plan they were measured with.
 constexpr int SHORT_SEQS = 128;
 __device__ __forceinline__ bool plan_short(const AttnParams& A, int tile_rows, Walker& W, long long& units64, long long& ctas64) {
   const int lane = threadIdx.x & 31;

@@ -433,8 +433,11 @@ static bool two_tiles(const spec_attn_ctx* h, const AttnParams& A, long long key
   return rows > BM && units >= (long long)TWO_TILE_UNITS * h->n_sm;
 }
 
-// Rows of a tile of the kernel for few rows, 0: not for this call.  The mean number of rows of a sequence and head
-// decides, and a tile holds a group at least.
+// Rows of a tile of the kernel for few rows (attn_few.cuh), 0: not for this call.  The mean number of rows of a
+// sequence and head decides, and a tile holds a group at least.  Measured, that kernel against the other: 64 single
+// tokens over 1000-16000 (8 rows) 178 against 270 us, 2 tokens each (16 rows) 228 against 268; with tiles of 24 and 32
+// rows 93 against 70 us for 32 sequences of 3 tokens over 300-5000, 108 against 70 for 4, and in two tiles of 16 longer
+// still (32 of 4 over 500-2000: 69 against 45), but for calls of next to nothing (2 of 8 over 500-3000: 18 against 23).
 static int few_rows(const AttnParams& A) {
   const long long mean = ((long long)A.B.n_tokens * A.group + A.B.n_seqs - 1) / A.B.n_seqs, rows = mean > A.group ? mean : A.group;
   return rows > 16 ? 0 : rows <= 8 ? 8 : 16;
@@ -487,18 +490,20 @@ extern "C" int spec_attn_chunk(spec_attn_t h, const spec_attn_pool* pool, const 
   const Batch B = batch_of(h, batch, pool);
   AttnParams A = attn_params(h, B, rows_of(q), causal, scale, out, lse);
   CUtensorMap mq, mk, mv;
-  if (!map_queries(&mq, h, A)) return SV_ERR_ARG;
-  if (!map_pool(&mk, h, pool, pool->k) || !map_pool(&mv, h, pool, pool->v)) return SV_ERR_CUDA;
+  if (!map_queries(&mq, h, A)) return SV_ERR_ARG;     // whatever kernel it is, the same calls are refused
   if (pool->dtype != SV_BF16) {
     A.ks = pool->k_scale; A.vs = pool->v_scale;
-    if (pool->dtype == SV_E2M1) {
-      A.kb = pool->k_block; A.vb = pool->v_block;
-      const int few = few_rows(A);
-      if (few) return few_launch(A, pool_of(pool), h->D, few, h->n_sm, s);
-      return h->D == 128 ? launch_attention<128, KIND_E2M1, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E2M1, 1>(h, A, mq, mk, mv, s);
-    }
-    return h->D == 128 ? launch_attention<128, KIND_E4M3, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E4M3, 1>(h, A, mq, mk, mv, s);
   }
+  if (pool->dtype == SV_E2M1) {
+    A.kb = pool->k_block; A.vb = pool->v_block;
+    const int few = few_rows(A);
+    if (few) return few_launch(A, pool_of(pool), h->D, few, h->n_sm, s);
+  }
+  if (!map_pool(&mk, h, pool, pool->k) || !map_pool(&mv, h, pool, pool->v)) return SV_ERR_CUDA;
+  if (pool->dtype == SV_E2M1)
+    return h->D == 128 ? launch_attention<128, KIND_E2M1, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E2M1, 1>(h, A, mq, mk, mv, s);
+  if (pool->dtype == SV_E4M3)
+    return h->D == 128 ? launch_attention<128, KIND_E4M3, 1>(h, A, mq, mk, mv, s) : launch_attention<64, KIND_E4M3, 1>(h, A, mq, mk, mv, s);
   // The table's width is a poor bound where it has room for the longest sequence of all: a chunk of 113 tokens over
   // 6096 with 64/8 heads of 128 and a table for 131,072 takes 51 us on two tiles, 39 with max_kv given.
   const long long room = (long long)B.max_pages << B.page_shift;
