@@ -32,14 +32,14 @@
  * their negatives; bit 3 is the sign), k and v [num_pages, kv_heads, page_size,
  * head_dim / 2] bytes with element 2i in the low half of byte i; k_block and
  * v_block [num_pages, kv_heads, page_size, head_dim / 16], an e4m3 scale for
- * every 16 elements; and k_scale and v_scale as above, all 16-byte aligned.  A value is code * scale *
- * 2^(byte - 127).  The exponent e is the least one >= -120 with max|x| <= 2688 *
- * 2^e; a block's scale is max|x_j| / 2^e / 6 rounded to e4m3; a code is
- * x / 2^e / scale rounded to the nearest, ties to the even code, in 32 bits.  So
- * the largest element of a block is off by 2^-4 of itself or less and the others
- * by up to 0.18 of the largest, in blocks above 2^-13 of their vector's largest
- * element; below, scales lose bits, and a block of less than 2^-18 is 0.  A
- * vector with an infinity or NaN has NaN scales too.
+ * every 16 elements; and k_scale and v_scale as above, all 16-byte aligned.  A
+ * value is code * scale * 2^(byte - 127).  The exponent e is the least one >=
+ * -120 with max|x| <= 2688 * 2^e; a block's scale is max|x_j| / 2^e / 6 rounded
+ * to e4m3; a code is x / 2^e / scale rounded to the nearest, ties to the even
+ * code, by 32-bit quotients.  So the largest element of a block is off by 2^-4 of
+ * itself or less and the others by up to 0.18 of the largest, in blocks above
+ * 2^-13 of their vector's largest element; below, scales lose bits, and a block
+ * of less than 2^-18 is 0.  A vector with an infinity or NaN has NaN scales too.
  *
  * Precision of the attention calls.  Sums, maxima and the products' accumulators
  * are 32 bits wide; the output is rounded once, to bf16.  Inputs of the matrix
@@ -47,10 +47,10 @@
  *   - the softmax weights: to bf16 over bf16 keys and values (relative 2^-8; the
  *     sum they are divided by is corrected for the largest weight of every 64
  *     keys), or to a sum of two bf16 (2^-16) for rows of up to 1152 keys, 128
- *     where two row tiles share a CTA; to f16 over a coded pool (e4m3 or e2m1; 2^-11, and
- *     2^-25 of the row's largest contribution, or of its largest weight where
- *     the vectors share a scale: a zero vector that takes nearly all the weight
- *     leaves the others 2^-25 of their size);
+ *     where two row tiles share a CTA; to f16 over a coded pool (e4m3 or e2m1;
+ *     2^-11, and 2^-25 of the row's largest contribution, or of its largest
+ *     weight where the vectors share a scale: a zero vector that takes nearly all
+ *     the weight leaves the others 2^-25 of their size);
  *   - over a coded pool query rows to f16 (2^-11, and 2^-25 of the row's largest
  *     element).  Codes and scales are used as they are, but vectors of scale
  *     2^-112 or less may count as zero.

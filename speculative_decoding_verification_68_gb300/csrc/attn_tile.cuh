@@ -600,7 +600,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
   int* const odd_flag = (int*)(small + 640);              // whether a run has values that are not finite in such a block [4]
   float2* const info = (float2*)(small + 384);            // block references of a coded cache [INFO]
   int* const red = (int*)(small + 448);                   // planning (20 sums and 2 places of 8 bytes), then the converters' maxima (e4m3)
-  int2* const refs = (int2*)(small + 3072);               // e2m1: exponents of blocks, whether vectors have their own: of keys [INFO], values [INFO]
+  int2* const refs = (int2*)(small + 3 * 1024);               // e2m1: exponents of blocks, whether vectors have their own: of keys [INFO], values [INFO]
   Segment* const runs = (Segment*)(small + 768);          // runs as the query warps announce them [4]
   static_assert(sizeof(Segment) <= 64, "ring of runs");
   float* const swap = (float*)(small + 1024);             // [tile][half][row]: between the two threads of a row

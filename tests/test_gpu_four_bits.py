@@ -109,6 +109,33 @@ def test_quantiser_extremes(lib, d):
     assert np.array_equal(out["v"].double().cpu().numpy(), ref.double().numpy(), equal_nan=True)
 
 
+@pytest.mark.parametrize("shift", [0, -100, 100])
+def test_every_scale(lib, shift):
+    """Blocks that take each of the 126 scales above 0, with ties between codes and other values under it, by append
+    and by the append that rotates (by nothing), which quantise in different ways."""
+    g = np.random.default_rng(5)
+    scales = _attn.e4m3_value(np.arange(1, 127, dtype=np.uint8)).reshape(18, 7)
+    x = np.zeros((18, 1, 8, 16))
+    x[:, 0, 7] = 2688.0 * np.where(g.random((18, 16)) < 0.5, 1, -1)                 # makes the exponent 0
+    x[:, 0, :7, 0] = 6 * scales
+    x[:, 0, :7, 1:8] = scales[..., None] * np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    x[:, 0, :7, 8:] = scales[..., None] * g.uniform(-6, 6, (18, 7, 8))
+    x = (torch.from_numpy(x.reshape(18, 1, 128)) * 2.0 ** shift).bfloat16()
+    want = quantise4(x.double().numpy())
+    assert np.array_equal(want[1][:, 0, :7].reshape(-1), np.arange(1, 127)) and (want[2] == 127 + shift).all()
+    w = World4([18], [0], 1, 1, 128, 32)
+    attn, pool, where = setup(lib, w)
+    rope = lib.Rope(torch.cat([torch.ones((18, 64)), torch.zeros((18, 64))], 1).cuda())
+    for call in (lambda: attn.append(pool, x.cuda(), x.cuda(), *where), lambda: attn.append_rotated(pool, x.cuda(), x.cuda(), *where, rope)):
+        pool.k.view(torch.uint8).zero_(), pool.v.view(torch.uint8).zero_()
+        call()
+        assert attn.get_error() == lib.SV_OK
+        got, page = bytes_of(pool), w.table[0, 0]
+        for part, y in zip(("", "_block", "_scale"), want):
+            for name in ("k", "v"):
+                assert np.array_equal(got[name + part][page, 0, :18].numpy(), y[:, 0]), name + part
+
+
 def test_tokens_before_the_first_position(lib):
     """kv_len below the number of new tokens: the first ones have no slot."""
     w = World4([6, 5, 3], None, 4, 2, 64, 16, kv_len=[4, 0, 3], seed=3)
