@@ -224,18 +224,22 @@ __host__ __device__ constexpr uint32_t instr_desc(bool bf16, int n, bool b_mn_ma
 }
 
 // ------------------------------------------------------------------ planning
-__device__ __forceinline__ Seq load_seq(const Batch& B, int b, int tile_rows) {
+// rows a .. e-1 and a length (of no meaning for packed prompts)
+__device__ __forceinline__ Seq make_seq(const Batch& B, int a, int e, int len, int tile_rows) {
   Seq s;
-  const int a = __ldg(B.cu + b), e = __ldg(B.cu + b + 1);
   const bool range = a >= 0 && e >= a && e <= B.n_tokens;
   s.row0 = range ? a : 0;
   s.n = range ? e - a : 0;
-  s.kv = B.kv_len ? __ldg(B.kv_len + b) : s.n;
+  s.kv = B.kv_len ? len : s.n;
   s.bad = B.kv_len && !len_valid(B, s.kv);
   if (s.bad) s.kv = 0;
   s.tiles = (s.n + tile_rows - 1) / tile_rows;
   s.bad |= !range;
   return s;
+}
+__device__ __forceinline__ Seq load_seq(const Batch& B, int b, int tile_rows) {
+  const int a = __ldg(B.cu + b), e = __ldg(B.cu + b + 1);
+  return make_seq(B, a, e, B.kv_len ? __ldg(B.kv_len + b) : 0, tile_rows);
 }
 struct Segment {      // a run of blocks of one item
   int b, head;
@@ -291,21 +295,26 @@ struct Walker {
 };
 
 // The same by every warp for itself, of up to SHORT_SEQS sequences and 2^24 units: no barriers, and numbers of 32 bits,
-// whose divisions are short (64 sequences of 16 tokens over 4-bit caches: 287 -> 278 us, of 8 tokens 149 -> 143).  False:
-// not for this batch, in all warps.  The other caches' kernels keep the plan they were measured with.
+// whose divisions are short (over 4-bit caches 64 sequences of 16 tokens 287 -> 278 us, of 8 tokens 149 -> 142, 4 single
+// tokens 14.2 -> 12.1).  False: not for this batch, in all warps.  The other caches' kernels keep the plan they were
+// measured with.
 constexpr int SHORT_SEQS = 128;
 __device__ __forceinline__ bool plan_short(const AttnParams& A, int tile_rows, Walker& W, long long& units64, long long& ctas64) {
   const int lane = threadIdx.x & 31;
   if (A.B.n_seqs > SHORT_SEQS) return false;
   constexpr int CH = SHORT_SEQS / 32;
-  Seq s[CH];
+  int cu0[CH], cu1[CH], len[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {                          // all loads before their first use
+    const int b = 32 * i + lane;
+    const bool in = b < A.B.n_seqs;
+    cu0[i] = in ? __ldg(A.B.cu + b) : 0;
+    cu1[i] = in ? __ldg(A.B.cu + b + 1) : 0;
+    len[i] = in ? __ldg(A.B.kv_len + b) : 0;
+  }
   unsigned end[CH];                                       // units up to the end of the lane's sequence
   bool fits = true;
-#pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    s[i] = Seq{0, 0, 0, 0, false};
-    if (32 * i + lane < A.B.n_seqs) s[i] = load_seq(A.B, 32 * i + lane, tile_rows);
-  }
+  Seq s[CH] = {};
   unsigned units = 0;
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
@@ -313,8 +322,9 @@ __device__ __forceinline__ bool plan_short(const AttnParams& A, int tile_rows, W
       end[i] = units;
       continue;
     }
+    s[i] = make_seq(A.B, cu0[i], cu1[i], len[i], tile_rows);
     if (s[i].bad && blockIdx.x == 0) A.B.flags[0] = 1;
-    const long long mine = tiles_before(s[i], s[i].tiles, tile_rows, A.causal) * A.kv_heads;
+    const long long mine = (s[i].tiles == 1 ? SETUP + tile_blocks(s[i], 0, tile_rows, A.causal) : tiles_before(s[i], s[i].tiles, tile_rows, A.causal)) * A.kv_heads;
     fits &= mine < 1 << 17;                               // 128 of these are 2^24
     unsigned scan = (unsigned)mine;
 #pragma unroll
@@ -338,7 +348,8 @@ __device__ __forceinline__ bool plan_short(const AttnParams& A, int tile_rows, W
   for (int e = 1; e >= 0; --e) {
     to[e] = cut[e];
     if (cut[e] == units) continue;
-    // the sequence: the first whose end lies past the cut
+    // the sequence: the first whose end lies past the cut (picking it by selects in place of these branches is shorter
+    // and leaves no spills, but the main loops then run 3% slower)
     int b = -1;
     Seq q = s[0];
     unsigned begin = 0, size = 0;
@@ -359,8 +370,8 @@ __device__ __forceinline__ bool plan_short(const AttnParams& A, int tile_rows, W
       }
     }
     const unsigned per_head = size / A.kv_heads, head = (cut[e] - begin) / per_head, r = cut[e] - begin - head * per_head;
-    int t = 0, in = 0, units_of = 0;
-    for (int t0 = 0; t0 < q.tiles; t0 += 32) {            // its tile
+    int t = 0, in = (int)r, units_of = SETUP + tile_blocks(q, 0, tile_rows, A.causal);
+    for (int t0 = 0; q.tiles > 1 && t0 < q.tiles; t0 += 32) {   // its tile
       const int x = t0 + lane;
       const long long lo = x < q.tiles ? tiles_before(q, x, tile_rows, A.causal) : 0;
       const int all = x < q.tiles ? SETUP + tile_blocks(q, x, tile_rows, A.causal) : 0;
