@@ -32,6 +32,16 @@
 // another but at a run's end, where it has the next run's first slices on the way
 // already.  (Three copying warps for all, in turns: a warp waited for its slice for
 // 37% of the time, behind those that were late.)
+//
+// What bounds it, measured on GB300: 64 single tokens over 1000-16000, 64 query and
+// 8 key-value heads of 128, take 174 us, 3.7 TB/s, where copies alone took 118.
+// A slice is some 780 instructions, 128 each of them conversions of two codes and
+// products of two elements with a scale, both at half rate; an SM issues half of
+// its slots, with four warps to a quarter whose chains of products and conversions
+// do not always cover one another.  16 rows: 225 us for 2 tokens each.  Rates that
+// decided the form: f16 products of warps 1,024 multiply-adds a clock and SM, a
+// quarter of the tensor-memory ones; conversions of two codes 64 lanes a clock.
+// Small calls are a chain of latencies: 4 tokens over up to 700 take 12.1 us.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -444,27 +454,6 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
               }
               sc[x] = st[C::VB_AT + key * C::NSC + (D == 128 ? gq : gq >> 1)];
             }
-            if constexpr (NTILES == 1) {
-              // With 8 rows the tensor pipe has room: a pair of columns of one key stands where two keys of one column
-              // would, and takes part twice, against weights in the first places and zeros in the second, and the other
-              // way round.  That spares the instructions that would interleave keys.
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                const uint32_t s2 = e4m3_to_f16x2((uint16_t)(sc[2 * h] | sc[2 * h + 1] << 8)), s0 = __byte_perm(s2, s2, 0x1010), s1 = __byte_perm(s2, s2, 0x3232);
-                const uint32_t w = p[m][0][h], w00 = w & 0xffff, w01 = w >> 16, w10 = w << 16, w11 = w & 0xffff0000u;
-#pragma unroll
-                for (int y = 0; y < DV / 8; ++y) {
-                  uint32_t v[2][4];
-                  e2m1_to_f16(code[2 * h][y], s0, v[0]);
-                  e2m1_to_f16(code[2 * h + 1][y], s1, v[1]);
-#pragma unroll
-                  for (int b = 0; b < 4; b += 2) {
-                    mma_f16(o[4 * y + b][0], v[0][b], v[0][b + 1], v[1][b], v[1][b + 1], w00, w01);
-                    mma_f16(o[4 * y + b + 1][0], v[0][b], v[0][b + 1], v[1][b], v[1][b + 1], w10, w11);
-                  }
-                }
-              }
-            } else {
             const uint32_t s01 = e4m3_to_f16x2((uint16_t)(sc[0] | sc[1] << 8)), s23 = e4m3_to_f16x2((uint16_t)(sc[2] | sc[3] << 8));
 #pragma unroll
             for (int y = 0; y < DV / 8; ++y) {
@@ -478,7 +467,6 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
 #pragma unroll
                 for (int nt = 0; nt < NTILES; ++nt) mma_f16(o[4 * y + b][nt], a0, a1, a2, a3, p[m][nt][0], p[m][nt][1]);
               }
-            }
             }
             if (edge && __any_sync(FULL, nan_blocks != 0)) {
               // a product of 1 where a value is NaN and 1 where a row sees its key says where NaN belongs
@@ -569,8 +557,7 @@ __global__ void __launch_bounds__(Few<D, NTILES>::THREADS, 1) sa_few_kernel(cons
             }
             // four lanes of a row group: the same columns of rows two apart
             const int x = 4 * x4, ln = x & 31, c = (x >> 5) & 3, nt = (x >> 7) % NTILES, m = m0 + (x >> 7) / NTILES;
-            const int col = NTILES == 1 ? 4 * (m >> 1) + 2 * (c >> 1) + (m & 1) : 2 * m + (c >> 1);
-            float* const to = res + (nt * 8 + (c & 1)) * D + DV * (ln >> 2) + col;
+            float* const to = res + (nt * 8 + (c & 1)) * D + DV * (ln >> 2) + 2 * m + (c >> 1);
             to[0] = sum.x; to[2 * D] = sum.y; to[4 * D] = sum.z; to[6 * D] = sum.w;
           }
         }

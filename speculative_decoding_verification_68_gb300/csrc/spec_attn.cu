@@ -435,7 +435,7 @@ static bool two_tiles(const spec_attn_ctx* h, const AttnParams& A, long long key
 
 // Rows of a tile of the kernel for few rows (attn_few.cuh), 0: not for this call.  The mean number of rows of a
 // sequence and head decides, and a tile holds a group at least.  Measured, that kernel against the other: 64 single
-// tokens over 1000-16000 (8 rows) 178 against 270 us, 2 tokens each (16 rows) 228 against 268; with tiles of 24 and 32
+// tokens over 1000-16000 (8 rows) 174 against 271 us, 2 tokens each (16 rows) 225 against 268; with tiles of 24 and 32
 // rows 93 against 70 us for 32 sequences of 3 tokens over 300-5000, 108 against 70 for 4, and in two tiles of 16 longer
 // still (32 of 4 over 500-2000: 69 against 45), but for calls of next to nothing (2 of 8 over 500-3000: 18 against 23).
 static int few_rows(const AttnParams& A) {
