@@ -166,8 +166,6 @@ class Rope:
         if table.data_ptr() % 16:
             raise ValueError("table must be 16-byte aligned")
         self.table, self.interleaved, self.device = table, bool(interleaved), table.device
-        self._c = _CRope(table.data_ptr(), None, self.max_positions, self.rot_dim, int(self.interleaved))
-        self._ref = ctypes.byref(self._c)
 
 
 class SpecAttention:
@@ -187,7 +185,8 @@ class SpecAttention:
         self._current = (lambda: raw(index)) if raw else (lambda: torch.cuda.current_stream(self.device).cuda_stream)
         # argument blocks of the calls, refilled by each (a handle is not thread-safe)
         self._batch_c, self._q_c, self._k_c, self._v_c = _CBatch(), _CRows(), _CRows(), _CRows()
-        self._q_out_c, self._k_out_c = _CRows(), _CRows()
+        self._q_out_c, self._k_out_c, self._rope_c = _CRows(), _CRows(), _CRope()
+        self._rope_ref = ctypes.byref(self._rope_c)
         self._batch_ref, self._q_ref, self._k_ref, self._v_ref, self._q_out_ref, self._k_out_ref = (
             ctypes.byref(x) for x in (self._batch_c, self._q_c, self._k_c, self._v_c, self._q_out_c, self._k_out_c))
 
@@ -309,11 +308,11 @@ class SpecAttention:
             raise ValueError(f"rope is on {rope.device}, expected {self.device}")
         if rope.rot_dim > self.head_dim:
             raise ValueError(f"rope turns {rope.rot_dim} elements of {self.head_dim}")
-        if positions is None:
-            rope._c.positions = None
-        else:
+        if positions is not None:
             _check(positions, "positions", torch.int32, (n,), self.device)
-            rope._c.positions = positions.data_ptr()
+        c = self._rope_c                # the handle's own: handles of several threads may share a Rope
+        c.table, c.positions = rope.table.data_ptr(), None if positions is None else positions.data_ptr()
+        c.max_positions, c.rot_dim, c.interleaved = rope.max_positions, rope.rot_dim, rope.interleaved
         q_ref = q_out = k_out = None
         if q is not None:
             self._rows(self._q_c, q, "q", self.q_heads, n)
@@ -335,7 +334,7 @@ class SpecAttention:
                 k_out = self._out_rows(self._k_out_c, self._k_out_ref, out["k"], "output k", self.kv_heads, n)
             elif want_k:
                 raise ValueError("output k is required")
-        rc = self._lib.spec_attn_append_rotated(self._h, pool._ref, batch, rope._ref, q_ref, self._k_ref, self._v_ref, q_out, k_out,
+        rc = self._lib.spec_attn_append_rotated(self._h, pool._ref, batch, self._rope_ref, q_ref, self._k_ref, self._v_ref, q_out, k_out,
                                                 self._stream(stream))
         if rc:
             self._status(rc, "spec_attn_append_rotated")

@@ -73,7 +73,14 @@ __device__ __forceinline__ int find_page(const Batch& B, int t, int lane, int& s
 // A warp works on some of the vectors of one token: queries, then keys, then
 // values, 16 bytes a lane, so that a lane keeps the cosines and sines of its
 // place in the vector and finds its partner's value by a shuffle.  The first
-// vectors are loaded ahead of the search for the token's page.
+// vectors are loaded ahead of the search for the token's page, the next ones
+// ahead of the work on these.
+//
+// Bound by memory where tokens are many: 35,894 tokens of 32 query and 8 key-value
+// heads of 128 into a bf16 cache, with the rotated keys out too, take 158 us, 6.1
+// TB/s (198 with twice as many loads at a time, none ahead, and 104 registers).
+// 2,048 tokens with 64 query heads into an e4m3 cache take 18 us where memory would
+// need 11.8: a warp's chain of search, page and five loads.  Few tokens 3.3 us.
 struct Turn {
   const float* table;              // [max_positions, rot]: cosines, then sines
   const int32_t* positions;        // of the tokens; null: their places in the cache

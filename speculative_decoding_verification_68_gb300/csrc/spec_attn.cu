@@ -32,7 +32,10 @@ template <bool FP8> constexpr int piece_of = FP8 ? 16 : 8;
 // The lanes of a vector find its largest magnitude by a few shuffles.  Bound by
 // memory, 2 D bytes read and D + 1 (e4m3) or 2 D written per vector: 35,894
 // tokens of 8 heads of 128 to e4m3 take 39.1 us, 5.65 TB/s; a few tokens 2.7 us,
-// a launch and the chain of search, page, vector and store.
+// a launch and the chain of search, page, vector and store.  To e2m1 (attn_rotate.cuh
+// has the quantiser) 39.1 us too, 4.8 TB/s: bound by issue, 0.74 of the slots.  A
+// lane's 16 elements are a block of one scale; with 8 a lane, and the blocks' and
+// vectors' extremes by more shuffles, the same call took 75 us.
 template <int D, int POOL>
 __global__ void __launch_bounds__(128) sa_append_kernel(Batch B, Pool P, Rows K, Rows V, int heads) {
   constexpr int E = piece_of<POOL != POOL_BF16>, LV = D / E, NL = E / 8;
@@ -122,7 +125,8 @@ __global__ void __launch_bounds__(128) sa_append_kernel(Batch B, Pool P, Rows K,
 // The reverse of append: code * 2^e, exact in bf16 but below its normal range.
 // Bound by memory: 42,403 tokens of 8 heads of 128 from e4m3 take 45.4 us,
 // 5.75 TB/s.  A lane's 16 codes leave as one 32-byte store: as two of 16 bytes,
-// which fill half a sector each, the same call took 60 us.
+// which fill half a sector each, the same call took 60 us.  From e2m1 a lane reads
+// 8 bytes and their scale: 35,894 tokens 36.5 us, 5.2 TB/s.
 template <int D, int POOL>
 __global__ void __launch_bounds__(128) sa_read_kernel(Batch B, Pool P, __nv_bfloat16* ko, __nv_bfloat16* vo, int heads) {
   constexpr bool FP8 = POOL == POOL_E4M3;
