@@ -1584,7 +1584,7 @@ sa_attention_kernel(const __grid_constant__ AttnParams A, const __grid_constant_
         uint8_t* const dst = out0 + bs * C::BUF;
         if (ok) {
 #pragma unroll 1
-          for (int h = 0; h < D / 64; ++h) {             // 64 codes: one line of the f16 block
+          for (int h = 0; h < D / 64; ++h) {               // 64 codes: one line of the f16 block
             uint4 xs[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -268,7 +268,8 @@ static RowsOut out_rows_of(const spec_attn_rows* r) { return RowsOut{(__nv_bfloa
 static int launched() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
 
 // Vectors of a token for a warp: all of them where there are tokens enough to fill the GPU, else fewer, a step of
-// loads at least.
+// loads at least.  More warps repeat the search for the page: 2,048 tokens with 64 query heads into an e4m3 cache take
+// 18.5 us with 16 warps per SM, 21.1 with 32, 21.8 with 64.
 constexpr int WARPS_PER_SM = 16;
 template <int D, int POOL>
 static int launch_rotate(const spec_attn_ctx* h, const Batch& B, const Pool& P, const Turn& T, const Rows& Q, const Rows& K, const Rows& V,
