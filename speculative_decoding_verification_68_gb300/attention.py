@@ -348,7 +348,9 @@ class SpecAttention:
 
     def _out_rows(self, c, ref, t, name, heads, n):
         self._rows(c, t, name, heads, n)
-        if n > 1 and abs(c.token_stride) < self.head_dim or heads > 1 and abs(c.head_stride) < self.head_dim:
+        # the rows of the closer stride lie apart, and the other stride steps over all of them
+        (near, few), (far, many) = sorted(((c.token_stride if n > 1 else 0, n), (c.head_stride if heads > 1 else 0, heads)))
+        if few > 1 and near < self.head_dim or many > 1 and far < (few - 1) * near + self.head_dim:
             raise ValueError(f"{name}: strides {tuple(t.stride())} let its rows overlap")
         return ref
 
