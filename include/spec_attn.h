@@ -153,7 +153,8 @@ int spec_attn_append(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_
  * the new tokens' queries from q into q_out; where k_out is not NULL it gets the
  * rotated keys too (spec_attn_prompt takes those).  q_out and k_out are rounded
  * once, to bf16; the pool gets the 32-bit keys, rounded or quantised once.  q_out
- * may be q and k_out may be k, with the same strides; no other overlap.  rope's
+ * may be q and k_out may be k, with the same strides; no other overlap (SV_ERR_ARG
+ * where an output's own rows overlap or it begins where another tensor does).  rope's
  * positions, where given, turn the vectors, and the cache's slots stay those of
  * kv_len.  A position outside [0, max_positions) is SV_ERR_DATA: the pool skips
  * the token, and its rows of q_out and k_out are NaN, as they are where its page

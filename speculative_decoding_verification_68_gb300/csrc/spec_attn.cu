@@ -245,6 +245,20 @@ static int check_rows(const spec_attn_rows* r) {
     return SV_ERR_ARG;
   return SV_OK;
 }
+// Whether rows that a call writes lie apart: those of the closer stride do, and the other stride steps over all of them.
+static bool rows_apart(const spec_attn_rows* r, int D, int n_tokens, int heads) {
+  long long near = n_tokens > 1 ? r->token_stride : 0, far = heads > 1 ? r->head_stride : 0, few = n_tokens, many = heads;
+  if (near > far) {
+    long long x = near; near = far; far = x;
+    x = few; few = many; many = x;
+  }
+  if (few > 1 && near < D) return false;
+  return many == 1 || (far >= D && (few == 1 || (far - D) / (few - 1) >= near));
+}
+// Whether rows that a call writes are other than those it reads from, or the same ones in the same places.
+static bool apart_or_in_place(const spec_attn_rows* to, const spec_attn_rows* from, int n_tokens, int heads) {
+  return to->ptr != from->ptr || ((n_tokens == 1 || to->token_stride == from->token_stride) && (heads == 1 || to->head_stride == from->head_stride));
+}
 static int log2_of(int x) {
   int s = 0;
   while ((1 << s) < x) ++s;
@@ -323,6 +337,12 @@ extern "C" int spec_attn_append_rotated(spec_attn_t h, const spec_attn_pool* poo
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return SV_OK;
   if ((rc = check_rows(k)) || (rc = check_rows(v)) || (q && ((rc = check_rows(q)) || (rc = check_rows(q_out)))) || (k_out && (rc = check_rows(k_out))))
     return rc;
+  const int n = batch->n_tokens;
+  if (q_out && (!rows_apart(q_out, h->D, n, h->q_heads) || !apart_or_in_place(q_out, q, n, h->q_heads) || q_out->ptr == k->ptr || q_out->ptr == v->ptr))
+    return SV_ERR_ARG;
+  if (k_out && (!rows_apart(k_out, h->D, n, h->kv_heads) || !apart_or_in_place(k_out, k, n, h->kv_heads) || k_out->ptr == v->ptr ||
+                (q && (k_out->ptr == q->ptr || k_out->ptr == q_out->ptr))))
+    return SV_ERR_ARG;
   const Turn T = {rope->table, rope->positions, rope->max_positions, rope->rot_dim, rope->interleaved != 0};
   const RowsOut none = {nullptr, 0, 0};
   const Rows Q = q ? rows_of(q) : rows_of(k);
