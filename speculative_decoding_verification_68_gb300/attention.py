@@ -16,6 +16,11 @@ rejected tokens by lowering its kv_len.  Where positions rotate queries and keys
     q = attn.append_rotated(pool, k, v, cu, kv_len, page_table, rope, q=q)["q"]
 
 does both on the way into the cache.
+
+Calls run on the current stream, or on `stream` where it is given: the caller
+orders it behind what makes the inputs, and what reads the outputs behind it.
+Outputs are allocated where `out` is not given; rows of tokens that lie in no
+sequence (behind cu[-1]) are not written, so in new tensors they hold anything.
 """
 from __future__ import annotations
 
@@ -260,13 +265,29 @@ class SpecAttention:
         c.ptr, c.token_stride, c.head_stride = ptr, token, head
         return n
 
-    def _outputs(self, n, want_lse, out):
+    def _allocate(self, stream, make, *args) -> dict:
+        """make's tensors, which a call on `stream` writes: memory of that stream, so that nothing still queued on the
+        current one uses it; and where the two differ the tensors are marked as used by the current stream too, which
+        may read them after waiting for the other, so that freeing them early is safe."""
+        if stream is None or stream.cuda_stream == self._current():
+            return make(*args)
+        current = torch.cuda.current_stream(self.device)
+        with torch.cuda.stream(stream):
+            out = make(*args)
+        for t in out.values():
+            t.record_stream(current)
+        return out
+
+    def _new_outputs(self, n, want_lse):
+        device = self.device
+        out = {"out": torch.empty((n, self.q_heads, self.head_dim), dtype=torch.bfloat16, device=device)}
+        if want_lse:
+            out["lse"] = torch.empty((n, self.q_heads), dtype=torch.float32, device=device)
+        return out
+
+    def _outputs(self, n, want_lse, out, stream):
         if out is None:
-            device = self.device
-            out = {"out": torch.empty((n, self.q_heads, self.head_dim), dtype=torch.bfloat16, device=device)}
-            if want_lse:
-                out["lse"] = torch.empty((n, self.q_heads), dtype=torch.float32, device=device)
-            return out
+            return self._allocate(stream, self._new_outputs, n, want_lse)
         _check(out.get("out"), "output out", torch.bfloat16, (n, self.q_heads, self.head_dim), self.device)
         if out["out"].data_ptr() % 32:
             raise ValueError("output out must be 32-byte aligned")
@@ -318,13 +339,8 @@ class SpecAttention:
             self._rows(self._q_c, q, "q", self.q_heads, n)
             q_ref = self._q_ref
         if out is None:
-            out = {}
-            if q is not None:
-                out["q"] = self._new_rows(self._q_out_c, n, self.q_heads)
-                q_out = self._q_out_ref
-            if want_k:
-                out["k"] = self._new_rows(self._k_out_c, n, self.kv_heads)
-                k_out = self._k_out_ref
+            out = self._allocate(stream, self._new_rotated, n, q is not None, want_k)
+            q_out, k_out = self._q_out_ref if q is not None else None, self._k_out_ref if want_k else None
         else:
             if (q is None) != (out.get("q") is None):
                 raise ValueError("q and output q go together")
@@ -338,6 +354,14 @@ class SpecAttention:
                                                 self._stream(stream))
         if rc:
             self._status(rc, "spec_attn_append_rotated")
+        return out
+
+    def _new_rotated(self, n, want_q, want_k):
+        out = {}
+        if want_q:
+            out["q"] = self._new_rows(self._q_out_c, n, self.q_heads)
+        if want_k:
+            out["k"] = self._new_rows(self._k_out_c, n, self.kv_heads)
         return out
 
     def _new_rows(self, c, n, heads):
@@ -361,8 +385,7 @@ class SpecAttention:
         batch = self._batch(pool, n_tokens, cu, kv_len, page_table)
         shape = (n_tokens, self.kv_heads, self.head_dim)
         if out is None:
-            out = {"k": torch.empty(shape, dtype=torch.bfloat16, device=self.device),
-                   "v": torch.empty(shape, dtype=torch.bfloat16, device=self.device)}
+            out = self._allocate(stream, lambda: {name: torch.empty(shape, dtype=torch.bfloat16, device=self.device) for name in ("k", "v")})
         else:
             for name in ("k", "v"):
                 _check(out.get(name), f"output {name}", torch.bfloat16, shape, self.device)
@@ -386,7 +409,7 @@ class SpecAttention:
             raise ValueError(f"max_kv must be 0 or a length, not {max_kv}")
         batch = self._batch(pool, n, cu, kv_len, page_table, max_kv)
         scale = self._scale(scale)
-        out = self._outputs(n, want_lse, out)
+        out = self._outputs(n, want_lse, out, stream)
         lse = out.get("lse")
         rc = self._lib.spec_attn_chunk(self._h, pool._ref, batch, self._q_ref, int(causal), scale, out["out"].data_ptr(),
                                        None if lse is None else lse.data_ptr(), self._stream(stream))
@@ -410,7 +433,7 @@ class SpecAttention:
         if not ok:
             n_seqs = check_sequences(cu, self.device, self.max_seqs, paged=False)
         scale = self._scale(scale)
-        out = self._outputs(n, want_lse, out)
+        out = self._outputs(n, want_lse, out, stream)
         lse = out.get("lse")
         rc = self._lib.spec_attn_prompt(self._h, n_seqs, n, cu.data_ptr(), self._q_ref, self._k_ref, self._v_ref, scale,
                                         out["out"].data_ptr(), None if lse is None else lse.data_ptr(), self._stream(stream))
