@@ -160,6 +160,21 @@ class SpecVerifier:
             stream = torch.cuda.current_stream()
         return ctypes.c_void_p(stream.cuda_stream)
 
+    @staticmethod
+    def _allocate(stream, make):
+        """make()'s tensor or dict of tensors, which a call on `stream` writes: memory of that stream, so that nothing
+        still queued on the current one uses it; where the two differ they are marked as used by the current one too,
+        which may read them after waiting for the other."""
+        import torch
+        if stream is None or stream.cuda_stream == torch.cuda.current_stream().cuda_stream:
+            return make()
+        current = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            out = make()
+        for t in out.values() if isinstance(out, dict) else (out,):
+            t.record_stream(current)
+        return out
+
     def alloc_outputs(self, batch: int, want_pq: bool = True, want_tv: bool = False, device="cuda",
                       want_entropy: bool = False) -> dict:
         import torch
@@ -190,7 +205,7 @@ class SpecVerifier:
         writes the entropy of every target and draft row."""
         B = self._check_inputs(target, draft, tokens, temperature, uniforms)
         if out is None:
-            out = self.alloc_outputs(B, want_pq, want_tv, device=target.device, want_entropy=want_entropy)
+            out = self._allocate(stream, lambda: self.alloc_outputs(B, want_pq, want_tv, device=target.device, want_entropy=want_entropy))
         self._check_outputs(out, B)
         if (out.get("entropy_target") is None) != (out.get("entropy_draft") is None):
             raise ValueError("entropy_target and entropy_draft go together")
@@ -211,7 +226,7 @@ class SpecVerifier:
         rejection (tokens and tau only; no p, q or TV)."""
         B = self._check_inputs(target, draft, tokens, temperature, uniforms)
         if out is None:
-            out = self.alloc_outputs(B, want_pq=False, want_tv=False, device=target.device)
+            out = self._allocate(stream, lambda: self.alloc_outputs(B, want_pq=False, want_tv=False, device=target.device))
         self._check_outputs(out, B)
         rc = self._lib.spec_verify_lazy(self._h, B, _ptr(target), _ptr(draft), _ptr(tokens), _ptr(temperature),
                                         _ptr(uniforms), _ptr(out["tokens"]), _ptr(out["tau"]), self._stream(stream))
@@ -231,8 +246,8 @@ class SpecVerifier:
         if weights is not None:
             _check_tensor(weights, "weights", torch.float32, (B, self.k), self.device)
         if out is None:
-            out = {"loss": torch.empty((B, self.k), dtype=torch.float32, device=target.device),
-                   "grad": torch.empty_like(draft)}
+            out = self._allocate(stream, lambda: {"loss": torch.empty((B, self.k), dtype=torch.float32, device=target.device),
+                                                  "grad": torch.empty_like(draft)})
         self._check_outputs(out, B, required=("grad",))
         rc = self._lib.spec_verify_loss_grad(self._h, B, _ptr(target), _ptr(draft), _ptr(temperature), code,
                                              _ptr(weights), _ptr(out.get("loss")), _ptr(out["grad"]),
@@ -245,7 +260,7 @@ class SpecVerifier:
         import torch
         B = self._check_inputs(target, draft, None, temperature, None, sampling=False)
         if out is None:
-            out = torch.empty((B, self.k), dtype=torch.float32, device=target.device)
+            out = self._allocate(stream, lambda: torch.empty((B, self.k), dtype=torch.float32, device=target.device))
         _check_tensor(out, "out", torch.float32, (B, self.k), self.device)
         rc = self._lib.spec_verify_tv(self._h, B, _ptr(target), _ptr(draft), _ptr(temperature), _ptr(out),
                                       self._stream(stream))
