@@ -38,8 +38,9 @@
  * to e4m3; a code is x / 2^e / scale rounded to the nearest, ties to the even
  * code, by 32-bit quotients.  So the largest element of a block is off by 2^-4 of
  * itself or less and the others by up to 0.18 of the largest, in blocks above
- * 2^-13 of their vector's largest element; below, scales lose bits, and a block
- * of less than 2^-18 is 0.  A vector with an infinity or NaN has NaN scales too.
+ * 2^-123 and 2^-13 of their vector's largest element; below, scales lose bits, and
+ * a block of less than 2^-128 or 2^-19 of that element is 0 (one of 2^-18 of it
+ * may be or not).  A vector with an infinity or NaN has NaN scales too.
  *
  * Precision of the attention calls.  Sums, maxima and the products' accumulators
  * are 32 bits wide; the output is rounded once, to bf16.  Inputs of the matrix
