@@ -79,8 +79,10 @@ __device__ __forceinline__ int find_page(const Batch& B, int t, int lane, int& s
 // Bound by memory where tokens are many: 35,894 tokens of 32 query and 8 key-value
 // heads of 128 into a bf16 cache, with the rotated keys out too, take 158 us, 6.1
 // TB/s (198 with twice as many loads at a time, none ahead, and 104 registers).
-// 2,048 tokens with 64 query heads into an e4m3 cache take 18 us where memory would
-// need 11.8: a warp's chain of search, page and five loads.  Few tokens 3.3 us.
+// 35,894 tokens with 32 query heads into 4 bits take 172 us where memory would
+// need 115.  2,048 tokens with 64 query heads into an e4m3 cache take 18.4 us where
+// L2 holds the outputs' memory already and 21.2 where not (memory: 11.8): a warp's
+// chain of search, page and five loads.  Few tokens 3.3 us.
 struct Turn {
   const float* table;              // [max_positions, rot]: cosines, then sines
   const int32_t* positions;        // of the tokens; null: their places in the cache

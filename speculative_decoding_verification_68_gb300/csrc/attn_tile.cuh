@@ -297,7 +297,9 @@ struct Walker {
 // The same by every warp for itself, of up to SHORT_SEQS sequences and 2^24 units: no barriers, and numbers of 32 bits,
 // whose divisions are short (over 4-bit caches 64 sequences of 16 tokens 287 -> 278 us, of 8 tokens 149 -> 142, 4 single
 // tokens 14.2 -> 12.1).  False: not for this batch, in all warps.  The other caches' kernels keep the plan they were
-// measured with.
+// measured with.  The limit, over 100-2000: 128 sequences of 8 tokens take 118 us with this plan and 122 without, 128
+// single tokens 88 either way; with a limit of 256 and twice the loads a lane 256 of 8 take 223 instead of 221, 256
+// single tokens 149 instead of 148.
 constexpr int SHORT_SEQS = 128;
 __device__ __forceinline__ bool plan_short(const AttnParams& A, int tile_rows, Walker& W, long long& units64, long long& ctas64) {
   const int lane = threadIdx.x & 31;

@@ -283,7 +283,8 @@ static int launched() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ER
 
 // Vectors of a token for a warp: all of them where there are tokens enough to fill the GPU, else fewer, a step of
 // loads at least.  More warps repeat the search for the page: 2,048 tokens with 64 query heads into an e4m3 cache take
-// 18.5 us with 16 warps per SM, 21.1 with 32, 21.8 with 64.
+// 18.4 us with 16 warps per SM, 25.7 with 8, 20.9 with 32, 21.7 with 64, and with outputs that L2 does not hold 21.2,
+// 28.8, 23.6 and 24.0 (each within 0.1 over repeats in turn; 36K tokens have one split whatever the figure).
 constexpr int WARPS_PER_SM = 16;
 template <int D, int POOL>
 static int launch_rotate(const spec_attn_ctx* h, const Batch& B, const Pool& P, const Turn& T, const Rows& Q, const Rows& K, const Rows& V,
@@ -463,6 +464,9 @@ static bool two_tiles(const spec_attn_ctx* h, const AttnParams& A, long long key
 // tokens over 1000-16000 (8 rows) 174 against 271 us, 2 tokens each (16 rows) 225 against 268; with tiles of 24 and 32
 // rows 93 against 70 us for 32 sequences of 3 tokens over 300-5000, 108 against 70 for 4, and in two tiles of 16 longer
 // still (32 of 4 over 500-2000: 69 against 45), but for calls of next to nothing (2 of 8 over 500-3000: 18 against 23).
+// A batch gets one kernel, whatever its longest sequence: 63 single tokens over 500-8000 and a chunk of 60, 150 or 512
+// over 4000 take 149, 211 or 209 us with 32/8 heads and 202, 195 or 245 with 64/8, where two calls, one for the chunk,
+// take 164, 162 or 183 and 160, 170 or 218.
 static int few_rows(const AttnParams& A) {
   const long long mean = ((long long)A.B.n_tokens * A.group + A.B.n_seqs - 1) / A.B.n_seqs, rows = mean > A.group ? mean : A.group;
   return rows > 16 ? 0 : rows <= 8 ? 8 : 16;
