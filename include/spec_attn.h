@@ -179,7 +179,9 @@ int spec_attn_read(spec_attn_t h, const spec_attn_pool* pool, const spec_attn_ba
  * speculative decoding", section "IndexShare and KVShare").
  *   out [n_tokens, q_heads, head_dim] contiguous bf16, 32-byte aligned: sum_j softmax(scale * q.k_j) v_j
  *   lse [n_tokens, q_heads] fp32 or NULL: ln sum_j exp(scale * q.k_j)
- * A row that sees nothing gets out = 0 and lse = -inf.  scale > 0, finite.
+ * A row that sees nothing gets out = 0 and lse = -inf, and so does one whose scores
+ * are all -inf, as those of an infinite query may be; other queries that are not
+ * finite give NaN, in their own row only.  scale > 0, finite.
  * One kernel launch; single tokens and chunks of any length.  Over e2m1 a batch gets
  * one of two kernels by its mean number of new tokens: where single tokens and
  * chunks of prompts meet, a call for each is up to 1.3 times as fast. */
